@@ -21,14 +21,28 @@ Raw layer (same names and arguments as the C ABI; pointers are integers):
     sgemm_f32_variant_describe(variant, M, N, K, lda, ldb, ldc, num_cus=0) -> dict
     sgemm_f32_variant_info(variant) -> dict, planned_variants() -> [index],
     streamk_variants() -> [index]
+    gemm_i8_quantize_rows(M, K, X, x_dtype, ldx, Q, ldq, scales, stream=0)
+    gemm_i8(M, N, K, A, lda, a_scales, B, ldb, b_scales, bias, C, c_dtype, ldc,
+            workspace=0, workspace_bytes=0, stream=0)
+    gemm_i8_workspace_size(M, N, K) -> int
+    gemm_i8_plan_describe(M, N, K, num_cus=0) -> dict
+    token_logprobs_raw(...), token_logprobs_workspace_size(M, V, dtype, top) -> int,
+    token_logprobs_backward_raw(...): token_logprobs.h's arguments in their order
 Tensor layer (torch tensors on the GPU, launched on torch's current stream):
     matmul(A, B, out=None, kernel="auto", variant=-1) -> C
+    quantize_rows(X, out=None, scales=None) -> (Q, scales)
+    matmul_i8(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None) -> C
+    linear_i8(X, B, b_scales, bias=None, out_dtype=None) -> C
+    token_logprobs(logits, tokens, top=0) -> TokenLogprobs (differentiable in logits)
+    token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy=None,
+                            grad_lse=None, out=None) -> gradient of the logits
 """
 from __future__ import annotations
 
 import ctypes
 import json
 import os
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsgemm_f32.so")
@@ -102,6 +116,21 @@ def _load():
         lib.sgemm_f32_plan_describe.restype = i
         lib.sgemm_f32_variant_describe.argtypes = [i] * 8 + [ctypes.c_char_p, i]
         lib.sgemm_f32_variant_describe.restype = i
+        l, z = ctypes.c_int64, ctypes.c_size_t
+        lib.gemm_i8_quantize_rows.argtypes = [i, i, p, i, l, p, l, p, p]
+        lib.gemm_i8_quantize_rows.restype = i
+        lib.gemm_i8.argtypes = [i, i, i, p, l, p, p, l, p, p, p, i, l, p, z, p]
+        lib.gemm_i8.restype = i
+        lib.gemm_i8_workspace_size.argtypes = [i, i, i]
+        lib.gemm_i8_workspace_size.restype = z
+        lib.gemm_i8_plan_describe.argtypes = [i, i, i, i, ctypes.c_char_p, i]
+        lib.gemm_i8_plan_describe.restype = i
+        lib.token_logprobs.argtypes = [i, i, p, i, l, p, i, p, p, p, i, p, p, p, z, p]
+        lib.token_logprobs.restype = i
+        lib.token_logprobs_workspace_size.argtypes = [i, i, i, i]
+        lib.token_logprobs_workspace_size.restype = z
+        lib.token_logprobs_backward.argtypes = [i, i, p, i, l, p, i, p, p, p, p, p, p, l, p]
+        lib.token_logprobs_backward.restype = i
         lib.sgemm_f32_abi_version.argtypes = []
         lib.sgemm_f32_abi_version.restype = i
         _lib = lib
@@ -243,6 +272,52 @@ def abi_version() -> int:
     return _load().sgemm_f32_abi_version()
 
 
+def gemm_i8_quantize_rows(M, K, X, x_dtype, ldx, Q, ldq, scales, stream=0) -> None:
+    _check(_load().gemm_i8_quantize_rows(M, K, X or None, x_dtype, ldx, Q or None, ldq,
+                                         scales or None, stream or None),
+           "gemm_i8_quantize_rows")
+
+
+def gemm_i8(M, N, K, A, lda, a_scales, B, ldb, b_scales, bias, C, c_dtype, ldc, workspace=0,
+            workspace_bytes=0, stream=0) -> None:
+    _check(_load().gemm_i8(M, N, K, A or None, lda, a_scales or None, B or None, ldb,
+                           b_scales or None, bias or None, C or None, c_dtype, ldc,
+                           workspace or None, workspace_bytes, stream or None), "gemm_i8")
+
+
+def gemm_i8_workspace_size(M, N, K) -> int:
+    return _load().gemm_i8_workspace_size(M, N, K)
+
+
+def gemm_i8_plan_describe(M, N, K, num_cus=0) -> dict:
+    buf = ctypes.create_string_buffer(1024)
+    _check(_load().gemm_i8_plan_describe(M, N, K, num_cus, buf, len(buf)),
+           "gemm_i8_plan_describe")
+    return json.loads(buf.value.decode())
+
+
+def token_logprobs_raw(M, V, logits, dtype, ld, tokens, token_bytes, logprobs, entropy, lse, top=0,
+                       top_logprobs=0, top_tokens=0, workspace=0, workspace_bytes=0,
+                       stream=0) -> None:
+    _check(_load().token_logprobs(M, V, logits or None, dtype, ld, tokens or None, token_bytes,
+                                  logprobs or None, entropy or None, lse or None, top,
+                                  top_logprobs or None, top_tokens or None, workspace or None,
+                                  workspace_bytes, stream or None), "token_logprobs")
+
+
+def token_logprobs_workspace_size(M, V, dtype, top) -> int:
+    return _load().token_logprobs_workspace_size(M, V, dtype, top)
+
+
+def token_logprobs_backward_raw(M, V, logits, dtype, ld, tokens, token_bytes, lse, entropy,
+                                g_logprob, g_entropy, g_lse, grad, ldg, stream=0) -> None:
+    _check(_load().token_logprobs_backward(M, V, logits or None, dtype, ld, tokens or None,
+                                           token_bytes, lse or None, entropy or None,
+                                           g_logprob or None, g_entropy or None, g_lse or None,
+                                           grad or None, ldg, stream or None),
+           "token_logprobs_backward")
+
+
 # ------------------------------------------------------------------ tensor layer ----------
 
 def _ld(t) -> int:
@@ -305,3 +380,278 @@ def matmul(A, B, out=None, kernel: str = "auto", variant: int = -1, tile=32, pad
         else:
             raise ValueError(f"unknown kernel {kernel!r}")
     return out
+
+
+# ------------------------------------------------------- 8-bit product, token log-probabilities
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns for M rows: logprobs, entropy and lse are (M,) float32;
+    top_logprobs (M, top) float32 and top_tokens (M, top) int64, or None with top = 0."""
+    logprobs: object
+    entropy: object
+    lse: object
+    top_logprobs: object = None
+    top_tokens: object = None
+
+
+_dtype_codes = None
+
+
+def _dtype_code(dtype) -> int:
+    """The sgemm_dtype of a torch element type."""
+    global _dtype_codes
+    if _dtype_codes is None:
+        import torch
+        _dtype_codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        raise TypeError(f"expected float32, bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _on_gpu(device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors must be on the same GPU")
+
+
+def _vector(t, n: int, dtype, name: str):
+    """A tensor of n elements of dtype, made contiguous (a broadcast gradient is not)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _rows(t, name: str):
+    """A 2-D GPU tensor the kernels can read: rows of unit-stride elements that do not
+    overlap, else (a transposed or broadcast tensor) a packed copy."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
+    rows, cols = t.shape
+    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        return t.contiguous()
+    return t
+
+
+def _out(t, shape, dtype, device, name: str):
+    """A caller's output: exactly this shape and type, written in place."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    if len(shape) == 1:
+        if shape[0] > 1 and t.stride(0) != 1:
+            raise ValueError(f"{name} must be contiguous")
+    elif (shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must have rows of unit-stride elements that do not overlap")
+    return t
+
+
+def _ld_of(t) -> int:
+    rows, cols = t.shape
+    return max(t.stride(0) if rows > 1 else cols, cols, 1)
+
+
+class _Device:
+    """Makes a tensor's device current for a launch, if it is not already."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        import torch
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return torch.cuda.current_stream(self.index).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            import torch
+            torch.cuda.set_device(self.before)
+
+
+def quantize_rows(X, out=None, scales=None):
+    """(Q, scales): each row of X (M, K) as 8-bit integers with one float32 scale, so that X
+    is about Q * scales[:, None]. X is float32, bfloat16 or float16; a row is a token of
+    activations or an output channel of weights. The integers are defined to the bit
+    (gemm_i8.h). No gradient flows through it."""
+    import torch
+
+    code = _dtype_code(X.dtype)
+    X = _rows(X.detach(), "X")
+    M, K = X.shape
+    out = (torch.empty((M, K), dtype=torch.int8, device=X.device) if out is None
+           else _out(out, (M, K), torch.int8, X.device, "out"))
+    scales = (torch.empty((M,), dtype=torch.float32, device=X.device) if scales is None
+              else _out(scales, (M,), torch.float32, X.device, "scales"))
+    with _Device(X.device) as stream:
+        gemm_i8_quantize_rows(M, K, X.data_ptr(), code, _ld_of(X), out.data_ptr(), _ld_of(out),
+                              scales.data_ptr(), stream)
+    return out, scales
+
+
+def matmul_i8(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
+    """C[i, j] = (sum_k A[i, k] B[j, k]) a_scales[i] b_scales[j] + bias[j], the sum exact in
+    32-bit integers. A is (M, K) and B (N, K) int8 (a row of B is an output channel);
+    a_scales (M,), b_scales (N,) and bias (N,) float32. C is out_dtype (float32 by default,
+    bfloat16 or float16). K is at most 131071. The split form's workspace is a torch
+    allocation made here. No gradient flows through it."""
+    import torch
+
+    if A.dtype != torch.int8 or B.dtype != torch.int8:
+        raise TypeError("A and B must be int8")
+    A, B = _rows(A, "A"), _rows(B, "B")
+    M, K = A.shape
+    N, K2 = B.shape
+    if K != K2:
+        raise ValueError(f"rows of A and B differ in length: {K} vs {K2}")
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    code = _dtype_code(out_dtype)
+    dev = A.device
+    _on_gpu(dev, B, a_scales, b_scales, bias)
+    a_scales = _vector(a_scales.detach(), M, torch.float32, "a_scales")
+    b_scales = _vector(b_scales.detach(), N, torch.float32, "b_scales")
+    bias = None if bias is None else _vector(bias.detach(), N, torch.float32, "bias")
+    out = (torch.empty((M, N), dtype=out_dtype, device=dev) if out is None
+           else _out(out, (M, N), out_dtype, dev, "out"))
+    with _Device(dev) as stream:
+        ws_bytes = gemm_i8_workspace_size(M, N, K)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        gemm_i8(M, N, K, A.data_ptr(), _ld_of(A), a_scales.data_ptr(), B.data_ptr(), _ld_of(B),
+                b_scales.data_ptr(), 0 if bias is None else bias.data_ptr(), out.data_ptr(),
+                code, _ld_of(out), 0 if ws is None else ws.data_ptr(), ws_bytes, stream)
+    return out
+
+
+def linear_i8(X, B, b_scales, bias=None, out_dtype=None):
+    """quantize_rows(X), then its product with the 8-bit weights B (N, K) of scales b_scales:
+    a projection of activations X (..., K) in 8 bits. The result has X's type unless
+    out_dtype says otherwise."""
+    q, scales = quantize_rows(X.reshape(-1, X.shape[-1]))
+    C = matmul_i8(q, scales, B, b_scales, bias=bias, out_dtype=out_dtype or X.dtype)
+    return C.view(*X.shape[:-1], B.shape[0])
+
+
+def _tokens(tokens, M: int, device):
+    import torch
+
+    if tokens.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"tokens must be int64 or int32, got {tokens.dtype}")
+    _on_gpu(device, tokens)
+    return _vector(tokens, M, tokens.dtype, "tokens"), (8 if tokens.dtype == torch.int64 else 4)
+
+
+def _logprobs_forward(logits, tokens, top: int):
+    import torch
+
+    code = _dtype_code(logits.dtype)
+    logits = _rows(logits, "logits")
+    M, V = logits.shape
+    dev = logits.device
+    tokens, token_bytes = _tokens(tokens, M, dev)
+    if not 0 <= top <= 64 or (M and top > V):
+        raise ValueError(f"top must be between 0 and min(64, {V}), got {top}")
+    logprobs, entropy, lse = (torch.empty((M,), dtype=torch.float32, device=dev)
+                              for _ in range(3))
+    top_logprobs = top_tokens = None
+    if top:
+        top_logprobs = torch.empty((M, top), dtype=torch.float32, device=dev)
+        top_tokens = torch.empty((M, top), dtype=torch.int64, device=dev)
+    with _Device(dev) as stream:
+        ws_bytes = token_logprobs_workspace_size(M, V, code, top)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        token_logprobs_raw(M, V, logits.data_ptr(), code, _ld_of(logits), tokens.data_ptr(),
+                           token_bytes, logprobs.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
+                           top, top_logprobs.data_ptr() if top else 0,
+                           top_tokens.data_ptr() if top else 0,
+                           0 if ws is None else ws.data_ptr(), ws_bytes, stream)
+    return logprobs, entropy, lse, top_logprobs, top_tokens
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy=None,
+                            grad_lse=None, out=None):
+    """The gradient with respect to logits of
+    sum(grad_logprobs * logprobs + grad_entropy * entropy + grad_lse * lse), from the lse and
+    entropy that token_logprobs returned for these logits; a gradient that is None counts as
+    zeros (entropy may be None where grad_entropy is). out may be logits itself: the gradient
+    then takes its place."""
+    import torch
+
+    code = _dtype_code(logits.dtype)
+    source = logits.detach()
+    logits = _rows(source, "logits")
+    M, V = logits.shape
+    dev = logits.device
+    tokens, token_bytes = _tokens(tokens, M, dev)
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    _on_gpu(dev, lse, entropy, grad_logprobs, grad_entropy, grad_lse)
+    vectors = [None if t is None else _vector(t.detach(), M, torch.float32, name)
+               for t, name in ((lse, "lse"), (entropy, "entropy"),
+                               (grad_logprobs, "grad_logprobs"),
+                               (grad_entropy, "grad_entropy"), (grad_lse, "grad_lse"))]
+    if vectors[0] is None:
+        raise ValueError("lse is needed")
+    out = (torch.empty((M, V), dtype=logits.dtype, device=dev) if out is None
+           else _out(out, (M, V), logits.dtype, dev, "out"))
+    with _Device(dev) as stream:
+        token_logprobs_backward_raw(M, V, logits.data_ptr(), code, _ld_of(logits),
+                                    tokens.data_ptr(), token_bytes,
+                                    *(0 if t is None else t.data_ptr() for t in vectors),
+                                    out.data_ptr(), _ld_of(out), stream)
+    return out
+
+
+_autograd = None
+
+
+def _autograd_function():
+    """The autograd form of token_logprobs, made on first use (the module imports without
+    torch)."""
+    global _autograd
+    if _autograd is None:
+        import torch
+        from torch.autograd.function import once_differentiable
+
+        class TokenLogprobsFunction(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, logits, tokens, top):
+                out = _logprobs_forward(logits, tokens, top)
+                ctx.save_for_backward(logits, tokens, out[2], out[1])
+                ctx.set_materialize_grads(False)
+                if top:
+                    ctx.mark_non_differentiable(*out[3:])
+                return out
+
+            @staticmethod
+            @once_differentiable
+            def backward(ctx, g_logprobs, g_entropy, g_lse, *_):
+                if g_logprobs is None and g_entropy is None and g_lse is None:
+                    return None, None, None
+                logits, tokens, lse, entropy = ctx.saved_tensors
+                return token_logprobs_backward(logits, tokens, lse, entropy, g_logprobs,
+                                               g_entropy, g_lse), None, None
+
+        _autograd = TokenLogprobsFunction
+    return _autograd
+
+
+def token_logprobs(logits, tokens, top: int = 0) -> TokenLogprobs:
+    """Log-probabilities of one token a row under softmax(logits), with each row's entropy
+    (nats), log-sum-exp and `top` (at most 64) likeliest alternatives, in one pass over the
+    logits. logits is (M, V) float32, bfloat16 or float16; tokens (M,) int64 or int32. A
+    token below 0 marks a row without one: logprob 0 and no gradient from it; one of V or
+    more gives NaN. Alternatives of equal logits come by ascending index.
+
+    logprobs, entropy and lse carry gradients to logits where it requires them
+    (token_logprobs_backward, in one pass too); the alternatives carry none."""
+    import torch
+
+    if logits.requires_grad and torch.is_grad_enabled():
+        return TokenLogprobs(*_autograd_function().apply(logits, tokens, top))
+    return TokenLogprobs(*_logprobs_forward(logits, tokens, top))

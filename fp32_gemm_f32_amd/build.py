@@ -25,7 +25,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 # on its own, without that option.
 SOURCES = [(os.path.join(CSRC, "sgemm_f32.hip"), True),
            (os.path.join(CSRC, "sgemm_regpanel.hip"), False),
-           (os.path.join(CSRC, "sgemm_persist.hip"), False)]
+           (os.path.join(CSRC, "sgemm_persist.hip"), False),
+           (os.path.join(CSRC, "gemm_i8.hip"), True),
+           (os.path.join(CSRC, "token_logprobs.hip"), True)]
 ARCH = "gfx950"
 
 

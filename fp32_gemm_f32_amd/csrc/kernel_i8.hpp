@@ -1,0 +1,369 @@
+// kernel_i8.hpp -- kernels of the 8-bit product (gemm_i8.h): the tile kernel on
+// v_mfma_i32_32x32x32_i8, the join of its split form, and the row quantiser.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "kernel_mfma.hpp"
+#include "ops_common.hpp"
+
+namespace sgemm {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+struct I8Args {
+    const int8_t *A;
+    const int8_t *B;
+    const float *sa;
+    const float *sb;
+    const float *bias;     // or NULL
+    void *C;
+    int *partial;          // splits > 1: sums of split s at partial + s * M * N
+    int64_t lda, ldb, ldc;
+    int M, N, K;
+    int c_dtype;
+    int tiles_m, tiles_n;
+    int splits, k_chunk;   // split s covers k in [s * k_chunk, min(K, (s + 1) * k_chunk))
+};
+
+// C's value from the exact integer sum: one rounding to FP32, one each for the scales'
+// product, the scaling and the bias.
+__device__ inline float i8_value(int sum, float sa, float sb, float bias)
+{
+    return static_cast<float>(sum) * (sa * sb) + bias;
+}
+
+template <int DT, int W>
+__device__ inline void i8_store(void *C, int64_t at, const float (&v)[W], int valid)
+{
+    typedef typename Elem<DT>::type T;
+    T *c = static_cast<T *>(C) + at;
+    if (valid >= W) {
+        Pack<T, W> p;
+#pragma unroll
+        for (int j = 0; j < W; ++j) p.v[j] = Elem<DT>::narrow(v[j]);
+        store_pack(c, p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j < valid) c[j] = Elem<DT>::narrow(v[j]);
+    }
+}
+
+// ------------------------------------------------------------------ the tile kernel ----
+//
+// One workgroup computes a BM x BN tile with WGM x WGN waves of (BM / WGM) x (BN / WGN),
+// panel by panel of BK bytes of K.
+//  * A panel's rows are BK / 16 chunks of 16 bytes; chunk q of row r lies at chunk
+//    position q ^ a_swizzle(r), so the 32 rows that one ds_read_b128 of an MFMA operand
+//    reads lie on distinct banks.
+//  * MFMA operands (32x32x32): lane l supplies row l % 32 and 16 values of k, the chunk
+//    2 t + l / 32 of step t, on both sides. Accumulator register v of lane l is row
+//    8 (v / 4) + v % 4 + 4 (l / 32) and column l % 32 of the block.
+//  * A lane's CB column blocks are consecutive columns of C: LDS row 32 j + c of a wave's
+//    share of B holds global row CB c + j, so lane column c of block j is column CB c + j
+//    and one store writes CB neighbours.
+//  * DIRECT: loads go straight to LDS (buffer loads, 16 bytes a lane), NSTG panels deep;
+//    chunks past the tile's rows or past K read as zero through an offset out of range.
+//    It needs 4-byte aligned rows and K a multiple of 16. Otherwise chunks are loaded at
+//    any alignment into registers and written to LDS a panel later; the chunk that holds
+//    K's end is gathered byte by byte.
+template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_, bool DIRECT_> struct I8Tile {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, BK = BK_, NSTG = NSTG_;
+    static constexpr bool DIRECT = DIRECT_;
+    static constexpr int NT = 64 * WGM * WGN;
+    static constexpr int WM = BM / WGM, WN = BN / WGN;
+    static constexpr int RB = WM / 32, CB = WN / 32;
+    static constexpr int CPR = BK / 16;              // chunks per row
+    static constexpr int STEPS = BK / 32;            // MFMA steps per panel
+    static constexpr int ACH = BM * CPR / NT, BCH = BN * CPR / NT;   // chunks per thread
+    static constexpr int A_BYTES = BM * BK, STAGE = (BM + BN) * BK;
+    static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
+    static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
+    static_assert(DIRECT || NSTG == 2, "register-staged panels use two stages");
+    static_assert(NSTG * STAGE <= 160 * 1024, "LDS");
+};
+
+// Global row of B (within the tile) at LDS row p.
+template <typename T> __device__ inline int i8_b_row(int p)
+{
+    const int w = p / T::WN, r = p % T::WN;
+    return w * T::WN + T::CB * (r % 32) + r / 32;
+}
+
+template <typename T>
+__global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
+{
+    typedef __attribute__((address_space(3))) void *lds_ptr;
+    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * T::STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / T::WGN, wn = wave % T::WGN;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int split = blockIdx.x / tiles;
+    int tm, tn;
+    tile_coords(blockIdx.x - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    const int k0 = split * p.k_chunk, k1 = min(p.K, k0 + p.k_chunk);
+    const int panels = (k1 - k0 + T::BK - 1) / T::BK;
+    const int8_t *At = p.A + m0 * p.lda + k0;
+    const int8_t *Bt = p.B + n0 * p.ldb + k0;
+    const int kn = k1 - k0;                          // values of k in this split
+
+    // this thread's chunks: LDS chunk i * NT + tid
+    const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
+    const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
+    uint32_t a_off[T::ACH], b_off[T::BCH];
+#pragma unroll
+    for (int i = 0; i < T::ACH; ++i) {
+        const int r = prow + i * (T::NT / T::CPR);
+        a_off[i] = m0 + r < p.M ? uint32_t(r * p.lda + q * 16) : kOob;
+    }
+#pragma unroll
+    for (int i = 0; i < T::BCH; ++i) {
+        const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
+        b_off[i] = n0 + r < p.N ? uint32_t(r * p.ldb + q * 16) : kOob;
+    }
+
+    i32x16 acc[T::RB][T::CB];
+#pragma unroll
+    for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j) acc[i][j] = i32x16(0);
+
+    // operand reads: row l % 32 of a block, chunk 2 t + l / 32
+    const int frow = lane & 31, fhi = lane >> 5;
+    const int fsw = a_swizzle<T::CPR>(frow);
+    const int a_base = (wm * T::WM + frow) * T::BK;
+    const int b_base = T::A_BYTES + (wn * T::WN + frow) * T::BK;
+    auto compute = [&](const char *st) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < T::STEPS; ++t) {
+            const int at = ((2 * t + fhi) ^ fsw) * 16;
+            i32x4 a[T::RB], b[T::CB];
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i)
+                a[i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
+#pragma unroll
+            for (int j = 0; j < T::CB; ++j)
+                b[j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+                for (int j = 0; j < T::CB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j],
+                                                                      0, 0, 0);
+        }
+    };
+
+    if constexpr (T::DIRECT) {
+        const auto rsa = make_rsrc32(reinterpret_cast<const float *>(At), kFullRange);
+        const auto rsb = make_rsrc32(reinterpret_cast<const float *>(Bt), kFullRange);
+        auto issue = [&](int panel) __attribute__((always_inline)) {
+            char *st = smem + (panel % T::NSTG) * T::STAGE;
+            const int k = panel * T::BK;
+            // the range's last panel, or one past it: chunks past its end read as zero
+            const bool tail = k + T::BK > kn, out = k + q * 16 >= kn;
+#pragma unroll
+            for (int i = 0; i < T::ACH; ++i) {
+                const uint32_t off = tail && out ? kOob : a_off[i];
+                char *to = st + (i * T::NT + wave * 64) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_ptr)to, 16, off, k, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < T::BCH; ++i) {
+                const uint32_t off = tail && out ? kOob : b_off[i];
+                char *to = st + T::A_BYTES + (i * T::NT + wave * 64) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_ptr)to, 16, off, k, 0, 0);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < T::NSTG - 1; ++i) issue(i);
+        for (int panel = 0; panel < panels; ++panel) {
+            // this wave's loads of the panel have landed; the barrier says so of every
+            // wave's, and that every wave has read the stage that is loaded next
+            wait_vmcnt<(T::NSTG - 2) * (T::ACH + T::BCH)>();
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            issue(panel + T::NSTG - 1);
+            compute(smem + (panel % T::NSTG) * T::STAGE);
+        }
+        wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
+    } else {
+        i32x4 ra[T::ACH], rb[T::BCH];
+        auto fetch = [&](const int8_t *base, uint32_t off, int k) __attribute__((always_inline)) {
+            i32x4 v = i32x4(0);
+            const int left = kn - (k + q * 16);
+            if (off != kOob && left > 0) {
+                const int8_t *src = base + off + k;
+                if (left >= 16) {
+                    const Pack<int, 4> w = load_pack<int, 4>(reinterpret_cast<const int *>(src));
+                    v = i32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
+                } else {
+                    for (int e = 0; e < 16; ++e) {
+                        const unsigned b = e < left ? uint8_t(src[e]) : 0u;
+                        const unsigned s = b << (8 * (e & 3));
+                        v[0] |= (e >> 2) == 0 ? s : 0u;
+                        v[1] |= (e >> 2) == 1 ? s : 0u;
+                        v[2] |= (e >> 2) == 2 ? s : 0u;
+                        v[3] |= (e >> 2) == 3 ? s : 0u;
+                    }
+                }
+            }
+            return v;
+        };
+        auto load = [&](int panel) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < T::ACH; ++i) ra[i] = fetch(At, a_off[i], panel * T::BK);
+#pragma unroll
+            for (int i = 0; i < T::BCH; ++i) rb[i] = fetch(Bt, b_off[i], panel * T::BK);
+        };
+        load(0);
+        for (int panel = 0; panel < panels; ++panel) {
+            char *st = smem + (panel & 1) * T::STAGE;
+#pragma unroll
+            for (int i = 0; i < T::ACH; ++i)
+                *reinterpret_cast<i32x4 *>(st + (i * T::NT + tid) * 16) = ra[i];
+#pragma unroll
+            for (int i = 0; i < T::BCH; ++i)
+                *reinterpret_cast<i32x4 *>(st + T::A_BYTES + (i * T::NT + tid) * 16) = rb[i];
+            // one barrier a panel: a wave writes a stage again only after the barrier that
+            // follows every wave's reads of it
+            __syncthreads();
+            if (panel + 1 < panels) load(panel + 1);
+            compute(st);
+        }
+    }
+
+    // epilogue: this lane's rows 8 (v / 4) + v % 4 + 4 fhi of each row block, columns
+    // CB (l % 32) + 0 .. CB - 1 of the wave's share
+    const int col = n0 + wn * T::WN + T::CB * frow;
+    const int valid = p.N - col;
+    const int row0 = m0 + wm * T::WM + 4 * fhi;
+    if (valid <= 0) return;
+    if (p.splits > 1) {
+        int *out = p.partial + int64_t(split) * p.M * p.N;
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
+                if (m < p.M)
+#pragma unroll
+                    for (int j = 0; j < T::CB; ++j)
+                        if (j < valid) out[int64_t(m) * p.N + col + j] = acc[i][j][v];
+            }
+        return;
+    }
+    float sb[T::CB], bias[T::CB];
+#pragma unroll
+    for (int j = 0; j < T::CB; ++j) {
+        const int n = min(col + j, p.N - 1);
+        sb[j] = p.sb[n];
+        bias[j] = p.bias ? p.bias[n] : 0.0f;
+    }
+    auto store_all = [&](auto dt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
+                if (m < p.M) {
+                    const float sa = p.sa[m];
+                    float x[T::CB];
+#pragma unroll
+                    for (int j = 0; j < T::CB; ++j) x[j] = i8_value(acc[i][j][v], sa, sb[j], bias[j]);
+                    i8_store<decltype(dt)::value, T::CB>(p.C, m * p.ldc + col, x, valid);
+                }
+            }
+    };
+    if (p.c_dtype == SGEMM_DTYPE_BF16) store_all(std::integral_constant<int, SGEMM_DTYPE_BF16>{});
+    else if (p.c_dtype == SGEMM_DTYPE_F16) store_all(std::integral_constant<int, SGEMM_DTYPE_F16>{});
+    else store_all(std::integral_constant<int, SGEMM_DTYPE_F32>{});
+}
+
+// ------------------------------------------------------------------ the split's join ----
+// Adds the splits' integer sums (exact in any order) and applies the epilogue; one thread
+// per element of C, strided over the grid. Bound by reading splits * M * N integers, which
+// the plan keeps small (it splits products with few tiles).
+__global__ __launch_bounds__(256) void k_gemm_i8_join(I8Args p)
+{
+    const int64_t total = int64_t(p.M) * p.N;
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < total;
+         e += int64_t(gridDim.x) * 256) {
+        const int64_t m = e / p.N;
+        const int n = int(e - m * p.N);
+        int sum = 0;
+        for (int s = 0; s < p.splits; ++s) sum += p.partial[s * total + e];
+        const float x[1] = {i8_value(sum, p.sa[m], p.sb[n], p.bias ? p.bias[n] : 0.0f)};
+        if (p.c_dtype == SGEMM_DTYPE_BF16) i8_store<SGEMM_DTYPE_BF16, 1>(p.C, m * p.ldc + n, x, 1);
+        else if (p.c_dtype == SGEMM_DTYPE_F16) i8_store<SGEMM_DTYPE_F16, 1>(p.C, m * p.ldc + n, x, 1);
+        else i8_store<SGEMM_DTYPE_F32, 1>(p.C, m * p.ldc + n, x, 1);
+    }
+}
+
+// K == 0: the empty sum plus the bias.
+__global__ __launch_bounds__(256) void k_gemm_i8_empty(I8Args p)
+{
+    const int64_t total = int64_t(p.M) * p.N;
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < total;
+         e += int64_t(gridDim.x) * 256) {
+        const int64_t m = e / p.N;
+        const int n = int(e - m * p.N);
+        const float x[1] = {p.bias ? p.bias[n] : 0.0f};
+        if (p.c_dtype == SGEMM_DTYPE_BF16) i8_store<SGEMM_DTYPE_BF16, 1>(p.C, m * p.ldc + n, x, 1);
+        else if (p.c_dtype == SGEMM_DTYPE_F16) i8_store<SGEMM_DTYPE_F16, 1>(p.C, m * p.ldc + n, x, 1);
+        else i8_store<SGEMM_DTYPE_F32, 1>(p.C, m * p.ldc + n, x, 1);
+    }
+}
+
+// ------------------------------------------------------------------ the row quantiser ---
+// The integer of x under `inverse` = 127 / peak: rint rounds ties to even; what is not a
+// number (inf * 0, NaN) becomes 0.
+__device__ inline int quantize_one(float x, float inverse)
+{
+    const float y = __builtin_rintf(x * inverse);
+    return y == y ? static_cast<int>(__builtin_fminf(__builtin_fmaxf(y, -127.0f), 127.0f)) : 0;
+}
+
+// The scale and the inverse from the row's peak. The division is IEEE's; 127 / peak
+// overflows for peaks below 3.8e-37 (0 included), and such a row becomes zeros.
+__device__ inline void row_scale(float peak, float &scale, float &inverse)
+{
+    scale = peak / 127.0f;
+    inverse = 127.0f / peak;
+    if (__builtin_isinf(inverse)) { scale = 0.0f; inverse = 0.0f; }
+}
+
+// max that keeps a NaN, for absolute values: as unsigned integers their bits are in order,
+// with the NaNs above infinity
+__device__ inline uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+
+// One workgroup per row: the peak, then the integers from a second read of the row (which
+// the cache still holds).
+template <int DT>
+__global__ __launch_bounds__(256) void k_quantize_rows(int M, int K, const void *X, int64_t ldx,
+                                                       int8_t *Q, int64_t ldq, float *scales)
+{
+    typedef typename Elem<DT>::type T;
+    __shared__ uint32_t peaks[4];
+    const int tid = threadIdx.x;
+    const int64_t row = blockIdx.x;
+    const T *x = static_cast<const T *>(X) + row * ldx;
+    uint32_t peak = 0;
+    for (int64_t k = tid; k < K; k += 256) peak = max(peak, abs_bits(Elem<DT>::widen(x[k])));
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) peak = max(peak, uint32_t(__shfl_xor(int(peak), d)));
+    if ((tid & 63) == 0) peaks[tid >> 6] = peak;
+    __syncthreads();
+    peak = max(max(peaks[0], peaks[1]), max(peaks[2], peaks[3]));
+    float scale, inverse;
+    row_scale(__builtin_bit_cast(float, peak), scale, inverse);
+    for (int64_t k = tid; k < K; k += 256)
+        Q[row * ldq + k] = int8_t(quantize_one(Elem<DT>::widen(x[k]), inverse));
+    if (tid == 0) scales[row] = scale;
+}
+
+}  // namespace sgemm

@@ -1,0 +1,165 @@
+// token_logprobs.hip -- the C ABI declared in include/token_logprobs.h: validation (pure
+// host code), how rows are split over workgroups, the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "kernel_logprobs.hpp"
+#include "ops_common.hpp"
+#include "token_logprobs.h"
+
+namespace sgemm {
+namespace {
+
+constexpr int kMaxTop = TOKEN_LOGPROBS_MAX_TOP;
+static_assert(kMaxTop == 64, "a wave's list holds one key per lane");
+constexpr int64_t kMaxGroups = int64_t(1) << 30;
+
+int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
+
+struct RowSplit {
+    int splits, part_len;
+    int64_t part_bytes;
+};
+
+// How many workgroups share a row: one where the rows alone give every compute unit two
+// workgroups, else as many as bring it there, each with at least kLeastPart elements.
+constexpr int kLeastPart = 4096;
+RowSplit split_rows(int M, int V, int top, int cus)
+{
+    RowSplit r{1, V, 0};
+    const int want = std::min(ceil_div(2 * cus, M), ceil_div(V, kLeastPart));
+    if (M < 2 * cus && want > 1) {
+        r.part_len = (ceil_div(V, want) + 7) / 8 * 8;
+        r.splits = ceil_div(V, r.part_len);
+    }
+    if (r.splits > 1) r.part_bytes = sizeof(RowPart) + int64_t((top + 1) / 2 * 2) * 8;
+    return r;
+}
+size_t split_bytes(const RowSplit &r, int M)
+{
+    return r.splits > 1 ? size_t(M) * r.splits * r.part_bytes : 0;
+}
+
+typedef void (*RowKernel)(RowArgs);
+template <int DT> RowKernel pass_kernel(bool top)
+{
+    return top ? &k_row_pass<DT, true> : &k_row_pass<DT, false>;
+}
+template <int DT> RowKernel join_kernel(bool top)
+{
+    return top ? &k_row_join<DT, true> : &k_row_join<DT, false>;
+}
+
+}  // namespace
+}  // namespace sgemm
+
+using namespace sgemm;
+
+extern "C" size_t token_logprobs_workspace_size(int M, int V, int dtype, int top)
+{
+    if (M <= 0 || V <= 0 || !known_dtype(dtype) || top < 0 || top > kMaxTop || top > V) return 0;
+    int cus = 0;
+    if (device_cus(&cus) != SGEMM_OK) return 0;
+    return split_bytes(split_rows(M, V, top, cus), M);
+}
+
+extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64_t ld,
+                              const void *tokens, int token_bytes, float *logprobs,
+                              float *entropy, float *lse, int top, float *top_logprobs,
+                              int64_t *top_tokens, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    if (M < 0 || V < 0 || (M > 0 && V == 0)) return SGEMM_EINVAL_DIM;
+    if (ld < std::max(V, 1)) return SGEMM_EINVAL_LD;
+    if (!known_dtype(dtype) || (token_bytes != 4 && token_bytes != 8) || top < 0 ||
+        top > kMaxTop || (M > 0 && top > V))
+        return SGEMM_EINVAL_ARG;
+    if (M == 0) return SGEMM_OK;
+    const int size = dtype_bytes(dtype);
+    const Region x = region(logits, M, V, ld, size), t = region(tokens, 1, M, M, token_bytes),
+                 w = {workspace, workspace_bytes};
+    const Region out[] = {region(logprobs, 1, M, M, 4),
+                          region(entropy, 1, entropy ? M : 0, M, 4),
+                          region(lse, 1, lse ? M : 0, M, 4),
+                          region(top_logprobs, M, top, top, 4),
+                          region(top_tokens, M, top, top, 8)};
+    if (bad_region(x, size) || bad_region(t, token_bytes) || bad_region(out[0], 4) ||
+        bad_region(out[1], 4) || bad_region(out[2], 4) || bad_region(out[3], 4) ||
+        bad_region(out[4], 8) || bad_region(w, 16))
+        return SGEMM_EINVAL_PTR;
+    for (int i = 0; i < 5; ++i) {
+        if (overlaps(out[i], x) || overlaps(out[i], t) || overlaps(out[i], w)) return SGEMM_EALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i], out[j])) return SGEMM_EALIAS;
+    }
+    if (overlaps(w, x) || overlaps(w, t)) return SGEMM_EALIAS;
+
+    int cus = 0;
+    int st = device_cus(&cus);
+    if (st != SGEMM_OK) return st;
+    RowSplit r = split_rows(M, V, top, cus);
+    const size_t need = split_bytes(r, M);
+    if (need > 0) {
+        if (workspace_bytes == 0) r = RowSplit{1, V, 0};
+        else if (workspace_bytes < need) return SGEMM_EINVAL_ARG;
+    }
+    if (int64_t(M) * r.splits > kMaxGroups) return SGEMM_ETOO_LARGE;
+    RowArgs p{};
+    p.logits = logits; p.ld = ld; p.tokens = tokens; p.token_bytes = token_bytes;
+    p.logprobs = logprobs; p.entropy = entropy; p.lse = lse;
+    p.top_logprobs = top_logprobs; p.top_tokens = top_tokens;
+    p.parts = static_cast<char *>(workspace); p.part_bytes = r.part_bytes;
+    p.M = M; p.V = V; p.top = top; p.splits = r.splits; p.part_len = r.part_len;
+    RowKernel pass, join;
+    if (dtype == SGEMM_DTYPE_F32) {
+        pass = pass_kernel<SGEMM_DTYPE_F32>(top > 0); join = join_kernel<SGEMM_DTYPE_F32>(top > 0);
+    } else if (dtype == SGEMM_DTYPE_BF16) {
+        pass = pass_kernel<SGEMM_DTYPE_BF16>(top > 0); join = join_kernel<SGEMM_DTYPE_BF16>(top > 0);
+    } else {
+        pass = pass_kernel<SGEMM_DTYPE_F16>(top > 0); join = join_kernel<SGEMM_DTYPE_F16>(top > 0);
+    }
+    st = launch(pass, dim3(unsigned(M * int64_t(r.splits))), dim3(kRowThreads), stream, p);
+    if (st != SGEMM_OK || r.splits == 1) return st;
+    return launch(join, dim3(unsigned(M)), dim3(kRowThreads), stream, p);
+}
+
+extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dtype, int64_t ld,
+                                       const void *tokens, int token_bytes, const float *lse,
+                                       const float *entropy, const float *g_logprob,
+                                       const float *g_entropy, const float *g_lse, void *grad,
+                                       int64_t ldg, void *stream)
+{
+    if (M < 0 || V < 0 || (M > 0 && V == 0)) return SGEMM_EINVAL_DIM;
+    if (ld < std::max(V, 1) || ldg < std::max(V, 1)) return SGEMM_EINVAL_LD;
+    if (!known_dtype(dtype) || (token_bytes != 4 && token_bytes != 8)) return SGEMM_EINVAL_ARG;
+    if (M == 0) return SGEMM_OK;
+    const int size = dtype_bytes(dtype);
+    const Region x = region(logits, M, V, ld, size), d = region(grad, M, V, ldg, size);
+    const Region in[] = {region(tokens, 1, M, M, token_bytes),
+                         region(lse, 1, M, M, 4),
+                         region(entropy, 1, g_entropy ? M : 0, M, 4),
+                         region(g_logprob, 1, g_logprob ? M : 0, M, 4),
+                         region(g_entropy, 1, g_entropy ? M : 0, M, 4),
+                         region(g_lse, 1, g_lse ? M : 0, M, 4)};
+    if (bad_region(x, size) || bad_region(d, size)) return SGEMM_EINVAL_PTR;
+    for (int i = 0; i < 6; ++i)
+        if (bad_region(in[i], i == 0 ? token_bytes : 4)) return SGEMM_EINVAL_PTR;
+    const bool in_place = grad == logits && ldg == ld;
+    if (!in_place && overlaps(d, x)) return SGEMM_EALIAS;
+    for (const Region &r : in)
+        if (overlaps(d, r)) return SGEMM_EALIAS;
+
+    GradArgs p{};
+    p.logits = logits; p.grad = grad; p.tokens = tokens; p.token_bytes = token_bytes;
+    p.lse = lse; p.entropy = entropy; p.g_logprob = g_logprob; p.g_entropy = g_entropy;
+    p.g_lse = g_lse; p.ld = ld; p.ldg = ldg; p.M = M; p.V = V;
+    p.part_len = 16384 / size;
+    p.parts = ceil_div(V, p.part_len);
+    if (int64_t(M) * p.parts > kMaxGroups) return SGEMM_ETOO_LARGE;
+    auto kern = dtype == SGEMM_DTYPE_F32    ? &k_row_gradient<SGEMM_DTYPE_F32>
+                : dtype == SGEMM_DTYPE_BF16 ? &k_row_gradient<SGEMM_DTYPE_BF16>
+                                            : &k_row_gradient<SGEMM_DTYPE_F16>;
+    return launch(kern, dim3(unsigned(M * int64_t(p.parts))), dim3(kRowThreads), stream, p);
+}
