@@ -75,6 +75,26 @@ unsigned element_blocks(int64_t total)
     return unsigned(std::min<int64_t>((total + 255) / 256, 16384));
 }
 
+// The smallest form whose registers hold a row: a wave to a row for short ones, the
+// workgroup for longer ones.
+template <int DT>
+int quantize(int M, int K, const void *X, int64_t ldx, int8_t *Q, int64_t ldq, float *scales,
+             void *stream)
+{
+    constexpr int W = 16 / (DT == SGEMM_DTYPE_F32 ? 4 : 2);
+    const auto run = [&](auto kern, int rows_per_group) {
+        return launch(kern, dim3(unsigned(ceil_div(M, rows_per_group))), dim3(256), stream, M, K, X,
+                      ldx, Q, ldq, scales);
+    };
+    if (K <= 64 * W) return run(&k_quantize_rows<DT, 1, 1>, 4);
+    if (K <= 256 * W) return run(&k_quantize_rows<DT, 4, 1>, 4);
+    if (K <= 512 * W) return run(&k_quantize_rows<DT, 2, 4>, 1);
+    if (K <= 1024 * W) return run(&k_quantize_rows<DT, 4, 4>, 1);
+    if (K <= 2048 * W) return run(&k_quantize_rows<DT, 8, 4>, 1);
+    return launch(&k_quantize_long_rows<DT>, dim3(unsigned(M)), dim3(1024), stream, K, X, ldx, Q,
+                  ldq, scales);
+}
+
 }  // namespace
 }  // namespace sgemm
 
@@ -92,10 +112,9 @@ extern "C" int gemm_i8_quantize_rows(int M, int K, const void *X, int x_dtype, i
         return SGEMM_EINVAL_PTR;
     if (overlaps(q, x) || overlaps(s, x) || overlaps(s, q)) return SGEMM_EALIAS;
     if (M == 0) return SGEMM_OK;
-    auto kern = x_dtype == SGEMM_DTYPE_F32    ? &k_quantize_rows<SGEMM_DTYPE_F32>
-                : x_dtype == SGEMM_DTYPE_BF16 ? &k_quantize_rows<SGEMM_DTYPE_BF16>
-                                              : &k_quantize_rows<SGEMM_DTYPE_F16>;
-    return launch(kern, dim3(unsigned(M)), dim3(256), stream, M, K, X, ldx, Q, ldq, scales);
+    if (x_dtype == SGEMM_DTYPE_F32) return quantize<SGEMM_DTYPE_F32>(M, K, X, ldx, Q, ldq, scales, stream);
+    if (x_dtype == SGEMM_DTYPE_BF16) return quantize<SGEMM_DTYPE_BF16>(M, K, X, ldx, Q, ldq, scales, stream);
+    return quantize<SGEMM_DTYPE_F16>(M, K, X, ldx, Q, ldq, scales, stream);
 }
 
 extern "C" size_t gemm_i8_workspace_size(int M, int N, int K)

@@ -84,6 +84,7 @@ template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_, bool DIRECT_
     static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
     static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
     static_assert(DIRECT || NSTG == 2, "register-staged panels use two stages");
+    static_assert(STEPS % 2 == 0, "operand buffers alternate over whole panels");
     static_assert(NSTG * STAGE <= 160 * 1024, "LDS");
 };
 
@@ -139,24 +140,23 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     const int fsw = a_swizzle<T::CPR>(frow);
     const int a_base = (wm * T::WM + frow) * T::BK;
     const int b_base = T::A_BYTES + (wn * T::WN + frow) * T::BK;
-    auto compute = [&](const char *st) __attribute__((always_inline)) {
+    i32x4 fa[2][T::RB], fb[2][T::CB];
+    auto read = [&](const char *st, int t, int buf) __attribute__((always_inline)) {
+        const int at = ((2 * t + fhi) ^ fsw) * 16;
 #pragma unroll
-        for (int t = 0; t < T::STEPS; ++t) {
-            const int at = ((2 * t + fhi) ^ fsw) * 16;
-            i32x4 a[T::RB], b[T::CB];
+        for (int i = 0; i < T::RB; ++i)
+            fa[buf][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
 #pragma unroll
-            for (int i = 0; i < T::RB; ++i)
-                a[i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
+        for (int j = 0; j < T::CB; ++j)
+            fb[buf][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
+    };
+    auto multiply = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
 #pragma unroll
             for (int j = 0; j < T::CB; ++j)
-                b[j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
-#pragma unroll
-            for (int i = 0; i < T::RB; ++i)
-#pragma unroll
-                for (int j = 0; j < T::CB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j],
-                                                                      0, 0, 0);
-        }
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[buf][i], fb[buf][j],
+                                                                  acc[i][j], 0, 0, 0);
     };
 
     if constexpr (T::DIRECT) {
@@ -165,30 +165,62 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
         auto issue = [&](int panel) __attribute__((always_inline)) {
             char *st = smem + (panel % T::NSTG) * T::STAGE;
             const int k = panel * T::BK;
-            // the range's last panel, or one past it: chunks past its end read as zero
-            const bool tail = k + T::BK > kn, out = k + q * 16 >= kn;
+            // in the range's last panel, and one past it, chunks past its end read as zero
+            const uint32_t past = k + q * 16 >= kn ? kOob : 0u;
 #pragma unroll
             for (int i = 0; i < T::ACH; ++i) {
-                const uint32_t off = tail && out ? kOob : a_off[i];
+                const uint32_t off = a_off[i] | past;
                 char *to = st + (i * T::NT + wave * 64) * 16;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_ptr)to, 16, off, k, 0, 0);
             }
 #pragma unroll
             for (int i = 0; i < T::BCH; ++i) {
-                const uint32_t off = tail && out ? kOob : b_off[i];
+                const uint32_t off = b_off[i] | past;
                 char *to = st + T::A_BYTES + (i * T::NT + wave * 64) * 16;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_ptr)to, 16, off, k, 0, 0);
             }
         };
+        // The step before a panel's last ends the reads of its stage, so the barrier comes
+        // there: the wave's loads of the next panel have landed, every wave's have after the
+        // barrier, and the stage just read is loaded again and the next one's first operands
+        // are read under the last step's MFMAs.
+        constexpr int LPP = T::ACH + T::BCH;
 #pragma unroll
-        for (int i = 0; i < T::NSTG - 1; ++i) issue(i);
+        for (int i = 0; i < T::NSTG; ++i) issue(i);
+        wait_vmcnt<(T::NSTG - 1) * LPP>();
+        asm volatile("s_barrier" ::: "memory");
+        read(smem, 0, 0);
+        int stage = 0;
         for (int panel = 0; panel < panels; ++panel) {
-            // this wave's loads of the panel have landed; the barrier says so of every
-            // wave's, and that every wave has read the stage that is loaded next
-            wait_vmcnt<(T::NSTG - 2) * (T::ACH + T::BCH)>();
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            issue(panel + T::NSTG - 1);
-            compute(smem + (panel % T::NSTG) * T::STAGE);
+            const char *st = smem + stage * T::STAGE;
+            stage = stage + 1 == T::NSTG ? 0 : stage + 1;
+            static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
+                constexpr int t = decltype(tc)::value;
+                constexpr bool last = t == T::STEPS - 1;
+                if constexpr (!last) {
+                    read(st, t + 1, (t + 1) & 1);
+                } else {
+                    __builtin_amdgcn_sched_barrier(0);
+                    wait_vmcnt<(T::NSTG - 2) * LPP>();
+                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    read(smem + stage * T::STAGE, 0, (t + 1) & 1);
+                    issue(panel + T::NSTG);
+                }
+                multiply(t & 1);
+                // operand reads behind the first MFMAs, the loads behind the others
+                constexpr int ops = T::RB + T::CB, mf = T::RB * T::CB;
+                constexpr int rm = last ? (mf + 1) / 2 : (ops < mf ? ops : mf);
+                constexpr int lm = mf - rm > 0 ? mf - rm : 1;
+                static_for<0, mf>([&](auto mc) __attribute__((always_inline)) {
+                    constexpr int m = decltype(mc)::value;
+                    constexpr int r = m < rm ? (m + 1) * ops / rm - m * ops / rm : 0;
+                    constexpr int n = m - (mf - lm);
+                    constexpr int l = last && n >= 0 ? (n + 1) * LPP / lm - n * LPP / lm : 0;
+                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, r, 0);
+                    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
+                });
+            });
         }
         wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
     } else {
@@ -233,7 +265,12 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
             // follows every wave's reads of it
             __syncthreads();
             if (panel + 1 < panels) load(panel + 1);
-            compute(st);
+            read(st, 0, 0);
+#pragma unroll
+            for (int t = 0; t < T::STEPS; ++t) {
+                if (t + 1 < T::STEPS) read(st, t + 1, (t + 1) & 1);
+                multiply(t & 1);
+            }
         }
     }
 
@@ -341,28 +378,106 @@ __device__ inline void row_scale(float peak, float &scale, float &inverse)
 // with the NaNs above infinity
 __device__ inline uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
 
-// One workgroup per row: the peak, then the integers from a second read of the row (which
-// the cache still holds).
-template <int DT>
+// WPR waves share a row, CH chunks of 16 bytes to a thread: the row is read once, into
+// registers, and the peak taken over lanes and then (WPR > 1) over the waves in LDS.
+// HBM-bound: M K (2 or 4) bytes in and M K out. Rows of odd length or address use the same
+// loads (one instruction serves any alignment); the chunk that holds the row's end is
+// filled element by element.
+template <int DT, int CH, int WPR>
 __global__ __launch_bounds__(256) void k_quantize_rows(int M, int K, const void *X, int64_t ldx,
                                                        int8_t *Q, int64_t ldq, float *scales)
 {
     typedef typename Elem<DT>::type T;
+    constexpr int W = 16 / sizeof(T), STEP = 64 * WPR;
     __shared__ uint32_t peaks[4];
+    const int tid = threadIdx.x;
+    const int in_row = tid % STEP;
+    const int64_t row = int64_t(blockIdx.x) * (4 / WPR) + tid / STEP;
+    if (WPR == 1 && row >= M) return;          // whole waves; no barrier follows
+    const T *x = static_cast<const T *>(X) + row * ldx;
+    Pack<T, W> c[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int k = (in_row + i * STEP) * W;
+        if (k + W <= K) {
+            c[i] = load_pack<T, W>(x + k);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j) c[i].v[j] = k + j < K ? x[k + j] : T(0.0f);
+        }
+    }
+    uint32_t peak = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int j = 0; j < W; ++j) peak = max(peak, abs_bits(Elem<DT>::widen(c[i].v[j])));
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) peak = max(peak, uint32_t(__shfl_xor(int(peak), d)));
+    if constexpr (WPR > 1) {
+        if ((tid & 63) == 0) peaks[tid >> 6] = peak;
+        __syncthreads();
+        peak = max(max(peaks[0], peaks[1]), max(peaks[2], peaks[3]));
+    }
+    float scale, inverse;
+    row_scale(__builtin_bit_cast(float, peak), scale, inverse);
+    int8_t *q = Q + row * ldq;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        const int k = (in_row + i * STEP) * W;
+        Pack<int8_t, W> o;
+#pragma unroll
+        for (int j = 0; j < W; ++j) o.v[j] = int8_t(quantize_one(Elem<DT>::widen(c[i].v[j]), inverse));
+        if (k + W <= K) {
+            store_pack(q + k, o);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (k + j < K) q[k + j] = o.v[j];
+        }
+    }
+    if (in_row == 0) scales[row] = scale;
+}
+
+// Rows too long for the registers: one workgroup reads the row twice (the second time from
+// the caches, for rows that fit them).
+template <int DT>
+__global__ __launch_bounds__(1024) void k_quantize_long_rows(int K, const void *X, int64_t ldx,
+                                                             int8_t *Q, int64_t ldq, float *scales)
+{
+    typedef typename Elem<DT>::type T;
+    constexpr int W = 16 / sizeof(T);
+    __shared__ uint32_t peaks[16];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const T *x = static_cast<const T *>(X) + row * ldx;
+    int8_t *q = Q + row * ldq;
+    const int chunks = K / W;
     uint32_t peak = 0;
-    for (int64_t k = tid; k < K; k += 256) peak = max(peak, abs_bits(Elem<DT>::widen(x[k])));
+#pragma unroll 4
+    for (int i = tid; i < chunks; i += 1024) {
+        const Pack<T, W> c = load_pack<T, W>(x + int64_t(i) * W);
+#pragma unroll
+        for (int j = 0; j < W; ++j) peak = max(peak, abs_bits(Elem<DT>::widen(c.v[j])));
+    }
+    const int64_t last = int64_t(chunks) * W + tid;       // at most W - 1 elements are left
+    if (last < K) peak = max(peak, abs_bits(Elem<DT>::widen(x[last])));
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) peak = max(peak, uint32_t(__shfl_xor(int(peak), d)));
     if ((tid & 63) == 0) peaks[tid >> 6] = peak;
     __syncthreads();
-    peak = max(max(peaks[0], peaks[1]), max(peaks[2], peaks[3]));
+#pragma unroll
+    for (int w = 0; w < 16; ++w) peak = max(peak, peaks[w]);
     float scale, inverse;
     row_scale(__builtin_bit_cast(float, peak), scale, inverse);
-    for (int64_t k = tid; k < K; k += 256)
-        Q[row * ldq + k] = int8_t(quantize_one(Elem<DT>::widen(x[k]), inverse));
+#pragma unroll 4
+    for (int i = tid; i < chunks; i += 1024) {
+        const Pack<T, W> c = load_pack<T, W>(x + int64_t(i) * W);
+        Pack<int8_t, W> o;
+#pragma unroll
+        for (int j = 0; j < W; ++j) o.v[j] = int8_t(quantize_one(Elem<DT>::widen(c.v[j]), inverse));
+        store_pack(q + int64_t(i) * W, o);
+    }
+    if (last < K) q[last] = int8_t(quantize_one(Elem<DT>::widen(x[last]), inverse));
     if (tid == 0) scales[row] = scale;
 }
 
