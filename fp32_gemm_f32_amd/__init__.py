@@ -24,8 +24,8 @@ Raw layer (same names and arguments as the C ABI; pointers are integers):
     gemm_i8_quantize_rows(M, K, X, x_dtype, ldx, Q, ldq, scales, stream=0)
     gemm_i8(M, N, K, A, lda, a_scales, B, ldb, b_scales, bias, C, c_dtype, ldc,
             workspace=0, workspace_bytes=0, stream=0)
-    gemm_i8_workspace_size(M, N, K) -> int
-    gemm_i8_plan_describe(M, N, K, num_cus=0) -> dict
+    gemm_i8_workspace_size(M, N, K, A=0, lda=K, B=0, ldb=K) -> int
+    gemm_i8_plan_describe(M, N, K, lda=K, ldb=K, num_cus=0) -> dict
     token_logprobs_raw(...), token_logprobs_workspace_size(M, V, dtype, top) -> int,
     token_logprobs_backward_raw(...): token_logprobs.h's arguments in their order
 Tensor layer (torch tensors on the GPU, launched on torch's current stream):
@@ -121,9 +121,9 @@ def _load():
         lib.gemm_i8_quantize_rows.restype = i
         lib.gemm_i8.argtypes = [i, i, i, p, l, p, p, l, p, p, p, i, l, p, z, p]
         lib.gemm_i8.restype = i
-        lib.gemm_i8_workspace_size.argtypes = [i, i, i]
+        lib.gemm_i8_workspace_size.argtypes = [i, i, i, p, l, p, l]
         lib.gemm_i8_workspace_size.restype = z
-        lib.gemm_i8_plan_describe.argtypes = [i, i, i, i, ctypes.c_char_p, i]
+        lib.gemm_i8_plan_describe.argtypes = [i, i, i, l, l, i, ctypes.c_char_p, i]
         lib.gemm_i8_plan_describe.restype = i
         lib.token_logprobs.argtypes = [i, i, p, i, l, p, i, p, p, p, i, p, p, p, z, p]
         lib.token_logprobs.restype = i
@@ -285,13 +285,16 @@ def gemm_i8(M, N, K, A, lda, a_scales, B, ldb, b_scales, bias, C, c_dtype, ldc, 
                            workspace or None, workspace_bytes, stream or None), "gemm_i8")
 
 
-def gemm_i8_workspace_size(M, N, K) -> int:
-    return _load().gemm_i8_workspace_size(M, N, K)
+def gemm_i8_workspace_size(M, N, K, A=0, lda=None, B=0, ldb=None) -> int:
+    """For packed operands at aligned addresses unless told otherwise."""
+    return _load().gemm_i8_workspace_size(M, N, K, A or None, K if lda is None else lda, B or None,
+                                          K if ldb is None else ldb)
 
 
-def gemm_i8_plan_describe(M, N, K, num_cus=0) -> dict:
+def gemm_i8_plan_describe(M, N, K, lda=None, ldb=None, num_cus=0) -> dict:
     buf = ctypes.create_string_buffer(1024)
-    _check(_load().gemm_i8_plan_describe(M, N, K, num_cus, buf, len(buf)),
+    _check(_load().gemm_i8_plan_describe(M, N, K, K if lda is None else lda,
+                                         K if ldb is None else ldb, num_cus, buf, len(buf)),
            "gemm_i8_plan_describe")
     return json.loads(buf.value.decode())
 
@@ -498,8 +501,8 @@ def matmul_i8(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
     """C[i, j] = (sum_k A[i, k] B[j, k]) a_scales[i] b_scales[j] + bias[j], the sum exact in
     32-bit integers. A is (M, K) and B (N, K) int8 (a row of B is an output channel);
     a_scales (M,), b_scales (N,) and bias (N,) float32. C is out_dtype (float32 by default,
-    bfloat16 or float16). K is at most 131071. The split form's workspace is a torch
-    allocation made here. No gradient flows through it."""
+    bfloat16 or float16). K is at most 131071. The workspace (for a split K, or for large
+    operands off the alignment the kernels load) is a torch allocation made here. No gradient flows through it."""
     import torch
 
     if A.dtype != torch.int8 or B.dtype != torch.int8:
@@ -520,7 +523,7 @@ def matmul_i8(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
     out = (torch.empty((M, N), dtype=out_dtype, device=dev) if out is None
            else _out(out, (M, N), out_dtype, dev, "out"))
     with _Device(dev) as stream:
-        ws_bytes = gemm_i8_workspace_size(M, N, K)
+        ws_bytes = gemm_i8_workspace_size(M, N, K, A.data_ptr(), _ld_of(A), B.data_ptr(), _ld_of(B))
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
         gemm_i8(M, N, K, A.data_ptr(), _ld_of(A), a_scales.data_ptr(), B.data_ptr(), _ld_of(B),
                 b_scales.data_ptr(), 0 if bias is None else bias.data_ptr(), out.data_ptr(),

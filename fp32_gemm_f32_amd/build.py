@@ -22,11 +22,12 @@ OUT = os.path.join(PKG, "libsgemm_f32.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 # Translation units and whether their MFMA accumulators are held in VGPRs (see flags()).
 # The one-wave-per-SIMD kernel keeps 256 accumulators per lane in AGPRs, so it is compiled
-# on its own, without that option.
+# on its own, without that option. The 8-bit product goes without it too: with it the compiler
+# gave the few-rows kernel an accumulator whose registers its load addresses overwrote.
 SOURCES = [(os.path.join(CSRC, "sgemm_f32.hip"), True),
            (os.path.join(CSRC, "sgemm_regpanel.hip"), False),
            (os.path.join(CSRC, "sgemm_persist.hip"), False),
-           (os.path.join(CSRC, "gemm_i8.hip"), True),
+           (os.path.join(CSRC, "gemm_i8.hip"), False),
            (os.path.join(CSRC, "token_logprobs.hip"), True)]
 ARCH = "gfx950"
 

@@ -5,9 +5,11 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <utility>
 
 #include "gemm_i8.h"
 #include "kernel_i8.hpp"
+#include "kernel_i8_rows.hpp"
 #include "ops_common.hpp"
 
 namespace sgemm {
@@ -18,56 +20,150 @@ constexpr int64_t kMaxLd = 8388608;         // 256 rows stay below 2^31 bytes
 constexpr int kWorkspaceAlign = 16;
 
 typedef void (*I8Kernel)(I8Args);
+
+// The tiles, smallest first. `c1` and `c2` are the microseconds a panel of 128 takes with one
+// and (where LDS holds two) two workgroups on every compute unit, operands in the caches;
+// measured on the products 1024^3 to 8192^3 and their thin kin (M of 64 to 1024).
 struct I8Variant {
     const char *name;
-    I8Kernel direct, staged;
+    I8Kernel aligned, any;
     int bm, bn, threads;
+    double c1, c2;
 };
 
-typedef I8Tile<64, 64, 2, 2, 128, 2, true> Tile64;
-typedef I8Tile<64, 64, 2, 2, 128, 2, false> Tile64Staged;
+template <int BM, int BN, int WGM, int WGN, int NSTG>
+constexpr I8Variant tile(const char *name, double c1, double c2)
+{
+    typedef I8Tile<BM, BN, WGM, WGN, 128, NSTG> T;
+    return {name, &k_gemm_i8<T, false>, &k_gemm_i8<T, true>, BM, BN, T::NT, c1, c2};
+}
 
 const I8Variant kVariants[] = {
-    {"i8_64x64", &k_gemm_i8<Tile64>, &k_gemm_i8<Tile64Staged>, 64, 64, Tile64::NT},
+    tile<64, 32, 2, 1, 6>("i8_64x32", 0.23, 0.37),
+    tile<64, 64, 2, 2, 4>("i8_64x64", 0.30, 0.53),
+    tile<64, 128, 2, 2, 3>("i8_64x128", 0.45, 0.77),
+    tile<128, 128, 2, 2, 2>("i8_128x128", 0.85, 1.26),
+    tile<128, 256, 2, 4, 3>("i8_128x256", 1.08, 0.0),
+    tile<256, 256, 4, 2, 2>("i8_256x256", 1.85, 0.0),
 };
+// Few rows: 16 rows, all of K to a workgroup.
+const I8Variant kFewRows = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 1, 8, 4, true>>,
+                            &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 16, 512, 0.0, 0.0};
 
 struct I8Plan {
     const I8Variant *v;
+    I8Kernel kernel;
+    int bm, bn;
     int tiles_m, tiles_n, splits, k_chunk;
+    bool copy_a, copy_b;
+    double cost;
 };
 
-int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-I8Plan make_plan(int M, int N, int K, int cus)
+// What the plan has to know of an operand: rows on word boundaries, K whole chunks.
+struct I8Layout {
+    bool a, b;       // A's and B's rows can be loaded as they are
+};
+I8Layout layout_of(int K, const void *A, int64_t lda, const void *B, int64_t ldb)
 {
-    I8Plan p{};
-    p.v = &kVariants[0];
-    p.tiles_m = ceil_div(M, p.v->bm);
-    p.tiles_n = ceil_div(N, p.v->bn);
-    p.splits = 1;
-    p.k_chunk = K;
-    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-    if (tiles * 2 <= cus) {
-        const int panels = ceil_div(K, 128);
-        const int want = std::min<int64_t>(std::min<int64_t>(cus / tiles, 16), panels / 4);
-        if (want > 1) {
-            p.k_chunk = ceil_div(panels, want) * 128;
-            p.splits = ceil_div(K, p.k_chunk);
-        }
-    }
-    return p;
+    const auto ok = [&](const void *p, int64_t ld) {
+        return K % 16 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 4 == 0;
+    };
+    return {ok(A, lda), ok(B, ldb)};
 }
 
-size_t plan_bytes(const I8Plan &p, int M, int N)
+constexpr double kLaunch = 2.5;          // us: a kernel's start and end
+constexpr double kBytesPerUs = 4.6e6;    // memory traffic of a copy or of streamed operands
+
+// Microseconds of `groups` workgroups of `panels` panels each.
+double tile_cost(const I8Variant &v, int64_t groups, int64_t panels, int cus)
 {
-    return p.splits > 1 ? size_t(p.splits) * M * N * 4 : 0;
+    const int per_cu = v.c2 > 0 ? 2 : 1;
+    const int64_t full = groups / (int64_t(cus) * per_cu), rest = groups % (int64_t(cus) * per_cu);
+    const double whole = per_cu == 2 ? v.c2 : v.c1;
+    const double tail = rest == 0 ? 0.0 : rest <= cus ? v.c1 : v.c2;
+    return (double(full) * whole + tail) * double(panels + 2);
+}
+
+// The cheapest of: every tile, K whole or split; rows as they are, in the slower form for any
+// alignment, or copied into place first. That form costs about half again as much (measured
+// at 8192^3 661 against 464 us, 1023x1025x1027 12.3 against 6.9, 128x8192^2 40 against 26); the
+// copy costs a launch and its traffic, and the workspace.
+I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
+{
+    I8Plan best{};
+    const int64_t panels = ceil_div(K, 128);
+    const bool any = !(rows.a && rows.b);
+    const double bytes = double(M) * K + double(N) * K;
+    const double copied = (rows.a ? 0.0 : double(M) * K) + (rows.b ? 0.0 : double(N) * K);
+    const auto offer = [&](const I8Plan &p) {
+        if (best.v == nullptr || p.cost < best.cost) best = p;
+    };
+    const auto splits_of = [&](int want) {
+        const int64_t chunk = ceil_div(panels, want) * 128;
+        return std::pair<int, int>(int(ceil_div(K, chunk)), int(std::min<int64_t>(chunk, K)));
+    };
+    const auto join_cost = [&](int splits) {
+        return splits == 1 ? 0.0 : kLaunch + 1.5 + double(splits + 1) * M * N * 4 / kBytesPerUs;
+    };
+    const int most = workspace ? int(std::min<int64_t>(16, std::max<int64_t>(1, panels / 4))) : 1;
+    if (M <= 16) {
+        // 8 waves share K in panels of 256 (128 in the form for any rows)
+        const int bn = any ? 32 : 16;
+        for (int want = 1; want <= most; ++want) {
+            const auto [s, chunk] = splits_of(want);
+            const int64_t groups = ceil_div(N, bn) * s;
+            const double step = double(ceil_div(groups, 2 * cus)) * double(ceil_div(chunk, 2048)) * 0.7;
+            const double cost = kLaunch + std::max(step, bytes / kBytesPerUs) * (any ? 1.25 : 1.0) +
+                                join_cost(s);
+            offer({&kFewRows, any ? kFewRows.any : kFewRows.aligned, 16, bn, 1,
+                   int(ceil_div(N, bn)), s, chunk, false, false, cost});
+        }
+        return best;
+    }
+    for (const I8Variant &v : kVariants) {
+        const int64_t tm = ceil_div(M, v.bm), tn = ceil_div(N, v.bn);
+        for (int want = 1; want <= most; ++want) {
+            const auto [s, chunk] = splits_of(want);
+            if (s > 1 && tm * tn * s > 2 * int64_t(cus)) break;
+            const double body = std::max(tile_cost(v, tm * tn * s, ceil_div(chunk, 128), cus),
+                                         bytes / kBytesPerUs);
+            I8Plan p{&v, any ? v.any : v.aligned, v.bm, v.bn, int(tm), int(tn), s, chunk,
+                     false, false, kLaunch + body * (any ? 1.5 : 1.0) + join_cost(s)};
+            offer(p);
+            if (any && workspace) {
+                p.kernel = v.aligned;
+                p.copy_a = !rows.a;
+                p.copy_b = !rows.b;
+                p.cost = 2 * kLaunch + body + 2.0 * copied / kBytesPerUs + join_cost(s);
+                offer(p);
+            }
+        }
+    }
+    return best;
+}
+
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+
+// Workspace: the splits' sums, then the copies.
+struct I8Space {
+    int64_t a, b, bytes;      // offsets of the copies, the whole
+};
+I8Space space_of(const I8Plan &p, int M, int N, int K)
+{
+    I8Space s{};
+    s.a = p.splits > 1 ? round16(int64_t(p.splits) * M * N * 4) : 0;
+    s.b = s.a + (p.copy_a ? int64_t(M) * round16(K) : 0);
+    s.bytes = s.b + (p.copy_b ? int64_t(N) * round16(K) : 0);
+    return s;
 }
 
 bool shape_in_limits(int M, int N, int K, int64_t lda, int64_t ldb)
 {
-    // the smallest tile is 64 wide: its tile count bounds every grid
-    const int64_t tiles = int64_t(ceil_div(M, 64)) * ceil_div(N, 64);
-    return K <= kMaxK && lda < kMaxLd && ldb < kMaxLd && tiles < (int64_t(1) << 26);
+    // 16 x 16 is the smallest tile: its count bounds every grid
+    const int64_t tiles = ceil_div(M, 16) * ceil_div(N, 16);
+    return K <= kMaxK && lda < kMaxLd && ldb < kMaxLd && tiles < (int64_t(1) << 30);
 }
 
 unsigned element_blocks(int64_t total)
@@ -117,12 +213,14 @@ extern "C" int gemm_i8_quantize_rows(int M, int K, const void *X, int x_dtype, i
     return quantize<SGEMM_DTYPE_F16>(M, K, X, ldx, Q, ldq, scales, stream);
 }
 
-extern "C" size_t gemm_i8_workspace_size(int M, int N, int K)
+extern "C" size_t gemm_i8_workspace_size(int M, int N, int K, const int8_t *A, int64_t lda,
+                                         const int8_t *B, int64_t ldb)
 {
-    if (M <= 0 || N <= 0 || K <= 0 || !shape_in_limits(M, N, K, 1, 1)) return 0;
+    if (M <= 0 || N <= 0 || K <= 0 || lda < K || ldb < K || !shape_in_limits(M, N, K, lda, ldb))
+        return 0;
     int cus = 0;
     if (device_cus(&cus) != SGEMM_OK) return 0;
-    return plan_bytes(make_plan(M, N, K, cus), M, N);
+    return size_t(space_of(make_plan(M, N, K, layout_of(K, A, lda, B, ldb), cus, true), M, N, K).bytes);
 }
 
 extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const float *a_scales,
@@ -160,45 +258,51 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     int cus = 0;
     int st = device_cus(&cus);
     if (st != SGEMM_OK) return st;
-    I8Plan plan = make_plan(M, N, K, cus);
-    const size_t need = plan_bytes(plan, M, N);
-    if (need > 0) {
-        if (workspace_bytes == 0) {
-            plan.splits = 1;
-            plan.k_chunk = K;
-        } else if (workspace_bytes < need) {
-            return SGEMM_EINVAL_ARG;
-        }
+    const I8Layout rows = layout_of(K, A, lda, B, ldb);
+    const I8Plan plan = make_plan(M, N, K, rows, cus, workspace_bytes > 0);
+    const I8Space space = space_of(plan, M, N, K);
+    if (workspace_bytes > 0 && workspace_bytes < size_t(space.bytes)) return SGEMM_EINVAL_ARG;
+    if (plan.copy_a || plan.copy_b) {
+        const int64_t ld16 = round16(K);
+        const int per = int(std::max<int64_t>(1, 2048 / (ld16 / 16)));
+        I8Rows16 a16{}, b16{};
+        if (plan.copy_a) a16 = {A, static_cast<int8_t *>(workspace) + space.a, lda, M, per, int(ceil_div(M, per))};
+        if (plan.copy_b) b16 = {B, static_cast<int8_t *>(workspace) + space.b, ldb, N, per, int(ceil_div(N, per))};
+        st = launch(&k_gemm_i8_align, dim3(unsigned(a16.blocks + b16.blocks)), dim3(256), stream, a16, b16, K);
+        if (st != SGEMM_OK) return st;
+        if (plan.copy_a) { p.A = a16.dst; p.lda = ld16; }
+        if (plan.copy_b) { p.B = b16.dst; p.ldb = ld16; }
+        p.K = int(ld16);
     }
     p.partial = static_cast<int *>(workspace);
     p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
-    p.splits = plan.splits; p.k_chunk = plan.k_chunk;
-    const bool direct = K % 16 == 0 && lda % 4 == 0 && ldb % 4 == 0 &&
-                        reinterpret_cast<uintptr_t>(A) % 4 == 0 &&
-                        reinterpret_cast<uintptr_t>(B) % 4 == 0;
-    st = launch(direct ? plan.v->direct : plan.v->staged,
-                dim3(unsigned(plan.tiles_m * plan.tiles_n * plan.splits)),
+    p.splits = plan.splits; p.k_chunk = plan.splits > 1 ? plan.k_chunk : p.K;
+    st = launch(plan.kernel, dim3(unsigned(int64_t(plan.tiles_m) * plan.tiles_n * plan.splits)),
                 dim3(plan.v->threads), stream, p);
     if (st != SGEMM_OK || plan.splits == 1) return st;
     return launch(&k_gemm_i8_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 }
 
-extern "C" int gemm_i8_plan_describe(int M, int N, int K, int num_cus, char *buf, int buflen)
+extern "C" int gemm_i8_plan_describe(int M, int N, int K, int64_t lda, int64_t ldb, int num_cus,
+                                     char *buf, int buflen)
 {
     if (M <= 0 || N <= 0 || K <= 0) return SGEMM_EINVAL_DIM;
+    if (lda < K || ldb < K) return SGEMM_EINVAL_LD;
     if (buf == nullptr || buflen <= 0) return SGEMM_EINVAL_ARG;
-    if (!shape_in_limits(M, N, K, K, K)) return SGEMM_ETOO_LARGE;
+    if (!shape_in_limits(M, N, K, lda, ldb)) return SGEMM_ETOO_LARGE;
     int cus = num_cus;
     if (cus <= 0) {
         const int st = device_cus(&cus);
         if (st != SGEMM_OK) return st;
     }
-    const I8Plan p = make_plan(M, N, K, cus);
+    const I8Plan p = make_plan(M, N, K, layout_of(K, nullptr, lda, nullptr, ldb), cus, true);
     const int n = snprintf(buf, size_t(buflen),
-                           "{\"name\": \"%s\", \"BM\": %d, \"BN\": %d, \"threads\": %d, "
-                           "\"tiles\": [%d, %d], \"splits\": %d, \"k_chunk\": %d, "
-                           "\"workspace_bytes\": %zu}",
-                           p.v->name, p.v->bm, p.v->bn, p.v->threads, p.tiles_m, p.tiles_n,
-                           p.splits, p.k_chunk, plan_bytes(p, M, N));
+                           "{\"name\": \"%s\", \"form\": \"%s\", \"copies\": [%s, %s], \"BM\": %d, "
+                           "\"BN\": %d, \"threads\": %d, \"tiles\": [%d, %d], \"splits\": %d, "
+                           "\"k_chunk\": %d, \"cost_us\": %.2f, \"workspace_bytes\": %lld}",
+                           p.v->name, p.kernel == p.v->aligned ? "aligned" : "any",
+                           p.copy_a ? "true" : "false", p.copy_b ? "true" : "false", p.bm, p.bn,
+                           p.v->threads, p.tiles_m, p.tiles_n, p.splits, p.k_chunk, p.cost,
+                           static_cast<long long>(space_of(p, M, N, K).bytes));
     return n < buflen ? SGEMM_OK : SGEMM_EINVAL_ARG;
 }

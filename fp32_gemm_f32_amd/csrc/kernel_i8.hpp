@@ -53,6 +53,14 @@ __device__ inline void i8_store(void *C, int64_t at, const float (&v)[W], int va
     }
 }
 
+template <int W>
+__device__ inline void i8_store_as(int dtype, void *C, int64_t at, const float (&v)[W], int valid)
+{
+    if (dtype == SGEMM_DTYPE_BF16) i8_store<SGEMM_DTYPE_BF16, W>(C, at, v, valid);
+    else if (dtype == SGEMM_DTYPE_F16) i8_store<SGEMM_DTYPE_F16, W>(C, at, v, valid);
+    else i8_store<SGEMM_DTYPE_F32, W>(C, at, v, valid);
+}
+
 // ------------------------------------------------------------------ the tile kernel ----
 //
 // One workgroup computes a BM x BN tile with WGM x WGN waves of (BM / WGM) x (BN / WGN),
@@ -66,14 +74,17 @@ __device__ inline void i8_store(void *C, int64_t at, const float (&v)[W], int va
 //  * A lane's CB column blocks are consecutive columns of C: LDS row 32 j + c of a wave's
 //    share of B holds global row CB c + j, so lane column c of block j is column CB c + j
 //    and one store writes CB neighbours.
-//  * DIRECT: loads go straight to LDS (buffer loads, 16 bytes a lane), NSTG panels deep;
-//    chunks past the tile's rows or past K read as zero through an offset out of range.
-//    It needs 4-byte aligned rows and K a multiple of 16. Otherwise chunks are loaded at
-//    any alignment into registers and written to LDS a panel later; the chunk that holds
-//    K's end is gathered byte by byte.
-template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_, bool DIRECT_> struct I8Tile {
+//  * Loads go straight to LDS (buffer loads, 16 bytes a lane), NSTG panels deep; chunks past
+//    the tile's rows or past K read as zero through an offset out of range. That needs rows
+//    on word boundaries and K a multiple of 16.
+//  * ANY takes rows at any address and any K. Loads start at the word that holds a row's
+//    first byte, so a row lies in LDS off its place by its address's low two bits, with one
+//    word more behind its last chunk. An operand is read with the word behind it and moved
+//    into place (join_words) before it is multiplied. In the panel that holds K's end A's
+//    values past it are zeroed there, so B's do not count. Words are loaded only where one
+//    of their bytes may be the matrix's (the resource ends with its last row).
+template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Tile {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, BK = BK_, NSTG = NSTG_;
-    static constexpr bool DIRECT = DIRECT_;
     static constexpr int NT = 64 * WGM * WGN;
     static constexpr int WM = BM / WGM, WN = BN / WGN;
     static constexpr int RB = WM / 32, CB = WN / 32;
@@ -81,11 +92,10 @@ template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_, bool DIRECT_
     static constexpr int STEPS = BK / 32;            // MFMA steps per panel
     static constexpr int ACH = BM * CPR / NT, BCH = BN * CPR / NT;   // chunks per thread
     static constexpr int A_BYTES = BM * BK, STAGE = (BM + BN) * BK;
+    static constexpr int NCH = (BM + BN + NT - 1) / NT, NEXT_BYTES = NCH * NT * 4;
     static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
     static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
-    static_assert(DIRECT || NSTG == 2, "register-staged panels use two stages");
     static_assert(STEPS % 2 == 0, "operand buffers alternate over whole panels");
-    static_assert(NSTG * STAGE <= 160 * 1024, "LDS");
 };
 
 // Global row of B (within the tile) at LDS row p.
@@ -95,187 +105,62 @@ template <typename T> __device__ inline int i8_b_row(int p)
     return w * T::WN + T::CB * (r % 32) + r / 32;
 }
 
-template <typename T>
-__global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
+// ---- rows of any alignment
+// 16 bytes at any address from the aligned words that hold them: four words from the one
+// that holds the first byte, and the one that holds the last.
+struct Unaligned {
+    i32x4 body;
+    int last;
+};
+__device__ inline Unaligned load_words(const int8_t *base, uint32_t first, uint32_t last)
 {
-    typedef __attribute__((address_space(3))) void *lds_ptr;
-    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * T::STAGE];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / T::WGN, wn = wave % T::WGN;
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int split = blockIdx.x / tiles;
-    int tm, tn;
-    tile_coords(blockIdx.x - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
-    const int m0 = tm * T::BM, n0 = tn * T::BN;
-    const int k0 = split * p.k_chunk, k1 = min(p.K, k0 + p.k_chunk);
-    const int panels = (k1 - k0 + T::BK - 1) / T::BK;
-    const int8_t *At = p.A + m0 * p.lda + k0;
-    const int8_t *Bt = p.B + n0 * p.ldb + k0;
-    const int kn = k1 - k0;                          // values of k in this split
-
-    // this thread's chunks: LDS chunk i * NT + tid
-    const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
-    const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
-    uint32_t a_off[T::ACH], b_off[T::BCH];
+    return {*reinterpret_cast<const i32x4 *>(base + first), *reinterpret_cast<const int *>(base + last)};
+}
+// Moves them into place; the low two bits of `shift` are the address's.
+__device__ inline i32x4 join_words(const Unaligned &w, uint32_t shift)
+{
+    return i32x4{int(__builtin_amdgcn_alignbyte(w.body[1], w.body[0], shift)),
+                 int(__builtin_amdgcn_alignbyte(w.body[2], w.body[1], shift)),
+                 int(__builtin_amdgcn_alignbyte(w.body[3], w.body[2], shift)),
+                 int(__builtin_amdgcn_alignbyte(w.last, w.body[3], shift))};
+}
+// The first `left` of 16 bytes, zeros behind them.
+__device__ inline i32x4 keep_bytes(i32x4 v, int left)
+{
 #pragma unroll
-    for (int i = 0; i < T::ACH; ++i) {
-        const int r = prow + i * (T::NT / T::CPR);
-        a_off[i] = m0 + r < p.M ? uint32_t(r * p.lda + q * 16) : kOob;
+    for (int i = 0; i < 4; ++i) {
+        const int n = left - 4 * i;
+        v[i] = n >= 4 ? v[i] : n <= 0 ? 0 : v[i] & ((1 << 8 * n) - 1);
     }
-#pragma unroll
-    for (int i = 0; i < T::BCH; ++i) {
-        const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
-        b_off[i] = n0 + r < p.N ? uint32_t(r * p.ldb + q * 16) : kOob;
-    }
+    return v;
+}
 
-    i32x16 acc[T::RB][T::CB];
-#pragma unroll
-    for (int i = 0; i < T::RB; ++i)
-#pragma unroll
-        for (int j = 0; j < T::CB; ++j) acc[i][j] = i32x16(0);
-
-    // operand reads: row l % 32 of a block, chunk 2 t + l / 32
-    const int frow = lane & 31, fhi = lane >> 5;
-    const int fsw = a_swizzle<T::CPR>(frow);
-    const int a_base = (wm * T::WM + frow) * T::BK;
-    const int b_base = T::A_BYTES + (wn * T::WN + frow) * T::BK;
-    i32x4 fa[2][T::RB], fb[2][T::CB];
-    auto read = [&](const char *st, int t, int buf) __attribute__((always_inline)) {
-        const int at = ((2 * t + fhi) ^ fsw) * 16;
-#pragma unroll
-        for (int i = 0; i < T::RB; ++i)
-            fa[buf][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
-#pragma unroll
-        for (int j = 0; j < T::CB; ++j)
-            fb[buf][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
-    };
-    auto multiply = [&](int buf) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < T::RB; ++i)
-#pragma unroll
-            for (int j = 0; j < T::CB; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[buf][i], fb[buf][j],
-                                                                  acc[i][j], 0, 0, 0);
-    };
-
-    if constexpr (T::DIRECT) {
-        const auto rsa = make_rsrc32(reinterpret_cast<const float *>(At), kFullRange);
-        const auto rsb = make_rsrc32(reinterpret_cast<const float *>(Bt), kFullRange);
-        auto issue = [&](int panel) __attribute__((always_inline)) {
-            char *st = smem + (panel % T::NSTG) * T::STAGE;
-            const int k = panel * T::BK;
-            // in the range's last panel, and one past it, chunks past its end read as zero
-            const uint32_t past = k + q * 16 >= kn ? kOob : 0u;
-#pragma unroll
-            for (int i = 0; i < T::ACH; ++i) {
-                const uint32_t off = a_off[i] | past;
-                char *to = st + (i * T::NT + wave * 64) * 16;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_ptr)to, 16, off, k, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < T::BCH; ++i) {
-                const uint32_t off = b_off[i] | past;
-                char *to = st + T::A_BYTES + (i * T::NT + wave * 64) * 16;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_ptr)to, 16, off, k, 0, 0);
-            }
-        };
-        // The step before a panel's last ends the reads of its stage, so the barrier comes
-        // there: the wave's loads of the next panel have landed, every wave's have after the
-        // barrier, and the stage just read is loaded again and the next one's first operands
-        // are read under the last step's MFMAs.
-        constexpr int LPP = T::ACH + T::BCH;
-#pragma unroll
-        for (int i = 0; i < T::NSTG; ++i) issue(i);
-        wait_vmcnt<(T::NSTG - 1) * LPP>();
-        asm volatile("s_barrier" ::: "memory");
-        read(smem, 0, 0);
-        int stage = 0;
-        for (int panel = 0; panel < panels; ++panel) {
-            const char *st = smem + stage * T::STAGE;
-            stage = stage + 1 == T::NSTG ? 0 : stage + 1;
-            static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
-                constexpr int t = decltype(tc)::value;
-                constexpr bool last = t == T::STEPS - 1;
-                if constexpr (!last) {
-                    read(st, t + 1, (t + 1) & 1);
-                } else {
-                    __builtin_amdgcn_sched_barrier(0);
-                    wait_vmcnt<(T::NSTG - 2) * LPP>();
-                    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                    read(smem + stage * T::STAGE, 0, (t + 1) & 1);
-                    issue(panel + T::NSTG);
-                }
-                multiply(t & 1);
-                // operand reads behind the first MFMAs, the loads behind the others
-                constexpr int ops = T::RB + T::CB, mf = T::RB * T::CB;
-                constexpr int rm = last ? (mf + 1) / 2 : (ops < mf ? ops : mf);
-                constexpr int lm = mf - rm > 0 ? mf - rm : 1;
-                static_for<0, mf>([&](auto mc) __attribute__((always_inline)) {
-                    constexpr int m = decltype(mc)::value;
-                    constexpr int r = m < rm ? (m + 1) * ops / rm - m * ops / rm : 0;
-                    constexpr int n = m - (mf - lm);
-                    constexpr int l = last && n >= 0 ? (n + 1) * LPP / lm - n * LPP / lm : 0;
-                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-                    if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, r, 0);
-                    if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
-                });
-            });
-        }
-        wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
-    } else {
-        i32x4 ra[T::ACH], rb[T::BCH];
-        auto fetch = [&](const int8_t *base, uint32_t off, int k) __attribute__((always_inline)) {
-            i32x4 v = i32x4(0);
-            const int left = kn - (k + q * 16);
-            if (off != kOob && left > 0) {
-                const int8_t *src = base + off + k;
-                if (left >= 16) {
-                    const Pack<int, 4> w = load_pack<int, 4>(reinterpret_cast<const int *>(src));
-                    v = i32x4{w.v[0], w.v[1], w.v[2], w.v[3]};
-                } else {
-                    for (int e = 0; e < 16; ++e) {
-                        const unsigned b = e < left ? uint8_t(src[e]) : 0u;
-                        const unsigned s = b << (8 * (e & 3));
-                        v[0] |= (e >> 2) == 0 ? s : 0u;
-                        v[1] |= (e >> 2) == 1 ? s : 0u;
-                        v[2] |= (e >> 2) == 2 ? s : 0u;
-                        v[3] |= (e >> 2) == 3 ? s : 0u;
-                    }
-                }
-            }
-            return v;
-        };
-        auto load = [&](int panel) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < T::ACH; ++i) ra[i] = fetch(At, a_off[i], panel * T::BK);
-#pragma unroll
-            for (int i = 0; i < T::BCH; ++i) rb[i] = fetch(Bt, b_off[i], panel * T::BK);
-        };
-        load(0);
-        for (int panel = 0; panel < panels; ++panel) {
-            char *st = smem + (panel & 1) * T::STAGE;
-#pragma unroll
-            for (int i = 0; i < T::ACH; ++i)
-                *reinterpret_cast<i32x4 *>(st + (i * T::NT + tid) * 16) = ra[i];
-#pragma unroll
-            for (int i = 0; i < T::BCH; ++i)
-                *reinterpret_cast<i32x4 *>(st + T::A_BYTES + (i * T::NT + tid) * 16) = rb[i];
-            // one barrier a panel: a wave writes a stage again only after the barrier that
-            // follows every wave's reads of it
-            __syncthreads();
-            if (panel + 1 < panels) load(panel + 1);
-            read(st, 0, 0);
-#pragma unroll
-            for (int t = 0; t < T::STEPS; ++t) {
-                if (t + 1 < T::STEPS) read(st, t + 1, (t + 1) & 1);
-                multiply(t & 1);
-            }
+// The chunk of 16 bytes at k of a row that ends at kn, which the chunk may cross or lie past:
+// zeros from there on, and no byte past kn is read. A row of 16 bytes and more is read at
+// its last 16, which are moved into place.
+__device__ inline i32x4 load_tail(const int8_t *row, int k, int kn)
+{
+    unsigned __int128 v = 0;
+    if (k < kn) {
+        if (kn >= 16) {
+            const int at = min(k, kn - 16);
+            const Pack<int, 4> w = load_pack<int, 4>(reinterpret_cast<const int *>(row + at));
+            v = __builtin_bit_cast(unsigned __int128, w) >> (8 * (k - at));
+        } else {
+            for (int e = kn - 1; e >= k; --e) v = v << 8 | uint8_t(row[e]);
         }
     }
+    return __builtin_bit_cast(i32x4, v);
+}
 
-    // epilogue: this lane's rows 8 (v / 4) + v % 4 + 4 fhi of each row block, columns
-    // CB (l % 32) + 0 .. CB - 1 of the wave's share
+// Stores a wave's accumulators (or, in the split form, its sums): this lane's rows
+// 8 (v / 4) + v % 4 + 4 (l / 32) of each row block, columns CB (l % 32) + 0 .. CB - 1 of the
+// wave's share.
+template <typename T>
+__device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)[T::RB][T::CB],
+                                            int m0, int n0, int split, int wm, int wn)
+{
+    const int frow = threadIdx.x & 31, fhi = (threadIdx.x & 63) >> 5;
     const int col = n0 + wn * T::WN + T::CB * frow;
     const int valid = p.N - col;
     const int row0 = m0 + wm * T::WM + 4 * fhi;
@@ -321,6 +206,267 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     else store_all(std::integral_constant<int, SGEMM_DTYPE_F32>{});
 }
 
+// Size of the resource that covers [from, end), `end` rounded up to a whole word.
+__device__ inline uint32_t i8_range(const int8_t *from, const int8_t *end)
+{
+    const int64_t n = end - from;
+    return n <= 0 ? 0u : n >= int64_t(kFullRange) ? kFullRange : (uint32_t(n) + 3u) & ~3u;
+}
+
+// 16 (or 4) bytes a lane from base + off, zeros where that is past `range`, to LDS at `to` plus
+// as many bytes times the lane.
+typedef __attribute__((address_space(3))) void *lds_ptr;
+__device__ __forceinline__ void i8_load16_lds(const int8_t *base, uint32_t range, uint32_t off, char *to)
+{
+    const auto rsrc = make_rsrc32(reinterpret_cast<const float *>(base), range);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 16, off, 0, 0, 0);
+}
+__device__ __forceinline__ void i8_load4_lds(const int8_t *base, uint32_t range, uint32_t off, char *to)
+{
+    const auto rsrc = make_rsrc32(reinterpret_cast<const float *>(base), range);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 4, off, 0, 0, 0);
+}
+
+template <typename T, bool ANY>
+__global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
+{
+    constexpr int STAGE = T::STAGE + (ANY ? T::NEXT_BYTES : 0);
+    static_assert(T::NSTG >= 2 && T::NSTG * STAGE <= 160 * 1024, "LDS");
+    static_assert(!ANY || T::BM % 64 == 0, "a wave's rows of next words are of one matrix");
+    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / T::WGN, wn = wave % T::WGN;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int split = blockIdx.x / tiles;
+    int tm, tn;
+    tile_coords(blockIdx.x - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
+    const int m0 = tm * T::BM, n0 = tn * T::BN;
+    const int k0 = split * p.k_chunk, k1 = min(p.K, k0 + p.k_chunk);
+    const int panels = (k1 - k0 + T::BK - 1) / T::BK;
+    const int kn = k1 - k0;                          // values of k in this split
+    const int8_t *At = p.A + m0 * p.lda + k0;
+    const int8_t *Bt = p.B + n0 * p.ldb + k0;
+    const uint32_t a_low = ANY ? uint32_t(reinterpret_cast<uintptr_t>(At)) & 3 : 0;
+    const uint32_t b_low = ANY ? uint32_t(reinterpret_cast<uintptr_t>(Bt)) & 3 : 0;
+    At -= a_low;
+    Bt -= b_low;
+
+    // this thread's chunks: LDS chunk i * NT + tid
+    const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
+    const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
+    uint32_t a_off[T::ACH], b_off[T::BCH], n_off[T::NCH];
+#pragma unroll
+    for (int i = 0; i < T::ACH; ++i) {
+        const int r = prow + i * (T::NT / T::CPR);
+        a_off[i] = m0 + r < p.M ? (a_low + uint32_t(r * p.lda) + q * 16) & ~3u : kOob;
+    }
+#pragma unroll
+    for (int i = 0; i < T::BCH; ++i) {
+        const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
+        b_off[i] = n0 + r < p.N ? (b_low + uint32_t(r * p.ldb) + q * 16) & ~3u : kOob;
+    }
+    // ANY: the word past a panel's last chunk of LDS row i * NT + tid (A's rows, then B's)
+#pragma unroll
+    for (int i = 0; i < T::NCH; ++i) {
+        const int e = i * T::NT + tid;
+        const int r = e < T::BM ? e : i8_b_row<T>(e - T::BM);
+        n_off[i] = e < T::BM ? (m0 + r < p.M ? (a_low + uint32_t(r * p.lda) + T::BK) & ~3u : kOob)
+                 : e < T::BM + T::BN && n0 + r < p.N
+                     ? (b_low + uint32_t(r * p.ldb) + T::BK) & ~3u : kOob;
+    }
+
+    i32x16 acc[T::RB][T::CB];
+#pragma unroll
+    for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j) acc[i][j] = i32x16(0);
+
+    // operand reads: row l % 32 of a block, chunk 2 t + l / 32
+    const int frow = lane & 31, fhi = lane >> 5;
+    const int fsw = a_swizzle<T::CPR>(frow);
+    const int a_row = wm * T::WM + frow, b_row = wn * T::WN + frow;
+    const int a_base = a_row * T::BK, b_base = T::A_BYTES + b_row * T::BK;
+    i32x4 fa[2][T::RB], fb[2][T::CB];
+    int na[2][T::RB], nb[2][T::CB];                  // ANY: the words behind the chunks
+    uint32_t a_shift[T::RB], b_shift[T::CB];
+    if constexpr (ANY) {
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i) a_shift[i] = a_low + uint32_t(a_row + 32 * i) * uint32_t(p.lda);
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j)
+            b_shift[j] = b_low + uint32_t(i8_b_row<T>(b_row + 32 * j)) * uint32_t(p.ldb);
+    }
+    // of a panel's last chunk the word behind lies past the rows, one to a row
+    const int a_last = fhi ? T::STAGE + a_row * 4 : a_base + (((T::CPR - 1) ^ fsw) * 16);
+    const int b_last = fhi ? T::STAGE + (T::BM + b_row) * 4 : b_base + (((T::CPR - 1) ^ fsw) * 16);
+    const int last_step = fhi ? 32 * 4 : 32 * T::BK;
+    auto read = [&](const char *st, auto tc, int buf) __attribute__((always_inline)) {
+        constexpr int t = decltype(tc)::value;
+        const int at = ((2 * t + fhi) ^ fsw) * 16;
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+            fa[buf][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j)
+            fb[buf][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
+        if constexpr (ANY && t < T::STEPS - 1) {
+            const int next = ((2 * t + fhi + 1) ^ fsw) * 16;
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i)
+                na[buf][i] = *reinterpret_cast<const int *>(st + a_base + next + i * 32 * T::BK);
+#pragma unroll
+            for (int j = 0; j < T::CB; ++j)
+                nb[buf][j] = *reinterpret_cast<const int *>(st + b_base + next + j * 32 * T::BK);
+        } else if constexpr (ANY) {
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i)
+                na[buf][i] = *reinterpret_cast<const int *>(st + a_last + i * last_step);
+#pragma unroll
+            for (int j = 0; j < T::CB; ++j)
+                nb[buf][j] = *reinterpret_cast<const int *>(st + b_last + j * last_step);
+        }
+    };
+    // MASK: values of k from `left` on (of this lane's chunk) count as zero
+    auto multiply = [&](int buf, auto mask, int left) __attribute__((always_inline)) {
+        if constexpr (ANY) {
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i) {
+                fa[buf][i] = join_words({fa[buf][i], na[buf][i]}, a_shift[i]);
+                if constexpr (decltype(mask)::value) fa[buf][i] = keep_bytes(fa[buf][i], left);
+            }
+#pragma unroll
+            for (int j = 0; j < T::CB; ++j) fb[buf][j] = join_words({fb[buf][j], nb[buf][j]}, b_shift[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < T::CB; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[buf][i], fb[buf][j],
+                                                                  acc[i][j], 0, 0, 0);
+    };
+
+    const int8_t *const a_end = p.A + (p.M - 1) * p.lda + p.K, *const b_end = p.B + (p.N - 1) * p.ldb + p.K;
+    auto issue = [&](int panel) __attribute__((always_inline)) {
+        char *st = smem + (panel % T::NSTG) * STAGE;
+        const int k = panel * T::BK;
+        const int8_t *const ak = At + k, *const bk = Bt + k;
+        const uint32_t an = ANY ? i8_range(ak, a_end) : kFullRange;
+        const uint32_t bn = ANY ? i8_range(bk, b_end) : kFullRange;
+        // in the range's last panel, and past it, chunks past its end read as zero (a row
+        // that lies off its place by up to 3 bytes may end in the next chunk)
+        const uint32_t past = k + q * 16 >= kn + (ANY ? 3 : 0) ? kOob : 0u;
+#pragma unroll
+        for (int i = 0; i < T::ACH; ++i)
+            i8_load16_lds(ak, an, a_off[i] | past, st + (i * T::NT + wave * 64) * 16);
+#pragma unroll
+        for (int i = 0; i < T::BCH; ++i)
+            i8_load16_lds(bk, bn, b_off[i] | past, st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
+        if constexpr (ANY) {
+            const uint32_t none = k >= kn ? kOob : 0u;
+#pragma unroll
+            for (int i = 0; i < T::NCH; ++i) {
+                // a wave's 64 rows are all A's or all B's
+                const bool of_a = i * T::NT + wave * 64 < T::BM;
+                i8_load4_lds(of_a ? ak : bk, of_a ? an : bn, n_off[i] | none,
+                               st + T::STAGE + (i * T::NT + wave * 64) * 4);
+            }
+        }
+    };
+    // The step before a panel's last ends the reads of its stage, so the barrier comes there:
+    // the wave's loads of the next panel have landed, every wave's have after the barrier, and
+    // the stage just read is loaded again and the next one's first operands are read under the
+    // last step's MFMAs.
+    constexpr int LPP = T::ACH + T::BCH + (ANY ? T::NCH : 0);
+    typedef std::integral_constant<int, 0> First;
+#pragma unroll
+    for (int i = 0; i < T::NSTG; ++i) issue(i);
+    wait_vmcnt<(T::NSTG - 1) * LPP>();
+    asm volatile("s_barrier" ::: "memory");
+    read(smem, First{}, 0);
+    int stage = 0;
+    const int full = ANY ? kn / T::BK : panels;      // panels without a masked step
+    auto run = [&](int panel, auto mask) __attribute__((always_inline)) {
+        const char *st = smem + stage * STAGE;
+        stage = stage + 1 == T::NSTG ? 0 : stage + 1;
+        static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
+            constexpr int t = decltype(tc)::value;
+            constexpr bool last = t == T::STEPS - 1;
+            if constexpr (!last) {
+                read(st, std::integral_constant<int, t + 1>{}, (t + 1) & 1);
+            } else {
+                __builtin_amdgcn_sched_barrier(0);
+                wait_vmcnt<(T::NSTG - 2) * LPP>();
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                read(smem + stage * STAGE, First{}, (t + 1) & 1);
+                issue(panel + T::NSTG);
+            }
+            multiply(t & 1, mask, kn - panel * T::BK - 16 * (2 * t + fhi));
+            // operand reads behind the first MFMAs, the loads behind the others
+            constexpr int ops = (T::RB + T::CB) * (ANY ? 2 : 1), mf = T::RB * T::CB;
+            constexpr int rm = last ? (mf + 1) / 2 : (ops < mf ? ops : mf);
+            constexpr int lm = mf - rm > 0 ? mf - rm : 1;
+            static_for<0, mf>([&](auto mc) __attribute__((always_inline)) {
+                constexpr int m = decltype(mc)::value;
+                constexpr int r = m < rm ? (m + 1) * ops / rm - m * ops / rm : 0;
+                constexpr int n = m - (mf - lm);
+                constexpr int l = last && n >= 0 ? (n + 1) * LPP / lm - n * LPP / lm : 0;
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, r, 0);
+                if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
+            });
+        });
+    };
+    for (int panel = 0; panel < full; ++panel) run(panel, std::false_type{});
+    if constexpr (ANY)
+        if (full < panels) run(full, std::true_type{});
+    wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
+    i8_epilogue<T>(p, acc, m0, n0, split, wm, wn);
+}
+
+// ------------------------------------------------------------------ rows put in place ---
+// Copies rows of any length and alignment to rows of whole 16-byte chunks, zeros behind
+// their ends, for products large enough to earn it. A workgroup copies `rows` rows at a time
+// (about 2048 chunks), of A in its first blocks and of B in the others.
+struct I8Rows16 {
+    const int8_t *src;
+    int8_t *dst;
+    int64_t ld;
+    int count, rows, blocks;     // rows in all, rows to a workgroup, workgroups
+};
+
+__global__ __launch_bounds__(256) void k_gemm_i8_align(I8Rows16 a, I8Rows16 b, int K)
+{
+    const bool of_a = int(blockIdx.x) < a.blocks;
+    const I8Rows16 &p = of_a ? a : b;
+    const int block = blockIdx.x - (of_a ? 0 : a.blocks);
+    const int cpr = (K + 15) / 16;
+    const int64_t row0 = int64_t(block) * p.rows;
+    const int n = min(p.rows, int(p.count - row0)) * cpr;
+    const int8_t *src = p.src + row0 * p.ld;
+    i32x4 *dst = reinterpret_cast<i32x4 *>(p.dst) + row0 * cpr;
+    constexpr int U = 4;
+    for (int e0 = threadIdx.x; e0 < n; e0 += 256 * U) {
+        Unaligned w[U];
+        uint32_t low[U];
+        int left[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int e = min(e0 + 256 * u, n - 1);
+            const int r = e / cpr, k = (e - r * cpr) * 16;
+            const int8_t *row = src + r * p.ld;
+            left[u] = K - k;
+            low[u] = uint32_t(reinterpret_cast<uintptr_t>(row + k)) & 3;
+            if (left[u] >= 16) w[u] = load_words(row + k - low[u], 0, (low[u] + 15) & ~3u);
+            else w[u] = {load_tail(row, k, K), 0};
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (e0 + 256 * u < n)
+                dst[e0 + 256 * u] = left[u] >= 16 ? join_words(w[u], low[u]) : w[u].body;
+    }
+}
+
 // ------------------------------------------------------------------ the split's join ----
 // Adds the splits' integer sums (exact in any order) and applies the epilogue; one thread
 // per element of C, strided over the grid. Bound by reading splits * M * N integers, which
@@ -335,9 +481,7 @@ __global__ __launch_bounds__(256) void k_gemm_i8_join(I8Args p)
         int sum = 0;
         for (int s = 0; s < p.splits; ++s) sum += p.partial[s * total + e];
         const float x[1] = {i8_value(sum, p.sa[m], p.sb[n], p.bias ? p.bias[n] : 0.0f)};
-        if (p.c_dtype == SGEMM_DTYPE_BF16) i8_store<SGEMM_DTYPE_BF16, 1>(p.C, m * p.ldc + n, x, 1);
-        else if (p.c_dtype == SGEMM_DTYPE_F16) i8_store<SGEMM_DTYPE_F16, 1>(p.C, m * p.ldc + n, x, 1);
-        else i8_store<SGEMM_DTYPE_F32, 1>(p.C, m * p.ldc + n, x, 1);
+        i8_store_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
     }
 }
 
@@ -350,9 +494,7 @@ __global__ __launch_bounds__(256) void k_gemm_i8_empty(I8Args p)
         const int64_t m = e / p.N;
         const int n = int(e - m * p.N);
         const float x[1] = {p.bias ? p.bias[n] : 0.0f};
-        if (p.c_dtype == SGEMM_DTYPE_BF16) i8_store<SGEMM_DTYPE_BF16, 1>(p.C, m * p.ldc + n, x, 1);
-        else if (p.c_dtype == SGEMM_DTYPE_F16) i8_store<SGEMM_DTYPE_F16, 1>(p.C, m * p.ldc + n, x, 1);
-        else i8_store<SGEMM_DTYPE_F32, 1>(p.C, m * p.ldc + n, x, 1);
+        i8_store_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
     }
 }
 

@@ -7,8 +7,8 @@
  * in elements, every argument validated before any HIP call, a negative sgemm_status on
  * refusal, asynchronous launches on `stream` (a hipStream_t; NULL is the default stream),
  * no mutable state between calls, no allocation. Any leading dimension and any address
- * aligned to the element works; 4-byte aligned rows of a length that 16 divides are the
- * fast case.
+ * aligned to the element works; rows at 4-byte aligned addresses, of a length that 16 divides,
+ * are the fast case.
  *
  * Validation (checked in this order):
  *   dimensions >= 0                                     else SGEMM_EINVAL_DIM
@@ -68,11 +68,13 @@ int gemm_i8_quantize_rows(int M, int K,
  * below 2^31 bytes (lda, ldb < 8388608), else SGEMM_ETOO_LARGE.
  *
  * workspace: products with few tiles split K over workgroups and join the partial sums
- * there (32-bit integers) with a second kernel. Caller-owned device memory of
- * gemm_i8_workspace_size bytes, 16-byte aligned; SGEMM_EINVAL_ARG if smaller, and it must
- * not overlap A, B, C, the scales or bias. NULL with 0 bytes runs without a split, which
- * is right for every shape and slower for those. No initialisation needed, contents
- * unspecified on return; calls that share one must not overlap in time.
+ * there (32-bit integers) with a second kernel; large products of rows off a word's boundary
+ * (or of a K that 16 does not divide) copy them there first, in whole 16-byte chunks.
+ * Caller-owned device memory of gemm_i8_workspace_size bytes, 16-byte aligned;
+ * SGEMM_EINVAL_ARG if smaller, and it must not overlap A, B, C, the scales or bias. NULL
+ * with 0 bytes runs without either, which is right for every shape and slower for those. No
+ * initialisation needed, contents unspecified on return; calls that share one must not
+ * overlap in time.
  *
  * M == 0 or N == 0 launches nothing; K == 0 writes the bias (or zeros; scales are not read
  * then).
@@ -85,17 +87,21 @@ int gemm_i8(int M, int N, int K,
             void *workspace, size_t workspace_bytes,
             void *stream);
 
-/* Bytes of workspace gemm_i8 uses for this shape on the current device (0: none, also for
- * dimensions it would refuse and where no device answers). */
-size_t gemm_i8_workspace_size(int M, int N, int K);
+/* Bytes of workspace gemm_i8 uses for these operands on the current device (0: none, also for
+ * arguments it would refuse and where no device answers). Of A and B only the addresses
+ * count; nothing is read. */
+size_t gemm_i8_workspace_size(int M, int N, int K, const int8_t *A, int64_t lda,
+                              const int8_t *B, int64_t ldb);
 
 /*
- * Writes a one-line JSON description of the plan gemm_i8 runs for packed, aligned operands
- * of this shape into buf: kernel, tile, waves, splits, grid, workspace bytes. num_cus > 0
- * plans for that many compute units (no GPU needed), otherwise the current device's.
- * Returns SGEMM_OK or a negative status (SGEMM_EINVAL_ARG: the buffer is too small).
+ * Writes a one-line JSON description of the plan gemm_i8 runs, given its workspace, for
+ * operands of this shape at 4-byte aligned addresses into buf: tile, form, copies, splits,
+ * workspace bytes, the cost the choice was made by. num_cus > 0 plans for that many compute
+ * units (no GPU needed), otherwise the current device's. Returns SGEMM_OK or a negative
+ * status (SGEMM_EINVAL_ARG: the buffer is too small).
  */
-int gemm_i8_plan_describe(int M, int N, int K, int num_cus, char *buf, int buflen);
+int gemm_i8_plan_describe(int M, int N, int K, int64_t lda, int64_t ldb, int num_cus, char *buf,
+                          int buflen);
 
 #ifdef __cplusplus
 }

@@ -155,11 +155,13 @@ def test_empty_shapes(torch):
     assert (g.matmul_i8(z(3, 0), f(3), z(5, 0), f(5)) == 0).all()
 
 
-def test_split_equals_unsplit(torch):
-    """The split form (with a workspace) and the unsplit one (without) give the same bits;
-    a workspace that is too small is refused."""
-    M, N, K = 96, 80, 16384
-    assert g.gemm_i8_workspace_size(M, N, K) > 0
+@pytest.mark.parametrize("M,N,K", [(96, 80, 16384), (9, 70, 65536), (700, 690, 8000), (1030, 1100, 1027),
+                                   (300, 5000, 4095), (24, 48, 20001)])
+def test_with_and_without_workspace(torch, M, N, K):
+    """The forms that use a workspace (split, copied into place) and those that run without
+    give the same bits; a workspace that is too small is refused."""
+    size = g.gemm_i8_workspace_size(M, N, K)
+    assert size > 0 or K < 10000          # a long K over few tiles is split
     rng = np.random.default_rng(8)
     A, B = torch.from_numpy(codes(rng, M, K)).cuda(), torch.from_numpy(codes(rng, N, K)).cuda()
     sa, sb = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
@@ -170,9 +172,37 @@ def test_split_equals_unsplit(torch):
     g.gemm_i8(*args, stream=torch.cuda.current_stream().cuda_stream)
     assert torch.equal(C, D)
     ws = torch.empty(64, dtype=torch.uint8, device="cuda")
-    with pytest.raises(g.SgemmError) as e:
-        g.gemm_i8(*args, ws.data_ptr(), 64)
-    assert e.value.status == -6
+    if size > 64:
+        with pytest.raises(g.SgemmError) as e:
+            g.gemm_i8(*args, ws.data_ptr(), 64)
+        assert e.value.status == -6
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 40, 200), (64, 96, 384), (130, 70, 1000), (260, 300, 513),
+                                   (1500, 2100, 130), (2300, 2500, 257), (4200, 4100, 40)])
+@pytest.mark.parametrize("lda,ldb,ao,bo", [(0, 0, 0, 0), (1, 2, 1, 0), (3, 5, 2, 3), (0, 4, 3, 1)])
+def test_rows_of_any_alignment_without_workspace(torch, M, N, K, lda, ldb, ao, bo):
+    """Rows at every offset from a word's boundary and every remainder of K, in the tiles' own
+    loads (no workspace, so nothing is copied into place first). The buffers end with the
+    matrices' last byte."""
+    rng = np.random.default_rng(M + K + lda)
+    A, B = codes(rng, M, K), codes(rng, N, K)
+
+    def flush(host, ld, offset):
+        rows = host.shape[0]
+        dev = torch.full((offset + (rows - 1) * ld + K,), -128, dtype=torch.int8, device="cuda")
+        dev.as_strided((rows, K), (ld, 1), offset).copy_(torch.from_numpy(host))
+        return dev, dev.data_ptr() + offset
+    for k in (K, K - 1, K - 2, K - 3):
+        keep_a, pa = flush(A, K + lda, ao)
+        keep_b, pb = flush(B, K + ldb, bo)
+        C = torch.empty(M, N, device="cuda")
+        one = torch.ones(max(M, N), device="cuda")
+        print(f"[i8 any] {M}x{N}x{k} ld +{lda} +{ldb} offsets {ao} {bo}", flush=True)
+        g.gemm_i8(M, N, k, pa, K + lda, one.data_ptr(), pb, K + ldb, one.data_ptr(), 0,
+                  C.data_ptr(), 0, N, stream=torch.cuda.current_stream().cuda_stream)
+        want = (A[:, :k].astype(np.float64) @ B[:, :k].astype(np.float64).T).astype(np.float32)
+        assert np.array_equal(C.cpu().numpy(), want)
 
 
 def quantized(x):

@@ -76,19 +76,34 @@ def test_gemm_i8_refusals():
 def test_gemm_i8_plan_on_the_host():
     buf = ctypes.create_string_buffer(512)
     lib = g.library()
-    assert lib.gemm_i8_plan_describe(0, 4, 4, 256, buf, 512) == DIM
-    assert lib.gemm_i8_plan_describe(4, 4, 4, 256, None, 0) == ARG
-    assert lib.gemm_i8_plan_describe(4, 4, 4, 256, buf, 8) == ARG
-    assert lib.gemm_i8_plan_describe(4, 4, 131072, 256, buf, 512) == LARGE
-    for M, N, K in [(1, 64, 64), (1, 8192, 8192), (48, 16384, 4096), (1024, 1024, 1024),
-                    (1023, 1025, 1027), (8192, 8192, 8192), (64, 64, 131071), (65, 130, 16384),
-                    (100000, 1, 1)]:
-        d = g.gemm_i8_plan_describe(M, N, K, num_cus=256)
-        assert d["tiles"][0] * d["BM"] >= M > (d["tiles"][0] - 1) * d["BM"]
-        assert d["tiles"][1] * d["BN"] >= N > (d["tiles"][1] - 1) * d["BN"]
-        # the splits cover K, none of them empty
-        assert d["splits"] * d["k_chunk"] >= K > (d["splits"] - 1) * d["k_chunk"]
-        assert d["workspace_bytes"] == (d["splits"] * M * N * 4 if d["splits"] > 1 else 0)
+    assert lib.gemm_i8_plan_describe(0, 4, 4, 4, 4, 256, buf, 512) == DIM
+    assert lib.gemm_i8_plan_describe(4, 4, 4, 3, 4, 256, buf, 512) == LD
+    assert lib.gemm_i8_plan_describe(4, 4, 4, 4, 4, 256, None, 0) == ARG
+    assert lib.gemm_i8_plan_describe(4, 4, 4, 4, 4, 256, buf, 8) == ARG
+    assert lib.gemm_i8_plan_describe(4, 4, 131072, 131072, 131072, 256, buf, 512) == LARGE
+    seen = set()
+    for M, N, K in [(1, 1, 1), (1, 64, 64), (1, 8192, 8192), (16, 64, 131071), (48, 16384, 4096),
+                    (1024, 1024, 1024), (1023, 1025, 1027), (8192, 8192, 8192), (64, 64, 131071),
+                    (65, 130, 16384), (100000, 1, 1), (4096, 4096, 4096), (1024, 4096, 4096),
+                    (2000, 16000, 500), (128, 8192, 8192), (1024, 4096, 8192), (2048, 2048, 2048)]:
+        for pad_a, pad_b in [(0, 0), (5, 0), (0, 3), (13, 13), (16, 4)]:
+            d = g.gemm_i8_plan_describe(M, N, K, K + pad_a, K + pad_b, num_cus=256)
+            seen.add(d["name"])
+            assert d["tiles"][0] * d["BM"] >= M > (d["tiles"][0] - 1) * d["BM"]
+            assert d["tiles"][1] * d["BN"] >= N > (d["tiles"][1] - 1) * d["BN"]
+            # the splits cover K, none of them empty, and start on whole panels
+            assert d["splits"] * d["k_chunk"] >= K > (d["splits"] - 1) * d["k_chunk"]
+            assert d["splits"] == 1 or d["k_chunk"] % 128 == 0
+            k16 = (K + 15) // 16 * 16
+            want = (d["splits"] * M * N * 4 + 15) // 16 * 16 if d["splits"] > 1 else 0
+            want += (M * k16 if d["copies"][0] else 0) + (N * k16 if d["copies"][1] else 0)
+            assert d["workspace_bytes"] == want
+            # the aligned form only ever sees rows it can load
+            fit = [K % 16 == 0 and p % 4 == 0 for p in (pad_a, pad_b)]
+            if d["form"] == "aligned":
+                assert all(f or c for f, c in zip(fit, d["copies"]))
+            assert not any(f and c for f, c in zip(fit, d["copies"]))
+    assert len(seen) >= 5, seen
 
 
 def test_token_logprobs_refusals():
@@ -127,6 +142,7 @@ def test_token_logprobs_backward_refusals():
 
 def test_workspace_sizes_of_refused_shapes():
     assert g.gemm_i8_workspace_size(-1, 4, 4) == 0 and g.gemm_i8_workspace_size(4, 4, 131072) == 0
+    assert g.gemm_i8_workspace_size(4, 4, 8, P, 7, P, 8) == 0
     assert g.token_logprobs_workspace_size(4, 100, 7, 0) == 0
     assert g.token_logprobs_workspace_size(4, 100, 0, 101) == 0
 
