@@ -23,14 +23,15 @@ struct RowSplit {
     int64_t part_bytes;
 };
 
-// How many workgroups share a row: one where the rows alone give every compute unit two
-// workgroups, else as many as bring it there, each with at least kLeastPart elements.
-constexpr int kLeastPart = 4096;
+// Long rows are split over workgroups where there are fewer rows than compute units, into
+// parts of at least kLeastPart elements: one compute unit takes 22 us over a row of 131072 (its
+// arithmetic), 32 of them and the join 13. Below kLeastRow the join costs what it saves.
+constexpr int kLeastPart = 4096, kLeastRow = 65536;
 RowSplit split_rows(int M, int V, int top, int cus)
 {
     RowSplit r{1, V, 0};
-    const int want = std::min(ceil_div(2 * cus, M), ceil_div(V, kLeastPart));
-    if (M < 2 * cus && want > 1) {
+    if (M < cus && V >= kLeastRow) {
+        const int want = std::min(ceil_div(2 * cus, M), V / kLeastPart);
         r.part_len = (ceil_div(V, want) + 7) / 8 * 8;
         r.splits = ceil_div(V, r.part_len);
     }
@@ -43,9 +44,20 @@ size_t split_bytes(const RowSplit &r, int M)
 }
 
 typedef void (*RowKernel)(RowArgs);
-template <int DT> RowKernel pass_kernel(bool top)
+struct RowLaunch {
+    RowKernel kernel;
+    int threads;
+};
+// Workgroups of more threads for fewer and longer rows, so that enough loads are in flight.
+template <int DT, bool TOP> RowLaunch pass_of(int64_t groups, int len, int cus)
 {
-    return top ? &k_row_pass<DT, true> : &k_row_pass<DT, false>;
+    if (groups <= cus && len >= 32768) return {&k_row_pass<DT, TOP, 1024, 4>, 1024};
+    if (groups <= 4 * cus && len >= 8192) return {&k_row_pass<DT, TOP, 512, 4>, 512};
+    return {&k_row_pass<DT, TOP, 256, 4>, 256};
+}
+template <int DT> RowLaunch pass_kernel(bool top, int64_t groups, int len, int cus)
+{
+    return top ? pass_of<DT, true>(groups, len, cus) : pass_of<DT, false>(groups, len, cus);
 }
 template <int DT> RowKernel join_kernel(bool top)
 {
@@ -112,17 +124,22 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
     p.top_logprobs = top_logprobs; p.top_tokens = top_tokens;
     p.parts = static_cast<char *>(workspace); p.part_bytes = r.part_bytes;
     p.M = M; p.V = V; p.top = top; p.splits = r.splits; p.part_len = r.part_len;
-    RowKernel pass, join;
+    const int64_t groups = int64_t(M) * r.splits;
+    RowLaunch pass;
+    RowKernel join;
     if (dtype == SGEMM_DTYPE_F32) {
-        pass = pass_kernel<SGEMM_DTYPE_F32>(top > 0); join = join_kernel<SGEMM_DTYPE_F32>(top > 0);
+        pass = pass_kernel<SGEMM_DTYPE_F32>(top > 0, groups, r.part_len, cus);
+        join = join_kernel<SGEMM_DTYPE_F32>(top > 0);
     } else if (dtype == SGEMM_DTYPE_BF16) {
-        pass = pass_kernel<SGEMM_DTYPE_BF16>(top > 0); join = join_kernel<SGEMM_DTYPE_BF16>(top > 0);
+        pass = pass_kernel<SGEMM_DTYPE_BF16>(top > 0, groups, r.part_len, cus);
+        join = join_kernel<SGEMM_DTYPE_BF16>(top > 0);
     } else {
-        pass = pass_kernel<SGEMM_DTYPE_F16>(top > 0); join = join_kernel<SGEMM_DTYPE_F16>(top > 0);
+        pass = pass_kernel<SGEMM_DTYPE_F16>(top > 0, groups, r.part_len, cus);
+        join = join_kernel<SGEMM_DTYPE_F16>(top > 0);
     }
-    st = launch(pass, dim3(unsigned(M * int64_t(r.splits))), dim3(kRowThreads), stream, p);
+    st = launch(pass.kernel, dim3(unsigned(groups)), dim3(pass.threads), stream, p);
     if (st != SGEMM_OK || r.splits == 1) return st;
-    return launch(join, dim3(unsigned(M)), dim3(kRowThreads), stream, p);
+    return launch(join, dim3(unsigned(M)), dim3(256), stream, p);
 }
 
 extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dtype, int64_t ld,
@@ -161,5 +178,5 @@ extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dty
     auto kern = dtype == SGEMM_DTYPE_F32    ? &k_row_gradient<SGEMM_DTYPE_F32>
                 : dtype == SGEMM_DTYPE_BF16 ? &k_row_gradient<SGEMM_DTYPE_BF16>
                                             : &k_row_gradient<SGEMM_DTYPE_F16>;
-    return launch(kern, dim3(unsigned(M * int64_t(p.parts))), dim3(kRowThreads), stream, p);
+    return launch(kern, dim3(unsigned(M * int64_t(p.parts))), dim3(kGradThreads), stream, p);
 }

@@ -96,7 +96,7 @@ def logits(torch, host, dt, pad=0, offset=0):
 @pytest.mark.parametrize("M,V,top", [(1, 1, 1), (1, 2, 0), (3, 5, 5), (2, 64, 64), (4, 65, 3),
                                      (7, 1000, 20), (1, 4097, 1), (2, 16384, 64), (1, 131072, 20),
                                      (1, 100003, 5), (5, 32001, 0), (600, 1003, 2), (1030, 300, 7),
-                                     (3, 250000, 33)])
+                                     (3, 250000, 33), (2, 1000003, 20), (300, 2500, 4)])
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (5, 3)])
 def test_logprobs(torch, M, V, top, dt, pad, offset):
@@ -109,7 +109,7 @@ def test_logprobs(torch, M, V, top, dt, pad, offset):
     check(r, x, tokens, top)
 
 
-@pytest.mark.parametrize("V", [3, 700, 9000, 40000])
+@pytest.mark.parametrize("V", [3, 700, 9000, 40000, 300000])
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("many", [False, True])
 def test_edge_rows(torch, V, dt, many):
@@ -117,6 +117,8 @@ def test_edge_rows(torch, V, dt, many):
     workgroups where V allows) and many."""
     rng = np.random.default_rng(V)
     top = min(V, 20)
+    if many and V > 100000:
+        pytest.skip("long rows are few")
     rows = [np.full(V, -np.inf), np.zeros(V), np.linspace(-5, 5, V), np.linspace(5, -5, V),
             np.where(np.arange(V) % 7 == 0, 1.0, -np.inf), np.full(V, 60000.0), np.full(V, -60000.0),
             np.where(np.arange(V) == V - 1, 3.0, -np.inf),
@@ -171,7 +173,7 @@ def test_no_rows_and_refusals(torch):
 def test_split_and_unsplit_agree(torch):
     """Without a workspace a row is not split: the alternatives are the same, the sums the
     same to their rounding; a workspace that is too small is refused. Repeats are identical."""
-    M, V, top = 2, 60000, 9
+    M, V, top = 2, 600001, 9
     assert g.token_logprobs_workspace_size(M, V, 0, top) > 0
     x = torch.randn(M, V, device="cuda")
     tok = torch.tensor([5, -1], device="cuda")
@@ -193,6 +195,33 @@ def test_split_and_unsplit_agree(torch):
     # entropy and lse may be left out
     g.token_logprobs_raw(M, V, x.data_ptr(), 0, V, tok.data_ptr(), 8, lp.data_ptr(), 0, 0)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("V", [50001, 131072, 700001])
+@pytest.mark.parametrize("top", [1, 5, 64])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rows_that_crowd_the_alternatives(torch, V, top, dt):
+    """Unsplit rows (no workspace) in which the largest values lie in few threads' share of the
+    row, rise along it, or are nearly all equal: the candidates' list is cut on the way."""
+    j = np.arange(V)
+    chunk = j // (4 if dt == "f32" else 8)
+    rows = [-(chunk % 256) + chunk / 4096.0, -(chunk % 256) * 2.0 - chunk / 2048.0,
+            np.where(chunk % 256 < 3, np.round(j / 997.0), -5.0), j / float(V), -j / float(V),
+            np.where(j % 2048 < 16, 1.0, 0.0), np.where(j < V - 3, -np.inf, 2.0),
+            np.where(chunk % 256 == 255, 7.0, np.where(j % 3 == 0, np.nan, -np.inf))]
+    d, x = logits(torch, np.stack(rows), dt)
+    M = len(rows)
+    tok = torch.full((M,), -1, device="cuda")
+    lp, ent, lse = (torch.empty(M, device="cuda") for _ in range(3))
+    tv = torch.empty(M, top, device="cuda")
+    ti = torch.empty(M, top, dtype=torch.int64, device="cuda")
+    print(f"[logprobs crowded] {V} top {top} {dt}", flush=True)
+    g.token_logprobs_raw(M, V, d.data_ptr(), 0 if dt == "f32" else 1, V, tok.data_ptr(), 8, lp.data_ptr(),
+                         ent.data_ptr(), lse.data_ptr(), top, tv.data_ptr(), ti.data_ptr(),
+                         stream=torch.cuda.current_stream().cuda_stream)
+    np.testing.assert_array_equal(ti.cpu().numpy(), ranked(x, top))
+    r = g.token_logprobs(d, tok, top=top)              # and split over workgroups
+    assert torch.equal(r.top_tokens, ti)
 
 
 def gradient_reference(x, tokens, lse, h, gl, gh, gs):
@@ -318,7 +347,7 @@ def test_autograd_paths(torch):
     check(g.token_logprobs(t, tok), t.double().cpu().numpy(), tok.cpu().numpy(), 0)
 
 
-@pytest.mark.parametrize("M,V,top", [(2, 60000, 9), (600, 3001, 3)])
+@pytest.mark.parametrize("M,V,top", [(2, 600001, 9), (600, 3001, 3)])
 def test_graph_capture_and_other_stream(torch, M, V, top):
     x = torch.randn(M, V, device="cuda")
     tok = torch.randint(0, V, (M,), device="cuda")
