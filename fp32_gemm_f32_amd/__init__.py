@@ -387,6 +387,25 @@ def matmul(A, B, out=None, kernel: str = "auto", variant: int = -1, tile=32, pad
 
 # ------------------------------------------------------- 8-bit product, token log-probabilities
 
+_calls = None
+
+
+def _load_calls():
+    """The extension module that makes the tensor layer's ordinary calls (csrc/torch_calls.cpp);
+    each of its functions returns None where the checks below have to decide."""
+    global _calls
+    if _calls is None:
+        library()
+        import torch  # noqa: F401  (the extension links against its libraries)
+        try:
+            from . import _torch_calls
+        except ImportError as e:
+            raise RuntimeError("the extension _torch_calls is not built or does not load; run "
+                               "`python -m fp32_gemm_f32_amd.build`") from e
+        _calls = _torch_calls
+    return _calls
+
+
 class TokenLogprobs(NamedTuple):
     """What token_logprobs returns for M rows: logprobs, entropy and lse are (M,) float32;
     top_logprobs (M, top) float32 and top_tokens (M, top) int64, or None with top = 0."""
@@ -424,7 +443,7 @@ def _vector(t, n: int, dtype, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    return t if t.is_contiguous() else t.contiguous()
+    return t.resolve_neg().contiguous()
 
 
 def _rows(t, name: str):
@@ -435,8 +454,8 @@ def _rows(t, name: str):
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {t.dim()}-D")
     rows, cols = t.shape
-    if (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        return t.contiguous()
+    if t.is_neg() or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        return t.resolve_neg().contiguous()
     return t
 
 
@@ -482,6 +501,10 @@ def quantize_rows(X, out=None, scales=None):
     is about Q * scales[:, None]. X is float32, bfloat16 or float16; a row is a token of
     activations or an output channel of weights. The integers are defined to the bit
     (gemm_i8.h). No gradient flows through it."""
+    if out is None and scales is None:
+        done = (_calls or _load_calls()).quantize_rows(X)
+        if done is not None:
+            return done
     import torch
 
     code = _dtype_code(X.dtype)
@@ -505,6 +528,11 @@ def matmul_i8(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
     operands off the alignment the kernels load) is a torch allocation made here. No gradient flows through it."""
     import torch
 
+    if out is None:
+        done = (_calls or _load_calls()).matmul_i8(A, a_scales, B, b_scales, bias,
+                                                   0 if out_dtype is None else _dtype_code(out_dtype))
+        if done is not None:
+            return done
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be int8")
     A, B = _rows(A, "A"), _rows(B, "B")
@@ -535,9 +563,9 @@ def linear_i8(X, B, b_scales, bias=None, out_dtype=None):
     """quantize_rows(X), then its product with the 8-bit weights B (N, K) of scales b_scales:
     a projection of activations X (..., K) in 8 bits. The result has X's type unless
     out_dtype says otherwise."""
-    q, scales = quantize_rows(X.reshape(-1, X.shape[-1]))
+    q, scales = quantize_rows(X if X.dim() == 2 else X.reshape(-1, X.shape[-1]))
     C = matmul_i8(q, scales, B, b_scales, bias=bias, out_dtype=out_dtype or X.dtype)
-    return C.view(*X.shape[:-1], B.shape[0])
+    return C if X.dim() == 2 else C.view(*X.shape[:-1], B.shape[0])
 
 
 def _tokens(tokens, M: int, device):
@@ -550,6 +578,9 @@ def _tokens(tokens, M: int, device):
 
 
 def _logprobs_forward(logits, tokens, top: int):
+    done = (_calls or _load_calls()).token_logprobs(logits, tokens, top)
+    if done is not None:
+        return done
     import torch
 
     code = _dtype_code(logits.dtype)
@@ -583,6 +614,12 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_en
     entropy that token_logprobs returned for these logits; a gradient that is None counts as
     zeros (entropy may be None where grad_entropy is). out may be logits itself: the gradient
     then takes its place."""
+    if out is None:
+        done = (_calls or _load_calls()).token_logprobs_backward(logits, tokens, lse, entropy,
+                                                                 grad_logprobs, grad_entropy,
+                                                                 grad_lse)
+        if done is not None:
+            return done
     import torch
 
     code = _dtype_code(logits.dtype)

@@ -1,4 +1,5 @@
-"""Build the HIP library libsgemm_f32.so in-tree for gfx950 with hipcc.
+"""Build the HIP library libsgemm_f32.so in-tree for gfx950 with hipcc, and the host extension
+_torch_calls.so that the tensor layer calls it through.
 
     python -m fp32_gemm_f32_amd.build           # build
     python -m fp32_gemm_f32_amd.build --asm     # also write the gfx950 assembly
@@ -84,9 +85,34 @@ def build(asm: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc link failed ({r.returncode})")
     check_symbols(OUT + ".tmp")
     os.replace(OUT + ".tmp", OUT)
+    build_calls(verbose)
     if asm:
         assemble()
     return OUT
+
+
+def build_calls(verbose: bool = False) -> str:
+    """Build the extension module _torch_calls (host code) against the library and torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    out = os.path.join(PKG, "_torch_calls.so")
+    includes = [INCLUDE, *include_paths(), "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{i}" for i in includes), os.path.join(CSRC, "torch_calls.cpp"), "-o", out + ".tmp",
+           *(f"-L{l}" for l in library_paths()), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_hip",
+           "-lc10", "-lc10_hip", f"-L{PKG}", f"-l:{os.path.basename(OUT)}", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stderr[-8000:])
+        raise RuntimeError(f"g++ failed ({r.returncode}) on torch_calls.cpp")
+    os.replace(out + ".tmp", out)
+    return out
 
 
 def check_symbols(lib: str) -> None:
