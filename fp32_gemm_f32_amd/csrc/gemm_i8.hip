@@ -87,9 +87,9 @@ double tile_cost(const I8Variant &v, int64_t groups, int64_t panels, int cus)
 }
 
 // The cheapest of: every tile, K whole or split; rows as they are, in the slower form for any
-// alignment, or copied into place first. That form costs about half again as much (measured
-// at 8192^3 661 against 464 us, 1023x1025x1027 12.3 against 6.9, 128x8192^2 40 against 26); the
-// copy costs a launch and its traffic, and the workspace.
+// alignment, or copied into place first. That form costs a quarter to a half more (measured at
+// 8192^3 598 against 482 us, 1023x1025x1027 10.4 against 6.9 for 1024^3, 128x8192^2 38 against
+// 26); the copy costs a launch and its traffic, and the workspace.
 I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
 {
     I8Plan best{};
@@ -114,8 +114,10 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             const int64_t groups = ceil_div(N, bn) * s;
-            const double step = double(ceil_div(groups, 2 * cus)) * double(ceil_div(chunk, 2048)) * 0.7;
-            const double cost = kLaunch + std::max(step, bytes / kBytesPerUs) * (any ? 1.25 : 1.0) +
+            // a panel of every wave takes this long when little else is in flight
+            const double turn = any ? double(ceil_div(chunk, 1024)) * 1.4 : double(ceil_div(chunk, 2048)) * 0.8;
+            const double step = double(ceil_div(groups, 2 * cus)) * turn;
+            const double cost = kLaunch + std::max(step, bytes / kBytesPerUs * (any ? 1.25 : 1.0)) +
                                 join_cost(s);
             offer({&kFewRows, any ? kFewRows.any : kFewRows.aligned, 16, bn, 1,
                    int(ceil_div(N, bn)), s, chunk, false, false, cost});
@@ -130,7 +132,8 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
             const double body = std::max(tile_cost(v, tm * tn * s, ceil_div(chunk, 128), cus),
                                          bytes / kBytesPerUs);
             I8Plan p{&v, any ? v.any : v.aligned, v.bm, v.bn, int(tm), int(tn), s, chunk,
-                     false, false, kLaunch + body * (any ? 1.5 : 1.0) + join_cost(s)};
+                     false, false, kLaunch + body + (any ? 0.25 * body + 0.08 * double(ceil_div(chunk, 128)) : 0.0) +
+                         join_cost(s)};
             offer(p);
             if (any && workspace) {
                 p.kernel = v.aligned;

@@ -78,9 +78,9 @@ __device__ inline void i8_store_as(int dtype, void *C, int64_t at, const float (
 //    the tile's rows or past K read as zero through an offset out of range. That needs rows
 //    on word boundaries and K a multiple of 16.
 //  * ANY takes rows at any address and any K. Loads start at the word that holds a row's
-//    first byte, so a row lies in LDS off its place by its address's low two bits, with one
-//    word more behind its last chunk. An operand is read with the word behind it and moved
-//    into place (join_words) before it is multiplied. In the panel that holds K's end A's
+//    first byte, so a row lies in LDS off its place by its address's low two bits. An operand
+//    is read with the word behind it, which may be the next panel's first, and moved into
+//    place (join_words) before it is multiplied. In the panel that holds K's end A's
 //    values past it are zeroed there, so B's do not count. Words are loaded only where one
 //    of their bytes may be the matrix's (the resource ends with its last row).
 template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Tile {
@@ -92,10 +92,8 @@ template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Til
     static constexpr int STEPS = BK / 32;            // MFMA steps per panel
     static constexpr int ACH = BM * CPR / NT, BCH = BN * CPR / NT;   // chunks per thread
     static constexpr int A_BYTES = BM * BK, STAGE = (BM + BN) * BK;
-    static constexpr int NCH = (BM + BN + NT - 1) / NT, NEXT_BYTES = NCH * NT * 4;
     static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
     static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
-    static_assert(STEPS % 2 == 0, "operand buffers alternate over whole panels");
 };
 
 // Global row of B (within the tile) at LDS row p.
@@ -213,26 +211,19 @@ __device__ inline uint32_t i8_range(const int8_t *from, const int8_t *end)
     return n <= 0 ? 0u : n >= int64_t(kFullRange) ? kFullRange : (uint32_t(n) + 3u) & ~3u;
 }
 
-// 16 (or 4) bytes a lane from base + off, zeros where that is past `range`, to LDS at `to` plus
-// as many bytes times the lane.
+// 16 bytes a lane from base + off, zeros where that is past `range`, to LDS at `to` + 16 lanes.
 typedef __attribute__((address_space(3))) void *lds_ptr;
 __device__ __forceinline__ void i8_load16_lds(const int8_t *base, uint32_t range, uint32_t off, char *to)
 {
     const auto rsrc = make_rsrc32(reinterpret_cast<const float *>(base), range);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 16, off, 0, 0, 0);
 }
-__device__ __forceinline__ void i8_load4_lds(const int8_t *base, uint32_t range, uint32_t off, char *to)
-{
-    const auto rsrc = make_rsrc32(reinterpret_cast<const float *>(base), range);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 4, off, 0, 0, 0);
-}
 
 template <typename T, bool ANY>
 __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
 {
-    constexpr int STAGE = T::STAGE + (ANY ? T::NEXT_BYTES : 0);
+    constexpr int STAGE = T::STAGE;
     static_assert(T::NSTG >= 2 && T::NSTG * STAGE <= 160 * 1024, "LDS");
-    static_assert(!ANY || T::BM % 64 == 0, "a wave's rows of next words are of one matrix");
     __shared__ __attribute__((aligned(16))) char smem[T::NSTG * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -255,7 +246,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     // this thread's chunks: LDS chunk i * NT + tid
     const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
     const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
-    uint32_t a_off[T::ACH], b_off[T::BCH], n_off[T::NCH];
+    uint32_t a_off[T::ACH], b_off[T::BCH];
 #pragma unroll
     for (int i = 0; i < T::ACH; ++i) {
         const int r = prow + i * (T::NT / T::CPR);
@@ -266,29 +257,23 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
         const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
         b_off[i] = n0 + r < p.N ? (b_low + uint32_t(r * p.ldb) + q * 16) & ~3u : kOob;
     }
-    // ANY: the word past a panel's last chunk of LDS row i * NT + tid (A's rows, then B's)
-#pragma unroll
-    for (int i = 0; i < T::NCH; ++i) {
-        const int e = i * T::NT + tid;
-        const int r = e < T::BM ? e : i8_b_row<T>(e - T::BM);
-        n_off[i] = e < T::BM ? (m0 + r < p.M ? (a_low + uint32_t(r * p.lda) + T::BK) & ~3u : kOob)
-                 : e < T::BM + T::BN && n0 + r < p.N
-                     ? (b_low + uint32_t(r * p.ldb) + T::BK) & ~3u : kOob;
-    }
-
     i32x16 acc[T::RB][T::CB];
 #pragma unroll
     for (int i = 0; i < T::RB; ++i)
 #pragma unroll
         for (int j = 0; j < T::CB; ++j) acc[i][j] = i32x16(0);
 
-    // operand reads: row l % 32 of a block, chunk 2 t + l / 32
+    // operand reads: row l % 32 of a block; chunk 2 t + l / 32 at step t, with ANY t + STEPS (l / 32),
+    // so that the word behind a lane's chunk is the first of its own next one (any order of k
+    // does that is the same on both sides)
     const int frow = lane & 31, fhi = lane >> 5;
     const int fsw = a_swizzle<T::CPR>(frow);
     const int a_row = wm * T::WM + frow, b_row = wn * T::WN + frow;
     const int a_base = a_row * T::BK, b_base = T::A_BYTES + b_row * T::BK;
-    i32x4 fa[2][T::RB], fb[2][T::CB];
-    int na[2][T::RB], nb[2][T::CB];                  // ANY: the words behind the chunks
+    i32x4 fa[T::STEPS][T::RB], fb[T::STEPS][T::CB];
+    // ANY: the words behind the last step's chunks: of lanes below 32 the panel's chunk STEPS, of
+    // the others the next panel's first
+    int na[2][T::RB], nb[2][T::CB];
     uint32_t a_shift[T::RB], b_shift[T::CB];
     if constexpr (ANY) {
 #pragma unroll
@@ -297,53 +282,44 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
         for (int j = 0; j < T::CB; ++j)
             b_shift[j] = b_low + uint32_t(i8_b_row<T>(b_row + 32 * j)) * uint32_t(p.ldb);
     }
-    // of a panel's last chunk the word behind lies past the rows, one to a row
-    const int a_last = fhi ? T::STAGE + a_row * 4 : a_base + (((T::CPR - 1) ^ fsw) * 16);
-    const int b_last = fhi ? T::STAGE + (T::BM + b_row) * 4 : b_base + (((T::CPR - 1) ^ fsw) * 16);
-    const int last_step = fhi ? 32 * 4 : 32 * T::BK;
-    auto read = [&](const char *st, auto tc, int buf) __attribute__((always_inline)) {
+    auto read = [&](const char *st, auto tc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value;
-        const int at = ((2 * t + fhi) ^ fsw) * 16;
+        const int at = ((ANY ? t + T::STEPS * fhi : 2 * t + fhi) ^ fsw) * 16;
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
-            fa[buf][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
+            fa[t][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
 #pragma unroll
         for (int j = 0; j < T::CB; ++j)
-            fb[buf][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
-        if constexpr (ANY && t < T::STEPS - 1) {
-            const int next = ((2 * t + fhi + 1) ^ fsw) * 16;
+            fb[t][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
+        if constexpr (ANY && (t == T::STEPS - 1 || t == 0)) {
+            const int behind = ((t == 0 ? 0 : T::STEPS) ^ fsw) * 16;
+            constexpr int of = t == 0 ? 1 : 0;
 #pragma unroll
             for (int i = 0; i < T::RB; ++i)
-                na[buf][i] = *reinterpret_cast<const int *>(st + a_base + next + i * 32 * T::BK);
+                na[of][i] = *reinterpret_cast<const int *>(st + a_base + behind + i * 32 * T::BK);
 #pragma unroll
             for (int j = 0; j < T::CB; ++j)
-                nb[buf][j] = *reinterpret_cast<const int *>(st + b_base + next + j * 32 * T::BK);
-        } else if constexpr (ANY) {
-#pragma unroll
-            for (int i = 0; i < T::RB; ++i)
-                na[buf][i] = *reinterpret_cast<const int *>(st + a_last + i * last_step);
-#pragma unroll
-            for (int j = 0; j < T::CB; ++j)
-                nb[buf][j] = *reinterpret_cast<const int *>(st + b_last + j * last_step);
+                nb[of][j] = *reinterpret_cast<const int *>(st + b_base + behind + j * 32 * T::BK);
         }
     };
     // MASK: values of k from `left` on (of this lane's chunk) count as zero
-    auto multiply = [&](int buf, auto mask, int left) __attribute__((always_inline)) {
+    auto multiply = [&](auto tc, auto mask, int left) __attribute__((always_inline)) {
+        constexpr int t = decltype(tc)::value, u = t + 1 < T::STEPS ? t + 1 : t;
         if constexpr (ANY) {
 #pragma unroll
             for (int i = 0; i < T::RB; ++i) {
-                fa[buf][i] = join_words({fa[buf][i], na[buf][i]}, a_shift[i]);
-                if constexpr (decltype(mask)::value) fa[buf][i] = keep_bytes(fa[buf][i], left);
+                fa[t][i] = join_words({fa[t][i], u > t ? fa[u][i][0] : fhi ? na[1][i] : na[0][i]}, a_shift[i]);
+                if constexpr (decltype(mask)::value) fa[t][i] = keep_bytes(fa[t][i], left);
             }
 #pragma unroll
-            for (int j = 0; j < T::CB; ++j) fb[buf][j] = join_words({fb[buf][j], nb[buf][j]}, b_shift[j]);
+            for (int j = 0; j < T::CB; ++j)
+                fb[t][j] = join_words({fb[t][j], u > t ? fb[u][j][0] : fhi ? nb[1][j] : nb[0][j]}, b_shift[j]);
         }
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
 #pragma unroll
             for (int j = 0; j < T::CB; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[buf][i], fb[buf][j],
-                                                                  acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[t][i], fb[t][j], acc[i][j], 0, 0, 0);
     };
 
     const int8_t *const a_end = p.A + (p.M - 1) * p.lda + p.K, *const b_end = p.B + (p.N - 1) * p.ldb + p.K;
@@ -362,55 +338,46 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
 #pragma unroll
         for (int i = 0; i < T::BCH; ++i)
             i8_load16_lds(bk, bn, b_off[i] | past, st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
-        if constexpr (ANY) {
-            const uint32_t none = k >= kn ? kOob : 0u;
-#pragma unroll
-            for (int i = 0; i < T::NCH; ++i) {
-                // a wave's 64 rows are all A's or all B's
-                const bool of_a = i * T::NT + wave * 64 < T::BM;
-                i8_load4_lds(of_a ? ak : bk, of_a ? an : bn, n_off[i] | none,
-                               st + T::STAGE + (i * T::NT + wave * 64) * 4);
-            }
-        }
     };
-    // The step before a panel's last ends the reads of its stage, so the barrier comes there:
-    // the wave's loads of the next panel have landed, every wave's have after the barrier, and
-    // the stage just read is loaded again and the next one's first operands are read under the
-    // last step's MFMAs.
-    constexpr int LPP = T::ACH + T::BCH + (ANY ? T::NCH : 0);
-    typedef std::integral_constant<int, 0> First;
+    // Operands are read LOOK steps ahead. LOOK steps before a panel's end the reads of its stage
+    // are over, so the barrier comes there: the wave's loads of the next panel have landed, every
+    // wave's have after the barrier, and the stage just read is loaded again and the next one's
+    // first operands are read under the last steps' MFMAs.
+    constexpr int LPP = T::ACH + T::BCH;
+    constexpr int LOOK = ANY ? 2 : 1;
 #pragma unroll
     for (int i = 0; i < T::NSTG; ++i) issue(i);
     wait_vmcnt<(T::NSTG - 1) * LPP>();
     asm volatile("s_barrier" ::: "memory");
-    read(smem, First{}, 0);
+    static_for<0, LOOK>([&](auto tc) __attribute__((always_inline)) { read(smem, tc); });
     int stage = 0;
     const int full = ANY ? kn / T::BK : panels;      // panels without a masked step
     auto run = [&](int panel, auto mask) __attribute__((always_inline)) {
         const char *st = smem + stage * STAGE;
         stage = stage + 1 == T::NSTG ? 0 : stage + 1;
+        const char *next = smem + stage * STAGE;
         static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
             constexpr int t = decltype(tc)::value;
-            constexpr bool last = t == T::STEPS - 1;
-            if constexpr (!last) {
-                read(st, std::integral_constant<int, t + 1>{}, (t + 1) & 1);
-            } else {
+            constexpr bool turn = t == T::STEPS - LOOK;
+            if constexpr (turn) {
                 __builtin_amdgcn_sched_barrier(0);
                 wait_vmcnt<(T::NSTG - 2) * LPP>();
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                read(smem + stage * STAGE, First{}, (t + 1) & 1);
-                issue(panel + T::NSTG);
             }
-            multiply(t & 1, mask, kn - panel * T::BK - 16 * (2 * t + fhi));
+            if constexpr (t + LOOK < T::STEPS) read(st, std::integral_constant<int, t + LOOK>{});
+            else read(next, std::integral_constant<int, t + LOOK - T::STEPS>{});
+            if constexpr (turn) issue(panel + T::NSTG);
+            multiply(tc, mask, kn - panel * T::BK - 16 * (ANY ? t + T::STEPS * fhi : 2 * t + fhi));
             // operand reads behind the first MFMAs, the loads behind the others
-            constexpr int ops = (T::RB + T::CB) * (ANY ? 2 : 1), mf = T::RB * T::CB;
-            constexpr int rm = last ? (mf + 1) / 2 : (ops < mf ? ops : mf);
+            constexpr int ops = (T::RB + T::CB) * (ANY && (t + LOOK) % T::STEPS % (T::STEPS - 1) == 0 ? 2 : 1);
+            constexpr int mf = T::RB * T::CB;
+            constexpr int rm = turn ? (mf + 1) / 2 : (ops < mf ? ops : mf);
             constexpr int lm = mf - rm > 0 ? mf - rm : 1;
             static_for<0, mf>([&](auto mc) __attribute__((always_inline)) {
                 constexpr int m = decltype(mc)::value;
                 constexpr int r = m < rm ? (m + 1) * ops / rm - m * ops / rm : 0;
                 constexpr int n = m - (mf - lm);
-                constexpr int l = last && n >= 0 ? (n + 1) * LPP / lm - n * LPP / lm : 0;
+                constexpr int l = turn && n >= 0 ? (n + 1) * LPP / lm - n * LPP / lm : 0;
                 __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
                 if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, r, 0);
                 if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
