@@ -101,55 +101,67 @@ __device__ inline float key_value(uint64_t key)
 }
 __device__ inline uint32_t key_index(uint64_t key) { return 0xffffffffu - uint32_t(key); }
 
+__device__ inline uint64_t lane_key(uint64_t key, int lane)
+{
+    const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(key), lane);
+    const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(key >> 32), lane);
+    return uint64_t(hi) << 32 | lo;
+}
+
 // The `top` largest of many keys, by a bound and a short list of candidates.
 //  * The elements lie in groups of neighbours (a chunk of one load); each thread knows the
 //    best key of its groups, key_of(largest value, first index of the first group that holds
 //    it). Of two groups' keys the larger belongs to the group whose best element is larger.
-//  * bound(): a wave takes the n-th largest of its threads' bests, n = ceil(top / waves); the
-//    smallest of those is T. At least `top` threads hold a group whose key is T or more, so
-//    elements of a group below T, and elements below T's value or equal to it behind its
-//    group, are not among the top ones.
-//  * The threads whose best reaches T (about `top` of them) have their elements looked at
-//    again, by all threads in turn, and the elements that reach T become candidates. With
-//    the keys in no order there are little more than `top`; each is ranked against all.
-//    Rows made to defeat the bound bring more: the list is cut to the `top` best whenever it
-//    could overflow, and T rises to the last of them.
+//  * top_bound(): the threads' bests are joined to 64, and T is the top-th largest of those:
+//    exact for top = 1, about 24 elements reach it for top = 20. At least `top` threads hold a
+//    group whose key is T or more, so elements of a group below T, and elements below T's value
+//    or equal to it behind its group, are not among the top ones.
+//  * The elements of the threads whose best reaches T become candidates where they reach it
+//    themselves: from registers where the row fits them, else looked at again, by all threads
+//    in turn. With the keys in no order there are little more than `top`; each is ranked
+//    against all. Rows made to defeat the bound bring more: the list is cut to the `top` best
+//    whenever it could overflow, and T rises to the last of them.
+// All of this runs once a row, behind the pass, so latency is what counts: 1 x 131072 f32 with 20
+// alternatives takes 9.4 us in both kernels (9.0 with the selections left out), 600 x 50001 bf16
+// with 5 takes 21.0 (15.6 without). Candidates kept on the way, above a T of the row's first
+// elements, save the second look, but the wait for that T costs more wherever rows share a
+// compute unit (1200 x 32000 bf16, 20: 38 us instead of 23.6). Ranking 64 keys in one wave costs
+// 1.7 us a row, shared among the waves 0.7.
 constexpr int kCandidates = 1024, kNarrow = 64;
 template <int NT> struct TopShared {
-    uint64_t best[NT];
+    uint64_t best[NT], joined[NT];
     uint64_t cand[kCandidates], kept[64];
-    uint64_t least[NT / 64];
-    int threads[NT];
+    int ranks[NT], threads[NT];
     int n_threads, n_cand;
 };
 
-// T, and the threads that reach it in sh.threads. best is 0 for a thread without elements.
+// T, 0 where fewer than `top` of the 64 joined threads have elements. best is 0 for a thread
+// without. Every wave joins all of them and compares them with its share of them.
 template <int NT>
 __device__ inline uint64_t top_bound(TopShared<NT> &sh, uint64_t best, int top)
 {
-    constexpr int WAVES = NT / 64;
-    const int tid = threadIdx.x, wave = tid >> 6;
+    constexpr int WAVES = NT / 64, SHARE = 64 / WAVES;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     sh.best[tid] = best;
-    if (tid == 0) { sh.n_threads = 0; sh.n_cand = 0; }
     __syncthreads();
-    int rank = 0;
-#pragma unroll 8
-    for (int u = 0; u < 64; ++u) rank += sh.best[wave * 64 + u] > best;
-    // equal keys are all 0: then the bound is 0 if the rank lies among them
-    const int want = (top + WAVES - 1) / WAVES - 1;
-    const uint64_t hit = __ballot(rank == want);
-    if (hit == 0) {
-        if ((tid & 63) == 0) sh.least[wave] = 0;
-    } else if (rank == want) {
-        sh.least[wave] = best;
-    }
-    __syncthreads();
-    uint64_t t = sh.least[0];
+    uint64_t k = sh.best[lane];
 #pragma unroll
-    for (int w = 1; w < WAVES; ++w) t = min(t, sh.least[w]);
-    if (best != 0 && best >= t) sh.threads[atomicAdd(&sh.n_threads, 1)] = tid;
+    for (int w = 1; w < WAVES; ++w) k = max(k, sh.best[w * 64 + lane]);
+    sh.joined[tid] = k;
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t *others = sh.joined + wave * 64 + wave * SHARE;
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < SHARE; ++j) rank += others[j] > k;
+    sh.ranks[tid] = rank;
     __syncthreads();
-    return t;
+    rank = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) rank += sh.ranks[w * 64 + lane];
+    // keys but 0 are distinct; with fewer than `top` of them none has this rank, or a 0 has
+    const uint64_t at = __ballot(rank == top - 1);
+    return at == 0 ? 0 : lane_key(k, __builtin_ctzll(at));
 }
 
 // Ranks the candidates; fn(rank, key) for those among the top.
@@ -165,10 +177,67 @@ __device__ inline void rank_candidates(const TopShared<NT> &sh, int n, int top, 
     }
 }
 
-template <int NT> __device__ inline void add_candidate(TopShared<NT> &sh, uint64_t key)
+template <int NT> __device__ inline void add_candidate(TopShared<NT> &sh, uint64_t key, uint64_t floor)
 {
-    const int at = atomicAdd(&sh.n_cand, 1);
-    if (at < kCandidates) sh.cand[at] = key;
+    if (key < floor) return;
+    const int to = atomicAdd(&sh.n_cand, 1);
+    if (to < kCandidates) sh.cand[to] = key;
+}
+
+// The elements of chunks b[u], u < U, that reach floor join the candidates; at(i) is the index of
+// element i of them, `there` has a bit for each that exists. The few that do are taken one
+// after another, picked from the registers: code that runs once a row is short, for its
+// instructions come from memory.
+template <int DT, int NT, int U, int W, typename At>
+__device__ inline void add_candidates(TopShared<NT> &sh, const Pack<typename Elem<DT>::type, W> (&b)[U],
+                                      uint32_t there, uint64_t floor, At at)
+{
+    typedef typename Elem<DT>::type T;
+    const float least = key_value(floor);          // not a number where NaNs reach it
+    uint32_t hits = 0;
+#pragma unroll
+    for (int i = 0; i < U * W; ++i)
+        hits |= Elem<DT>::widen(b[i / W].v[i % W]) < least ? 0u : 1u << i;
+    hits &= there;
+    while (hits != 0) {
+        const int i = __builtin_ctz(hits);
+        hits &= hits - 1;
+        T x = b[0].v[0];
+#pragma unroll
+        for (int k = 1; k < U * W; ++k) x = i == k ? b[k / W].v[k % W] : x;
+        add_candidate(sh, key_of(Elem<DT>::widen(x), uint32_t(at(i))), floor);
+    }
+}
+
+// The top of the n <= kCandidates candidates, all of them in the list behind a barrier.
+template <int NT, typename Emit>
+__device__ inline void rank_top(TopShared<NT> &sh, int n, int top, Emit emit)
+{
+    if (n > 96) {                              // cut the list first: ranking takes n^2
+        constexpr int EACH = (kCandidates + NT - 1) / NT;
+        uint64_t mine[EACH], best = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int at = i * NT + int(threadIdx.x);
+            mine[i] = at < n ? sh.cand[at] : 0;
+            best = max(best, mine[i]);
+        }
+        const uint64_t t = top_bound(sh, best, top);
+        if (threadIdx.x == 0) sh.n_cand = 0;
+        __syncthreads();
+        int more = 0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) more += mine[i] != 0 && mine[i] >= t;
+        if (more != 0) {
+            int to = atomicAdd(&sh.n_cand, more);
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                if (mine[i] != 0 && mine[i] >= t) sh.cand[to++] = mine[i];
+        }
+        __syncthreads();
+        n = sh.n_cand;
+    }
+    rank_candidates(sh, n, top, emit);
 }
 
 // look(slot, floor) adds what reaches floor among the at most 8 elements of a slot to the
@@ -185,10 +254,11 @@ __device__ inline void select_top(TopShared<NT> &sh, uint64_t floor, int slots, 
         if (int(threadIdx.x) < width && slot < slots) look(slot, floor);
         __syncthreads();
         const int n = sh.n_cand;
-        __syncthreads();                       // all have read it before it changes
         const bool fits = n <= kCandidates;
         if (fits) { at += width; have = n; }
         else width = kNarrow;                  // and this step again
+        if (at >= slots) break;
+        __syncthreads();                       // all have read n before it changes
         if (!fits || n > kCandidates - kNarrow * 8) {
             if (have > top) {
                 rank_candidates(sh, have, top, [&](int r, uint64_t k) { sh.kept[r] = k; });
@@ -201,7 +271,7 @@ __device__ inline void select_top(TopShared<NT> &sh, uint64_t floor, int slots, 
             __syncthreads();
         }
     }
-    rank_candidates(sh, have, top, emit);
+    rank_top(sh, have, top, emit);
 }
 
 // ------------------------------------------------------------------ joining lanes -------
@@ -209,43 +279,49 @@ template <int NT> struct StatsShared {
     float m[NT / 64], s[NT / 64], d[NT / 64];
 };
 
-// A lane's value from the lane CTRL says, inside rows of 16.
-template <int CTRL> __device__ inline float dpp(float x)
+// A reduction over the wave's lanes in a fixed order: cross-lane moves inside rows of 16, then
+// the four rows. Every lane gets the result.
+template <int CTRL> __device__ inline float lane_moved(float x)
 {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL,
                                                                  0xf, 0xf, true));
 }
-template <int CTRL> __device__ inline void join_dpp(RowStats &st)
+template <typename Op> __device__ inline float wave_reduce(float x, Op op)
 {
-    st.join(dpp<CTRL>(st.m), dpp<CTRL>(st.s), dpp<CTRL>(st.d));
+    x = op(x, lane_moved<0xb1>(x));          // lane ^ 1
+    x = op(x, lane_moved<0x4e>(x));          // lane ^ 2
+    x = op(x, lane_moved<0x141>(x));         // the other four of eight
+    x = op(x, lane_moved<0x140>(x));         // the other eight of 16
+    auto row = [&](int r) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16 * r));
+    };
+    return op(op(row(0), row(1)), op(row(2), row(3)));
 }
 
-// Every thread gets the workgroup's joined sums (in the same order each time). Lanes are
-// joined by cross-lane moves up to 16, then by shuffles.
+// Every thread gets the workgroup's joined sums (in the same order each time): the lanes are
+// brought to their largest peak first, then summed.
 template <int NT> __device__ inline RowStats join_stats(StatsShared<NT> &sh, RowStats st)
 {
+    const auto larger = [](float a, float b) { return __builtin_fmaxf(a, b); };
+    const auto plus = [](float a, float b) { return a + b; };
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    join_dpp<0xb1>(st);          // lane ^ 1
-    join_dpp<0x4e>(st);          // lane ^ 2
-    join_dpp<0x141>(st);         // mirrored in 8 lanes: the other four
-    join_dpp<0x140>(st);         // mirrored in 16: the other eight
-    st.join(__shfl_xor(st.m, 16), __shfl_xor(st.s, 16), __shfl_xor(st.d, 16));
-    st.join(__shfl_xor(st.m, 32), __shfl_xor(st.s, 32), __shfl_xor(st.d, 32));
+    st.raise(wave_reduce(st.m, larger));
+    st.s = wave_reduce(st.s, plus);
+    st.d = wave_reduce(st.d, plus);
     if (lane == 0) { sh.m[wave] = st.m; sh.s[wave] = st.s; sh.d[wave] = st.d; }
     __syncthreads();
     RowStats all;
-    for (int w = 0; w < NT / 64; ++w) all.join(sh.m[w], sh.s[w], sh.d[w]);
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) all.m = __builtin_fmaxf(all.m, sh.m[w]);
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) {
+        RowStats one;
+        one.m = sh.m[w]; one.s = sh.s[w]; one.d = sh.d[w];
+        one.raise(all.m);
+        all.s += one.s;
+        all.d += one.d;
+    }
     return all;
-}
-
-struct RowResult {
-    float lse, entropy;
-};
-__device__ inline RowResult row_result(const RowStats &st)
-{
-    if (st.s == 0.0f) return {kNegInf, 0.0f};            // nothing but -infinity
-    const float logs = __builtin_logf(st.s);
-    return {st.m + logs, logs - kLn2 * (st.d / st.s)};
 }
 
 // The row's token and its logit, loaded ahead of the sums.
@@ -263,14 +339,14 @@ template <int DT> __device__ inline RowToken load_token(const RowArgs &p, int64_
 
 __device__ inline void write_row(const RowArgs &p, int64_t row, const RowStats &st, RowToken token)
 {
-    const RowResult r = row_result(st);
+    const bool none = st.s == 0.0f;                       // nothing but -infinity
+    const float logs = __builtin_logf(st.s);
     // x - m is small where x is likely, so it is taken before log s is
-    float lp = (token.x - st.m) - __builtin_logf(st.s);
-    if (st.s == 0.0f) lp = kNegInf;
+    float lp = none ? kNegInf : (token.x - st.m) - logs;
     if (token.t >= p.V) lp = __builtin_nanf("");
     p.logprobs[row] = token.t < 0 ? 0.0f : lp;
-    if (p.entropy) p.entropy[row] = r.entropy;
-    if (p.lse) p.lse[row] = r.lse;
+    if (p.entropy) p.entropy[row] = none ? 0.0f : logs - kLn2 * (st.d / st.s);
+    if (p.lse) p.lse[row] = none ? kNegInf : st.m + logs;
 }
 __device__ inline void write_top(const RowArgs &p, int64_t row, const RowStats &st, int r,
                                  uint64_t key)
@@ -283,10 +359,9 @@ __device__ inline void write_top(const RowArgs &p, int64_t row, const RowStats &
 
 // ------------------------------------------------------------------ the pass ------------
 // One workgroup per (row, part). A thread's elements: up to one of the head before the
-// first 16-byte boundary, then the chunks tid, tid + 256, ... of 16 bytes, then up to one
-// of the tail. U chunks are in flight, and the peak is raised once for them. HBM-bound where rows fill the card; the
-// arithmetic (a conversion, 1/2 max, a difference, a product, an exponential at a quarter of
-// the rate, a max, two sums an element) comes to most of that time.
+// first 16-byte boundary, then the chunks tid, tid + NT, ... of 16 bytes, then up to one
+// of the tail. U chunks are in flight, and the peak is raised once for them. HBM-bound where
+// rows fill the card: 4096 x 131072 bf16 takes 188 us (5.7 TB/s; reading alone 181).
 template <int DT, bool TOP, int NT, int U>
 __global__ __launch_bounds__(NT) void k_row_pass(RowArgs p)
 {
@@ -305,9 +380,12 @@ __global__ __launch_bounds__(NT) void k_row_pass(RowArgs p)
     const int tail = head + chunks * W;                   // first element of the tail
     const T *body = x + head;
     RowToken token{};
-    if (p.splits == 1 && tid == 0) token = load_token<DT>(p, row);
+    // the row's results are the last wave's to write, while the others go on to the alternatives
+    if (p.splits == 1 && tid == NT - 1) token = load_token<DT>(p, row);
+    if (TOP && tid == 0) { tops.n_cand = 0; tops.n_threads = 0; }
 
     RowStats st;
+    Pack<T, W> b[U];
     // the best group: its value in key order, and its first element
     uint32_t best = 0;
     int best_at = tid < head ? tid : tid < chunks ? head + tid * W : tail + tid;
@@ -319,34 +397,34 @@ __global__ __launch_bounds__(NT) void k_row_pass(RowArgs p)
             best = max(best, o);
         }
     };
-    auto take1 = [&](int at) __attribute__((always_inline)) {
-        const float v = Elem<DT>::widen(x[at]);
+    float edge[2] = {0.0f, 0.0f};                         // the thread's head and tail elements
+    auto take1 = [&](int at, float &v) __attribute__((always_inline)) {
+        v = Elem<DT>::widen(x[at]);
         note(v, at);
         st.raise(v);
         st.add(v);
     };
-    if (tid < head) take1(tid);
-    auto load = [&](Pack<T, W> (&b)[U], int c) __attribute__((always_inline)) {
+    auto load = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             b[u] = load_pack<T, W>(body + int64_t(min(c + u * NT, chunks - 1)) * W);
     };
-    auto widen = [&](float (&v)[W], const Pack<T, W> &b, int c) __attribute__((always_inline)) {
+    auto widen = [&](float (&v)[W], int u, int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[j] = Elem<DT>::widen(b.v[j]);
+        for (int j = 0; j < W; ++j) v[j] = Elem<DT>::widen(b[u].v[j]);
         float peak = v[0];
 #pragma unroll
         for (int j = 1; j < W; ++j) peak = __builtin_fmaxf(peak, v[j]);
-        note(peak, head + c * W);
+        note(peak, head + (c + u * NT) * W);
         return peak;
     };
+    if (tid < head) take1(tid, edge[0]);
     int c = tid;
     for (; c + (U - 1) * NT < chunks; c += U * NT) {
-        Pack<T, W> b[U];
         float v[U][W], peak = kNegInf;
-        load(b, c);
+        load(c);
 #pragma unroll
-        for (int u = 0; u < U; ++u) peak = __builtin_fmaxf(peak, widen(v[u], b[u], c + u * NT));
+        for (int u = 0; u < U; ++u) peak = __builtin_fmaxf(peak, widen(v[u], u, c));
         st.raise(peak);
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -354,101 +432,126 @@ __global__ __launch_bounds__(NT) void k_row_pass(RowArgs p)
             for (int j = 0; j < W; ++j) st.add(v[u][j]);
     }
     if (c < chunks) {                                     // fewer than U are left
-        Pack<T, W> b[U];
-        load(b, c);
+        load(c);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (c + u * NT >= chunks) break;
             float v[W];
-            st.raise(widen(v, b[u], c + u * NT));
+            st.raise(widen(v, u, c));
 #pragma unroll
             for (int j = 0; j < W; ++j) st.add(v[j]);
         }
     }
-    if (tid < n - tail) take1(tail + tid);
+    if (tid < n - tail) take1(tail + tid, edge[1]);
 
-    const RowStats all = join_stats(stats, st);
+    const RowStats all = join_stats(stats, st);           // a barrier: the candidates are there
     RowPart *out = reinterpret_cast<RowPart *>(p.parts + int64_t(blockIdx.x) * p.part_bytes);
-    if (tid == 0) {
+    if (tid == NT - 1) {
         if (p.splits == 1) write_row(p, row, all, token);
         else *out = RowPart{all.m, all.s, all.d, 0.0f};
     }
     if constexpr (TOP) {
+        uint64_t *keys = reinterpret_cast<uint64_t *>(out + 1);
+        auto emit = [&](int r, uint64_t k) {
+            if (p.splits > 1) keys[r] = k - uint32_t(first);     // indices in the row
+            else write_top(p, row, all, r, k);
+        };
+        // a part shorter than `top` leaves its last keys empty
+        if (p.splits > 1 && tid < p.top && tid >= n) keys[tid] = 0;
         const uint64_t mine = empty ? 0 : uint64_t(best) << 32 | (0xffffffffu - uint32_t(best_at));
         uint64_t floor = top_bound(tops, mine, p.top);
         // T's group reaches W - 1 elements behind its first
-        const uint32_t low = uint32_t(floor);
-        floor -= min(low, uint32_t(W - 1));
+        floor = max(floor - min(uint32_t(floor), uint32_t(W - 1)), uint64_t(1));
+        if (chunks <= U * NT) {                           // b holds all of this thread's chunks
+            static_assert(U * W <= 32, "a bit for each element");
+            if (mine >= floor) {
+                const int mine_n = tid < chunks ? (chunks - tid + NT - 1) / NT * W : 0;
+                add_candidates<DT>(tops, b, mine_n == 32 ? 0xffffffffu : (1u << mine_n) - 1, floor,
+                                   [&](int i) { return head + (tid + i / W * NT) * W + i % W; });
+                if (tid < head) add_candidate(tops, key_of(edge[0], uint32_t(tid)), floor);
+                if (tid < n - tail) add_candidate(tops, key_of(edge[1], uint32_t(tail + tid)), floor);
+            }
+            __syncthreads();
+            const int found = tops.n_cand;
+            if (found <= kCandidates) {
+                rank_top(tops, found, p.top, emit);
+                return;
+            }
+            __syncthreads();                              // all have read it
+            if (tid == 0) tops.n_cand = 0;
+        }
+        if (mine >= floor) tops.threads[atomicAdd(&tops.n_threads, 1)] = tid;
+        __syncthreads();
         // the threads' chunks, and one more slot for their head and tail
         const int per = (chunks + NT - 1) / NT + 1;
-        auto look = [&](int slot, uint64_t least) {
+        auto look = [&](int slot, uint64_t from) {
             const int u = tops.threads[slot / per], i = slot % per;
-            auto offer = [&](float v, int at) {
-                const uint64_t k = key_of(v, uint32_t(at));
-                if (k >= least) add_candidate(tops, k);
-            };
             if (i == per - 1) {
-                if (u < head) offer(Elem<DT>::widen(x[u]), u);
-                if (u < n - tail) offer(Elem<DT>::widen(x[tail + u]), tail + u);
+                if (u < head) add_candidate(tops, key_of(Elem<DT>::widen(x[u]), uint32_t(u)), from);
+                if (u < n - tail)
+                    add_candidate(tops, key_of(Elem<DT>::widen(x[tail + u]), uint32_t(tail + u)), from);
                 return;
             }
             const int chunk = u + i * NT;
             if (chunk >= chunks) return;
-            const Pack<T, W> b = load_pack<T, W>(body + int64_t(chunk) * W);
-#pragma unroll
-            for (int j = 0; j < W; ++j) offer(Elem<DT>::widen(b.v[j]), head + chunk * W + j);
+            const Pack<T, W> c[1] = {load_pack<T, W>(body + int64_t(chunk) * W)};
+            add_candidates<DT>(tops, c, (1u << W) - 1, from, [&](int j) { return head + chunk * W + j; });
         };
-        const int slots = tops.n_threads * per;
-        if (p.splits > 1) {
-            uint64_t *keys = reinterpret_cast<uint64_t *>(out + 1);
-            // a part shorter than `top` leaves its last keys empty
-            if (tid < p.top && tid >= n) keys[tid] = 0;
-            // indices in the row
-            select_top(tops, floor, slots, p.top, look,
-                       [&](int r, uint64_t k) { keys[r] = k - uint32_t(first); });
-        } else {
-            select_top(tops, floor, slots, p.top, look,
-                       [&](int r, uint64_t k) { write_top(p, row, all, r, k); });
-        }
+        select_top(tops, floor, tops.n_threads * per, p.top, look, emit);
     }
 }
 
 // Joins a row's parts: the sums in one order of the parts, the alternatives from the parts'
-// lists (in the parts' order, so every key is a group of its own).
+// lists (every key is a group of its own).
 template <int DT, bool TOP>
 __global__ __launch_bounds__(256) void k_row_join(RowArgs p)
 {
-    constexpr int NT = 256;
+    constexpr int NT = 256, EACH = 4;
+    static_assert(EACH * NT <= kCandidates, "the list holds every key");
     __shared__ StatsShared<NT> stats;
     __shared__ TopShared<TOP ? NT : 64> tops;
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x;
     const char *parts = p.parts + row * p.splits * p.part_bytes;
     RowToken token{};
-    if (tid == 0) token = load_token<DT>(p, row);
+    if (tid == NT - 1) token = load_token<DT>(p, row);
+    if (TOP && tid == 0) tops.n_cand = 0;
     const int n = TOP ? p.splits * p.top : 0;
     auto key_at = [&](int i) {
         const int s = i / p.top;
         return reinterpret_cast<const uint64_t *>(parts + s * p.part_bytes +
                                                   sizeof(RowPart))[i - s * p.top];
     };
-    uint64_t best = 0;
-    for (int i = tid; i < n; i += NT) best = max(best, key_at(i));
+    uint64_t mine[EACH], best = 0;                        // the first keys; often they are all
+    if constexpr (TOP) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            mine[i] = tid + i * NT < n ? key_at(tid + i * NT) : 0;
+            best = max(best, mine[i]);
+        }
+        for (int i = tid + EACH * NT; i < n; i += NT) best = max(best, key_at(i));
+    }
     RowStats st;
     for (int s = tid; s < p.splits; s += NT) {
         const RowPart *q = reinterpret_cast<const RowPart *>(parts + s * p.part_bytes);
         st.join(q->peak, q->sum, q->dot);
     }
     const RowStats all = join_stats(stats, st);
-    if (tid == 0) write_row(p, row, all, token);
+    if (tid == NT - 1) write_row(p, row, all, token);
     if constexpr (TOP) {
         const uint64_t floor = max(top_bound(tops, best, p.top), uint64_t(1));
-        select_top(tops, floor, n, p.top,
-                   [&](int slot, uint64_t least) {
-                       const uint64_t k = key_at(slot);
-                       if (k >= least) add_candidate(tops, k);
-                   },
-                   [&](int r, uint64_t k) { write_top(p, row, all, r, k); });
+        auto emit = [&](int r, uint64_t k) { write_top(p, row, all, r, k); };
+        if (n <= EACH * NT) {
+#pragma unroll
+            for (int i = 0; i < EACH; ++i)
+                add_candidate(tops, mine[i], floor);
+            __syncthreads();
+            rank_top(tops, tops.n_cand, p.top, emit);
+        } else {
+            select_top(tops, floor, n, p.top,
+                       [&](int slot, uint64_t least) { add_candidate(tops, key_at(slot), least); },
+                       emit);
+        }
     }
 }
 

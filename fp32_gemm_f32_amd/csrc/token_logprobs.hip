@@ -25,7 +25,7 @@ struct RowSplit {
 
 // Long rows are split over workgroups where there are fewer rows than compute units, into
 // parts of at least kLeastPart elements: one compute unit takes 22 us over a row of 131072 (its
-// arithmetic), 32 of them and the join 13. Below kLeastRow the join costs what it saves.
+// arithmetic), 32 of them and the join 9.4. Below kLeastRow the join costs what it saves.
 constexpr int kLeastPart = 4096, kLeastRow = 65536;
 RowSplit split_rows(int M, int V, int top, int cus)
 {
