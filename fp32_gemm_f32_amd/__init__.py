@@ -689,7 +689,9 @@ def token_logprobs(logits, tokens, top: int = 0) -> TokenLogprobs:
     more gives NaN. Alternatives of equal logits come by ascending index.
 
     logprobs, entropy and lse carry gradients to logits where it requires them
-    (token_logprobs_backward, in one pass too); the alternatives carry none."""
+    (token_logprobs_backward, in one pass too); the alternatives carry none. In a graph capture
+    call token_logprobs_backward itself rather than .backward(): autograd accumulates into a leaf
+    on the stream it first saw it on, which a capture must not wait for."""
     import torch
 
     if logits.requires_grad and torch.is_grad_enabled():

@@ -75,6 +75,7 @@ I8Layout layout_of(int K, const void *A, int64_t lda, const void *B, int64_t ldb
 
 constexpr double kLaunch = 2.5;          // us: a kernel's start and end
 constexpr double kBytesPerUs = 4.6e6;    // memory traffic of a copy or of streamed operands
+constexpr double kMostCopied = 4.0e9;    // bytes of workspace a copy may ask for
 
 // Microseconds of `groups` workgroups of `panels` panels each.
 double tile_cost(const I8Variant &v, int64_t groups, int64_t panels, int cus)
@@ -135,7 +136,7 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
                      false, false, kLaunch + body + (any ? 0.25 * body + 0.08 * double(ceil_div(chunk, 128)) : 0.0) +
                          join_cost(s)};
             offer(p);
-            if (any && workspace) {
+            if (any && workspace && copied <= kMostCopied) {
                 p.kernel = v.aligned;
                 p.copy_a = !rows.a;
                 p.copy_b = !rows.b;

@@ -357,12 +357,20 @@ __device__ inline void write_top(const RowArgs &p, int64_t row, const RowStats &
     p.top_tokens[row * p.top + r] = key_index(key);
 }
 
+template <bool STREAM, typename T, int W> __device__ inline Pack<T, W> load_chunk_of(const T *p)
+{
+    if constexpr (STREAM) return load_pack_stream<T, W>(p);
+    else return load_pack<T, W>(p);
+}
+
 // ------------------------------------------------------------------ the pass ------------
 // One workgroup per (row, part). A thread's elements: up to one of the head before the
 // first 16-byte boundary, then the chunks tid, tid + NT, ... of 16 bytes, then up to one
 // of the tail. U chunks are in flight, and the peak is raised once for them. HBM-bound where
-// rows fill the card: 4096 x 131072 bf16 takes 188 us (5.7 TB/s; reading alone 181).
-template <int DT, bool TOP, int NT, int U>
+// rows fill the card: 4096 x 131072 bf16 takes 165 us (6.5 TB/s) with STREAM, loads that do not
+// stay in the caches, and 188 without; where the logits fit the caches, STREAM costs (511 x 32001
+// f32 12.4 to 12.8 us).
+template <int DT, bool TOP, int NT, int U, bool STREAM>
 __global__ __launch_bounds__(NT) void k_row_pass(RowArgs p)
 {
     typedef typename Elem<DT>::type T;
@@ -407,7 +415,7 @@ __global__ __launch_bounds__(NT) void k_row_pass(RowArgs p)
     auto load = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            b[u] = load_pack<T, W>(body + int64_t(min(c + u * NT, chunks - 1)) * W);
+            b[u] = load_chunk_of<STREAM, T, W>(body + int64_t(min(c + u * NT, chunks - 1)) * W);
     };
     auto widen = [&](float (&v)[W], int u, int c) __attribute__((always_inline)) {
 #pragma unroll
@@ -566,9 +574,10 @@ struct GradArgs {
 };
 
 // One workgroup per (row, part): dx = -p (a + h (logp + H)), plus g at the token, with
-// a = g - g_lse and h = g_entropy.
+// a = g - g_lse and h = g_entropy. HBM-bound: 4096 x 131072 bf16 with the entropy's term takes 362 us
+// (5.9 TB/s, reading and writing; a large copy reaches 4.8), 511 x 32001 f32 22.3.
 constexpr int kGradThreads = 256;
-template <int DT>
+template <int DT, bool STREAM>
 __global__ __launch_bounds__(kGradThreads) void k_row_gradient(GradArgs p)
 {
     typedef typename Elem<DT>::type T;
@@ -607,7 +616,7 @@ __global__ __launch_bounds__(kGradThreads) void k_row_gradient(GradArgs p)
     const int token_chunk = body < 0 ? -1 : body / W, place = body % W;
     for (int c = tid; c < chunks; c += kGradThreads) {
         const int64_t e = head + int64_t(c) * W;
-        const Pack<T, W> in = load_pack<T, W>(x + e);
+        const Pack<T, W> in = load_chunk_of<STREAM, T, W>(x + e);
         float v[W];
         Pack<T, W> o;
 #pragma unroll

@@ -48,16 +48,23 @@ struct RowLaunch {
     RowKernel kernel;
     int threads;
 };
+// Logits of half the last-level cache (256 MB) and more are read past it: 2048 x 50000 bf16 (205 MB)
+// 38.5 to 36.4 us, 4096 x 131072 188 to 165; 1500 x 50000 (150 MB) 28.0 to 28.3 where it was
+// there still and 30.5 to 28.8 where not; 600 x 50001 level.
+constexpr int64_t kStreamBytes = int64_t(128) << 20;
+bool streamed(int M, int V, int dtype) { return int64_t(M) * V * dtype_bytes(dtype) >= kStreamBytes; }
+
 // Workgroups of more threads for fewer and longer rows, so that enough loads are in flight.
-template <int DT, bool TOP> RowLaunch pass_of(int64_t groups, int len, int cus)
+template <int DT, bool TOP> RowLaunch pass_of(int64_t groups, int len, int cus, bool stream)
 {
-    if (groups <= cus && len >= 32768) return {&k_row_pass<DT, TOP, 1024, 4>, 1024};
-    if (groups <= 4 * cus && len >= 8192) return {&k_row_pass<DT, TOP, 512, 4>, 512};
-    return {&k_row_pass<DT, TOP, 256, 4>, 256};
+    if (groups <= cus && len >= 32768) return {&k_row_pass<DT, TOP, 1024, 4, false>, 1024};
+    if (groups <= 4 * cus && len >= 8192)
+        return {stream ? &k_row_pass<DT, TOP, 512, 4, true> : &k_row_pass<DT, TOP, 512, 4, false>, 512};
+    return {stream ? &k_row_pass<DT, TOP, 256, 4, true> : &k_row_pass<DT, TOP, 256, 4, false>, 256};
 }
-template <int DT> RowLaunch pass_kernel(bool top, int64_t groups, int len, int cus)
+template <int DT> RowLaunch pass_kernel(bool top, int64_t groups, int len, int cus, bool stream)
 {
-    return top ? pass_of<DT, true>(groups, len, cus) : pass_of<DT, false>(groups, len, cus);
+    return top ? pass_of<DT, true>(groups, len, cus, stream) : pass_of<DT, false>(groups, len, cus, stream);
 }
 template <int DT> RowKernel join_kernel(bool top)
 {
@@ -125,16 +132,17 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
     p.parts = static_cast<char *>(workspace); p.part_bytes = r.part_bytes;
     p.M = M; p.V = V; p.top = top; p.splits = r.splits; p.part_len = r.part_len;
     const int64_t groups = int64_t(M) * r.splits;
+    const bool past_caches = streamed(M, V, dtype);
     RowLaunch pass;
     RowKernel join;
     if (dtype == SGEMM_DTYPE_F32) {
-        pass = pass_kernel<SGEMM_DTYPE_F32>(top > 0, groups, r.part_len, cus);
+        pass = pass_kernel<SGEMM_DTYPE_F32>(top > 0, groups, r.part_len, cus, past_caches);
         join = join_kernel<SGEMM_DTYPE_F32>(top > 0);
     } else if (dtype == SGEMM_DTYPE_BF16) {
-        pass = pass_kernel<SGEMM_DTYPE_BF16>(top > 0, groups, r.part_len, cus);
+        pass = pass_kernel<SGEMM_DTYPE_BF16>(top > 0, groups, r.part_len, cus, past_caches);
         join = join_kernel<SGEMM_DTYPE_BF16>(top > 0);
     } else {
-        pass = pass_kernel<SGEMM_DTYPE_F16>(top > 0, groups, r.part_len, cus);
+        pass = pass_kernel<SGEMM_DTYPE_F16>(top > 0, groups, r.part_len, cus, past_caches);
         join = join_kernel<SGEMM_DTYPE_F16>(top > 0);
     }
     st = launch(pass.kernel, dim3(unsigned(groups)), dim3(pass.threads), stream, p);
@@ -175,8 +183,11 @@ extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dty
     p.part_len = 16384 / size;
     p.parts = ceil_div(V, p.part_len);
     if (int64_t(M) * p.parts > kMaxGroups) return SGEMM_ETOO_LARGE;
-    auto kern = dtype == SGEMM_DTYPE_F32    ? &k_row_gradient<SGEMM_DTYPE_F32>
-                : dtype == SGEMM_DTYPE_BF16 ? &k_row_gradient<SGEMM_DTYPE_BF16>
-                                            : &k_row_gradient<SGEMM_DTYPE_F16>;
+    const bool past_caches = streamed(M, V, dtype);
+    auto kern = dtype == SGEMM_DTYPE_F32
+                    ? (past_caches ? &k_row_gradient<SGEMM_DTYPE_F32, true> : &k_row_gradient<SGEMM_DTYPE_F32, false>)
+                : dtype == SGEMM_DTYPE_BF16
+                    ? (past_caches ? &k_row_gradient<SGEMM_DTYPE_BF16, true> : &k_row_gradient<SGEMM_DTYPE_BF16, false>)
+                    : (past_caches ? &k_row_gradient<SGEMM_DTYPE_F16, true> : &k_row_gradient<SGEMM_DTYPE_F16, false>);
     return launch(kern, dim3(unsigned(M * int64_t(p.parts))), dim3(kGradThreads), stream, p);
 }

@@ -64,8 +64,8 @@ int gemm_i8_quantize_rows(int M, int K,
  * and offset in FP32, and rounded once to C's type c_dtype. bias is NULL or N floats. The
  * result does not depend on the plan: any tiling and split gives the same bits.
  *
- * Limits: K <= 131071 (so that K * 128 * 128 stays below 2^31) and 256 rows of A or B
- * below 2^31 bytes (lda, ldb < 8388608), else SGEMM_ETOO_LARGE.
+ * Limits: K <= 131071 (so that K * 128 * 128 stays below 2^31), 256 rows of A or B below 2^31
+ * bytes (lda, ldb < 8388608), fewer than 2^30 blocks of 16 x 16 in C, else SGEMM_ETOO_LARGE.
  *
  * workspace: products with few tiles split K over workgroups and join the partial sums
  * there (32-bit integers) with a second kernel; large products of rows off a word's boundary
