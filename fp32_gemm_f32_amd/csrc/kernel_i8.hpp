@@ -184,19 +184,22 @@ __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)
         sb[j] = p.sb[n];
         bias[j] = p.bias ? p.bias[n] : 0.0f;
     }
+    // all of the rows' scales ahead of the stores: one wait instead of one a row
+    float sa[T::RB][16];
+#pragma unroll
+    for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) sa[i][v] = p.sa[min(row0 + 32 * i + 8 * (v / 4) + v % 4, p.M - 1)];
     auto store_all = [&](auto dt) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
                 const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
-                if (m < p.M) {
-                    const float sa = p.sa[m];
-                    float x[T::CB];
+                float x[T::CB];
 #pragma unroll
-                    for (int j = 0; j < T::CB; ++j) x[j] = i8_value(acc[i][j][v], sa, sb[j], bias[j]);
-                    i8_store<decltype(dt)::value, T::CB>(p.C, m * p.ldc + col, x, valid);
-                }
+                for (int j = 0; j < T::CB; ++j) x[j] = i8_value(acc[i][j][v], sa[i][v], sb[j], bias[j]);
+                if (m < p.M) i8_store<decltype(dt)::value, T::CB>(p.C, m * p.ldc + col, x, valid);
             }
     };
     if (p.c_dtype == SGEMM_DTYPE_BF16) store_all(std::integral_constant<int, SGEMM_DTYPE_BF16>{});
