@@ -21,34 +21,36 @@ constexpr int kWorkspaceAlign = 16;
 
 typedef void (*I8Kernel)(I8Args);
 
-// The tiles, smallest first. `c1` and `c2` are the microseconds a panel of 128 takes with one
-// and (where LDS holds two) two workgroups on every compute unit, operands in the caches;
-// measured on the products 1024^3 to 8192^3 and their thin kin (M of 64 to 1024).
+// The tiles, smallest first. In microseconds: `c1` and `c2` are a panel of 128 with one and (where
+// LDS holds two) two workgroups on every compute unit, `ends` a workgroup's start and stores. They
+// and the constants of make_plan were fitted to the times of every tile and split of 239 products
+// drawn over M of 17 to 8192 and N, K of 64 to 16384, so that the plan's choice costs least: 1.3 %
+// more than the best of each on average, 18 % at most.
 struct I8Variant {
     const char *name;
     I8Kernel aligned, any;
     int bm, bn, threads;
-    double c1, c2;
+    double c1, c2, ends;
 };
 
 template <int BM, int BN, int WGM, int WGN, int NSTG>
-constexpr I8Variant tile(const char *name, double c1, double c2)
+constexpr I8Variant tile(const char *name, double c1, double c2, double ends)
 {
     typedef I8Tile<BM, BN, WGM, WGN, 128, NSTG> T;
-    return {name, &k_gemm_i8<T, false>, &k_gemm_i8<T, true>, BM, BN, T::NT, c1, c2};
+    return {name, &k_gemm_i8<T, false>, &k_gemm_i8<T, true>, BM, BN, T::NT, c1, c2, ends};
 }
 
 const I8Variant kVariants[] = {
-    tile<64, 32, 2, 1, 6>("i8_64x32", 0.23, 0.37),
-    tile<64, 64, 2, 2, 4>("i8_64x64", 0.30, 0.53),
-    tile<64, 128, 2, 2, 3>("i8_64x128", 0.45, 0.77),
-    tile<128, 128, 2, 2, 2>("i8_128x128", 0.85, 1.26),
-    tile<128, 256, 2, 4, 3>("i8_128x256", 1.08, 0.0),
-    tile<256, 256, 4, 2, 2>("i8_256x256", 1.85, 0.0),
+    tile<64, 32, 2, 1, 6>("i8_64x32", 0.18, 0.32, 2.6),
+    tile<64, 64, 2, 2, 4>("i8_64x64", 0.18, 0.40, 3.1),
+    tile<64, 128, 2, 2, 3>("i8_64x128", 0.25, 0.64, 3.2),
+    tile<128, 128, 2, 2, 2>("i8_128x128", 0.73, 0.82, 2.9),
+    tile<128, 256, 2, 4, 3>("i8_128x256", 0.74, 0.0, 3.6),
+    tile<256, 256, 4, 2, 2>("i8_256x256", 1.32, 0.0, 3.7),
 };
 // Few rows: 16 rows, all of K to a workgroup.
 const I8Variant kFewRows = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 1, 8, 4, true>>,
-                            &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 16, 512, 0.0, 0.0};
+                            &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 16, 512, 0.0, 0.0, 0.0};
 
 struct I8Plan {
     const I8Variant *v;
@@ -73,18 +75,25 @@ I8Layout layout_of(int K, const void *A, int64_t lda, const void *B, int64_t ldb
     return {ok(A, lda), ok(B, ldb)};
 }
 
-constexpr double kLaunch = 2.5;          // us: a kernel's start and end
-constexpr double kBytesPerUs = 4.6e6;    // memory traffic of a copy or of streamed operands
+constexpr double kLaunch = 1.6;          // us: a kernel's start and end
+constexpr double kStreamPerUs = 6.8e6;   // bytes of operands, from the last-level cache too
 constexpr double kMostCopied = 4.0e9;    // bytes of workspace a copy may ask for
 
-// Microseconds of `groups` workgroups of `panels` panels each.
-double tile_cost(const I8Variant &v, int64_t groups, int64_t panels, int cus)
+struct Rounds {
+    int64_t full, rest;      // whole rounds of workgroups on every compute unit, what is left
+    int64_t all() const { return full + (rest > 0); }
+};
+Rounds rounds_of(const I8Variant &v, int64_t groups, int cus)
 {
-    const int per_cu = v.c2 > 0 ? 2 : 1;
-    const int64_t full = groups / (int64_t(cus) * per_cu), rest = groups % (int64_t(cus) * per_cu);
-    const double whole = per_cu == 2 ? v.c2 : v.c1;
-    const double tail = rest == 0 ? 0.0 : rest <= cus ? v.c1 : v.c2;
-    return (double(full) * whole + tail) * double(panels + 2);
+    const int64_t at_once = int64_t(cus) * (v.c2 > 0 ? 2 : 1);
+    return {groups / at_once, groups % at_once};
+}
+// Microseconds of rounds of workgroups of `panels` panels each.
+double tile_cost(const I8Variant &v, const Rounds &r, int64_t panels, int cus)
+{
+    const double whole = v.c2 > 0 ? v.c2 : v.c1;
+    const double tail = r.rest == 0 ? 0.0 : r.rest <= cus ? v.c1 : v.c2;
+    return (double(r.full) * whole + tail) * (double(panels) + 3.4) + double(r.all()) * v.ends;
 }
 
 // The cheapest of: every tile, K whole or split; rows as they are, in the slower form for any
@@ -106,7 +115,7 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         return std::pair<int, int>(int(ceil_div(K, chunk)), int(std::min<int64_t>(chunk, K)));
     };
     const auto join_cost = [&](int splits) {
-        return splits == 1 ? 0.0 : kLaunch + 1.5 + double(splits + 1) * M * N * 4 / kBytesPerUs;
+        return splits == 1 ? 0.0 : 2.4 + double(splits + 1) * M * N * 4 / 2.5e6;
     };
     const int most = workspace ? int(std::min<int64_t>(16, std::max<int64_t>(1, panels / 4))) : 1;
     if (M <= 16) {
@@ -118,7 +127,7 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
             // a panel of every wave takes this long when little else is in flight
             const double turn = any ? double(ceil_div(chunk, 1024)) * 1.4 : double(ceil_div(chunk, 2048)) * 0.8;
             const double step = double(ceil_div(groups, 2 * cus)) * turn;
-            const double cost = kLaunch + std::max(step, bytes / kBytesPerUs * (any ? 1.25 : 1.0)) +
+            const double cost = kLaunch + 1.0 + std::max(step, bytes / 4.6e6 * (any ? 1.25 : 1.0)) +
                                 join_cost(s);
             offer({&kFewRows, any ? kFewRows.any : kFewRows.aligned, 16, bn, 1,
                    int(ceil_div(N, bn)), s, chunk, false, false, cost});
@@ -130,17 +139,18 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             if (s > 1 && tm * tn * s > 2 * int64_t(cus)) break;
-            const double body = std::max(tile_cost(v, tm * tn * s, ceil_div(chunk, 128), cus),
-                                         bytes / kBytesPerUs);
-            I8Plan p{&v, any ? v.any : v.aligned, v.bm, v.bn, int(tm), int(tn), s, chunk,
-                     false, false, kLaunch + body + (any ? 0.25 * body + 0.08 * double(ceil_div(chunk, 128)) : 0.0) +
-                         join_cost(s)};
+            const int64_t depth = ceil_div(chunk, 128);
+            const Rounds r = rounds_of(v, tm * tn * s, cus);
+            const double body = std::max(tile_cost(v, r, depth, cus), bytes / kStreamPerUs);
+            I8Plan p{&v, any ? v.any : v.aligned, v.bm, v.bn, int(tm), int(tn), s, chunk, false, false,
+                     kLaunch + body + join_cost(s)};
+            if (any) p.cost += 0.09 * body + 0.15 * double(depth) * double(r.all());
             offer(p);
             if (any && workspace && copied <= kMostCopied) {
                 p.kernel = v.aligned;
                 p.copy_a = !rows.a;
                 p.copy_b = !rows.b;
-                p.cost = 2 * kLaunch + body + 2.0 * copied / kBytesPerUs + join_cost(s);
+                p.cost = kLaunch + body + join_cost(s) + 4.7 + 2.0 * copied / 5.9e6;
                 offer(p);
             }
         }
@@ -256,6 +266,9 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     p.A = A; p.B = B; p.sa = a_scales; p.sb = b_scales; p.bias = bias; p.C = C;
     p.lda = lda; p.ldb = ldb; p.ldc = ldc;
     p.M = M; p.N = N; p.K = K; p.c_dtype = c_dtype;
+    // (2560 x 13056 x 512 to f32, 256 x 256 tiles: rows on lines of 64 bytes 44.5 to 42.0 us, off
+    // them 50.6 to 54.8, as each row of a tile ends in parts of a line)
+    p.stream = reinterpret_cast<uintptr_t>(C) % 64 == 0 && ldc * dtype_bytes(c_dtype) % 64 == 0;
     if (K == 0)
         return launch(&k_gemm_i8_empty, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 

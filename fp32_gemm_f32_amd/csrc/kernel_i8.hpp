@@ -27,6 +27,7 @@ struct I8Args {
     int c_dtype;
     int tiles_m, tiles_n;
     int splits, k_chunk;   // split s covers k in [s * k_chunk, min(K, (s + 1) * k_chunk))
+    bool stream;           // C's rows start on lines of 64 bytes: store past the caches
 };
 
 // C's value from the exact integer sum: one rounding to FP32, one each for the scales'
@@ -36,7 +37,7 @@ __device__ inline float i8_value(int sum, float sa, float sb, float bias)
     return static_cast<float>(sum) * (sa * sb) + bias;
 }
 
-template <int DT, int W>
+template <int DT, int W, bool STREAM = false>
 __device__ inline void i8_store(void *C, int64_t at, const float (&v)[W], int valid)
 {
     typedef typename Elem<DT>::type T;
@@ -45,7 +46,8 @@ __device__ inline void i8_store(void *C, int64_t at, const float (&v)[W], int va
         Pack<T, W> p;
 #pragma unroll
         for (int j = 0; j < W; ++j) p.v[j] = Elem<DT>::narrow(v[j]);
-        store_pack(c, p);
+        if constexpr (STREAM) store_pack_stream(c, p);
+        else store_pack(c, p);
     } else {
 #pragma unroll
         for (int j = 0; j < W; ++j)
@@ -190,7 +192,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)
     for (int i = 0; i < T::RB; ++i)
 #pragma unroll
         for (int v = 0; v < 16; ++v) sa[i][v] = p.sa[min(row0 + 32 * i + 8 * (v / 4) + v % 4, p.M - 1)];
-    auto store_all = [&](auto dt) __attribute__((always_inline)) {
+    auto store_all = [&](auto dt, auto stream) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
 #pragma unroll
@@ -199,12 +201,17 @@ __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)
                 float x[T::CB];
 #pragma unroll
                 for (int j = 0; j < T::CB; ++j) x[j] = i8_value(acc[i][j][v], sa[i][v], sb[j], bias[j]);
-                if (m < p.M) i8_store<decltype(dt)::value, T::CB>(p.C, m * p.ldc + col, x, valid);
+                if (m < p.M)
+                    i8_store<decltype(dt)::value, T::CB, decltype(stream)::value>(p.C, m * p.ldc + col, x, valid);
             }
     };
-    if (p.c_dtype == SGEMM_DTYPE_BF16) store_all(std::integral_constant<int, SGEMM_DTYPE_BF16>{});
-    else if (p.c_dtype == SGEMM_DTYPE_F16) store_all(std::integral_constant<int, SGEMM_DTYPE_F16>{});
-    else store_all(std::integral_constant<int, SGEMM_DTYPE_F32>{});
+    auto store = [&](auto dt) __attribute__((always_inline)) {
+        if (p.stream) store_all(dt, std::true_type{});
+        else store_all(dt, std::false_type{});
+    };
+    if (p.c_dtype == SGEMM_DTYPE_BF16) store(std::integral_constant<int, SGEMM_DTYPE_BF16>{});
+    else if (p.c_dtype == SGEMM_DTYPE_F16) store(std::integral_constant<int, SGEMM_DTYPE_F16>{});
+    else store(std::integral_constant<int, SGEMM_DTYPE_F32>{});
 }
 
 // Size of the resource that covers [from, end), `end` rounded up to a whole word.
@@ -540,7 +547,7 @@ __global__ __launch_bounds__(256) void k_quantize_rows(int M, int K, const void 
 #pragma unroll
         for (int j = 0; j < W; ++j) o.v[j] = int8_t(quantize_one(Elem<DT>::widen(c[i].v[j]), inverse));
         if (k + W <= K) {
-            store_pack(q + k, o);
+            store_pack_stream(q + k, o);
         } else {
 #pragma unroll
             for (int j = 0; j < W; ++j)
@@ -587,7 +594,7 @@ __global__ __launch_bounds__(1024) void k_quantize_long_rows(int K, const void *
         Pack<int8_t, W> o;
 #pragma unroll
         for (int j = 0; j < W; ++j) o.v[j] = int8_t(quantize_one(Elem<DT>::widen(c.v[j]), inverse));
-        store_pack(q + int64_t(i) * W, o);
+        store_pack_stream(q + int64_t(i) * W, o);
     }
     if (last < K) q[last] = int8_t(quantize_one(Elem<DT>::widen(x[last]), inverse));
     if (tid == 0) scales[row] = scale;

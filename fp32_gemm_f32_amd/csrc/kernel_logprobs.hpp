@@ -627,7 +627,7 @@ __global__ __launch_bounds__(kGradThreads) void k_row_gradient(GradArgs p)
         }
 #pragma unroll
         for (int j = 0; j < W; ++j) o.v[j] = Elem<DT>::narrow(v[j]);
-        store_pack(out + e, o);
+        store_pack_stream(out + e, o);
     }
 }
 

@@ -115,14 +115,18 @@ template <typename T, int W> __device__ inline Pack<T, W> load_pack_stream(const
     typedef B __attribute__((aligned(alignof(T)))) unaligned;
     return __builtin_bit_cast(Pack<T, W>, static_cast<B>(__builtin_nontemporal_load(reinterpret_cast<const unaligned *>(p))));
 }
-// Results leave this way: they are written once, and the caches serve the operands instead
-// (gradient of 511 x 32001 f32 27.4 to 22.3 us, quantiser of 8192 x 4000 bf16 20.9 to 17.4, product
-// 2000 x 16000 x 512 to bf16 40.2 to 34.0).
-template <typename T, int W> __device__ inline void store_pack(T *p, const Pack<T, W> &x)
+// Results leave this way where whole lines do: they are written once, and the caches serve the
+// operands instead (gradient of 511 x 32001 f32 27.4 to 22.3 us, quantiser of 8192 x 4000 bf16 20.9 to
+// 17.4).
+template <typename T, int W> __device__ inline void store_pack_stream(T *p, const Pack<T, W> &x)
 {
     typedef typename Bits<sizeof(T) * W>::type B;
     typedef B __attribute__((aligned(alignof(T)))) unaligned;
     __builtin_nontemporal_store(__builtin_bit_cast(B, x), reinterpret_cast<unaligned *>(p));
+}
+template <typename T, int W> __device__ inline void store_pack(T *p, const Pack<T, W> &x)
+{
+    *reinterpret_cast<Pack<T, W> *>(p) = x;
 }
 
 }  // namespace
