@@ -220,7 +220,8 @@ def quantized(x):
 
 @pytest.mark.parametrize("M,K", [(1, 1), (1, 7), (3, 64), (5, 100), (2, 1000), (17, 2048),
                                  (4, 4097), (3, 8192), (300, 515), (2, 20011), (1, 70000),
-                                 (2000, 33), (5, 0)])
+                                 (2000, 33), (5, 0), (70, 64),
+                                 (33, 127), (65, 255), (130, 512), (9, 1030), (600, 9000), (520, 16383)])
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (3, 1)])
 def test_quantize(torch, M, K, dt, pad, offset):
