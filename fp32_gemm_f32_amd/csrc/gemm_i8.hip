@@ -180,6 +180,19 @@ bool shape_in_limits(int M, int N, int K, int64_t lda, int64_t ldb)
     return K <= kMaxK && lda < kMaxLd && ldb < kMaxLd && tiles < (int64_t(1) << 30);
 }
 
+// t / d == mulhi(t, mul) >> shift for t < 2^31 and 2^shift < d <= 2^(shift + 1): mul = 2^(32 + shift) / d
+// rounded up is too large by less than 1, which adds less than t / 2^(32 + shift) < 1 / d to t / d.
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+Divisor divisor(uint32_t d)
+{
+    int shift = 0;
+    while ((uint64_t(2) << shift) < d) ++shift;
+    return {uint32_t(((uint64_t(1) << (32 + shift)) + d - 1) / d), shift};
+}
+
 unsigned element_blocks(int64_t total)
 {
     return unsigned(std::min<int64_t>((total + 255) / 256, 16384));
@@ -302,6 +315,8 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     p.partial = static_cast<int *>(workspace);
     p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
     p.splits = plan.splits; p.k_chunk = plan.splits > 1 ? plan.k_chunk : p.K;
+    const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(plan.tiles_n));
+    p.group_mul = d.mul; p.group_shift = d.shift;
     st = launch(plan.kernel, dim3(unsigned(int64_t(plan.tiles_m) * plan.tiles_n * plan.splits)),
                 dim3(plan.v->threads), stream, p);
     if (st != SGEMM_OK || plan.splits == 1) return st;

@@ -26,6 +26,8 @@ struct I8Args {
     int M, N, K;
     int c_dtype;
     int tiles_m, tiles_n;
+    uint32_t group_mul;    // division by kGroupM * tiles_n without dividing: see i8_tile
+    int group_shift;
     int splits, k_chunk;   // split s covers k in [s * k_chunk, min(K, (s + 1) * k_chunk))
     bool stream;           // C's rows start on lines of 64 bytes: store past the caches
 };
@@ -94,6 +96,8 @@ template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Til
     static constexpr int STEPS = BK / 32;            // MFMA steps per panel
     static constexpr int ACH = BM * CPR / NT, BCH = BN * CPR / NT;   // chunks per thread
     static constexpr int A_BYTES = BM * BK, STAGE = (BM + BN) * BK;
+    static constexpr int SN = (BN + 63) / 64 * 64;   // floats B's scales take in LDS, and the bias
+    static_assert(BM % 64 == 0, "A's scales are loaded 64 at a time");
     static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
     static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
 };
@@ -158,7 +162,8 @@ __device__ inline i32x4 load_tail(const int8_t *row, int k, int kn)
 // wave's share.
 template <typename T>
 __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)[T::RB][T::CB],
-                                            int m0, int n0, int split, int wm, int wn)
+                                            const float *scales, int m0, int n0, int split, int wm,
+                                            int wn)
 {
     const int frow = threadIdx.x & 31, fhi = (threadIdx.x & 63) >> 5;
     const int col = n0 + wn * T::WN + T::CB * frow;
@@ -179,19 +184,18 @@ __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)
             }
         return;
     }
-    float sb[T::CB], bias[T::CB];
+    // the scales and the bias wait in LDS: A's of the tile's rows, B's of its columns, the bias
+    float sa[T::RB][16], sb[T::CB], bias[T::CB];
+    const float *sbs = scales + T::BM + wn * T::WN + T::CB * frow;
 #pragma unroll
     for (int j = 0; j < T::CB; ++j) {
-        const int n = min(col + j, p.N - 1);
-        sb[j] = p.sb[n];
-        bias[j] = p.bias ? p.bias[n] : 0.0f;
+        sb[j] = sbs[j];
+        bias[j] = p.bias ? sbs[T::SN + j] : 0.0f;
     }
-    // all of the rows' scales ahead of the stores: one wait instead of one a row
-    float sa[T::RB][16];
 #pragma unroll
     for (int i = 0; i < T::RB; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) sa[i][v] = p.sa[min(row0 + 32 * i + 8 * (v / 4) + v % 4, p.M - 1)];
+        for (int v = 0; v < 16; ++v) sa[i][v] = scales[wm * T::WM + 4 * fhi + 32 * i + 8 * (v / 4) + v % 4];
     auto store_all = [&](auto dt, auto stream) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
@@ -229,19 +233,46 @@ __device__ __forceinline__ void i8_load16_lds(const int8_t *base, uint32_t range
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 16, off, 0, 0, 0);
 }
 
+// 64 floats from base + first to LDS, at `to` + 4 lanes: zeros from `count` on.
+__device__ __forceinline__ void i8_load_floats(const float *base, int first, int count, int lane, char *to)
+{
+    const auto rsrc = make_rsrc32(base, uint32_t(max(count, 0)) * 4u);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 4, (first + lane) * 4, 0, 0, 0);
+}
+
+// The tile of workgroup bid, in tile_coords' order. Divisions by numbers the host knows are a
+// product's upper half and a shift there (exact below 2^31): a division takes some 200 cycles that
+// nothing covers at a kernel's start.
+__device__ inline void i8_tile(const I8Args &p, int bid, int &tm, int &tn)
+{
+    const int t = xcd_contiguous(bid, p.tiles_m * p.tiles_n);
+    const int g = int(__umulhi(uint32_t(t), p.group_mul) >> p.group_shift);
+    const int w = t - g * kGroupM * p.tiles_n, first = g * kGroupM;
+    const int rows = min(p.tiles_m - first, kGroupM);
+    static_assert(kGroupM == 8, "whole groups are divided by shifts");
+    if (rows == kGroupM) {
+        tm = first + w % kGroupM;
+        tn = w / kGroupM;
+    } else {
+        tm = first + w % rows;
+        tn = w / rows;
+    }
+}
+
 template <typename T, bool ANY>
 __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
 {
     constexpr int STAGE = T::STAGE;
-    static_assert(T::NSTG >= 2 && T::NSTG * STAGE <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * STAGE];
+    constexpr int SCALES = (T::BM + 2 * T::SN) * 4;
+    static_assert(T::NSTG >= 2 && T::NSTG * STAGE + SCALES <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * STAGE + SCALES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / T::WGN, wn = wave % T::WGN;
     const int tiles = p.tiles_m * p.tiles_n;
-    const int split = blockIdx.x / tiles;
+    const int split = p.splits == 1 ? 0 : int(blockIdx.x) / tiles;
     int tm, tn;
-    tile_coords(blockIdx.x - split * tiles, p.tiles_m, p.tiles_n, tm, tn);
+    i8_tile(p, int(blockIdx.x) - split * tiles, tm, tn);
     const int m0 = tm * T::BM, n0 = tn * T::BN;
     const int k0 = split * p.k_chunk, k1 = min(p.K, k0 + p.k_chunk);
     const int panels = (k1 - k0 + T::BK - 1) / T::BK;
@@ -355,6 +386,16 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     // first operands are read under the last steps' MFMAs.
     constexpr int LPP = T::ACH + T::BCH;
     constexpr int LOOK = ANY ? 2 : 1;
+    // ahead of the panels, so that the first wait covers them: the epilogue's scales and bias (1024^3
+    // 6.2 to 5.7 us against loading them there)
+    char *const scales = smem + T::NSTG * STAGE;
+    for (int i = wave; p.splits == 1 && i < (T::BM + 2 * T::SN) / 64; i += T::NT / 64) {
+        char *to = scales + i * 256;
+        const int at = i * 64;
+        if (at < T::BM) i8_load_floats(p.sa + m0, at, min(p.M - m0, T::BM), lane, to);
+        else if (at < T::BM + T::SN) i8_load_floats(p.sb + n0, at - T::BM, min(p.N - n0, T::BN), lane, to);
+        else if (p.bias) i8_load_floats(p.bias + n0, at - T::BM - T::SN, min(p.N - n0, T::BN), lane, to);
+    }
 #pragma unroll
     for (int i = 0; i < T::NSTG; ++i) issue(i);
     wait_vmcnt<(T::NSTG - 1) * LPP>();
@@ -398,7 +439,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     if constexpr (ANY)
         if (full < panels) run(full, std::true_type{});
     wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
-    i8_epilogue<T>(p, acc, m0, n0, split, wm, wn);
+    i8_epilogue<T>(p, acc, reinterpret_cast<const float *>(scales), m0, n0, split, wm, wn);
 }
 
 // ------------------------------------------------------------------ rows put in place ---

