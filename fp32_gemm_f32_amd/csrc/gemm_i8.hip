@@ -23,39 +23,55 @@ typedef void (*I8Kernel)(I8Args);
 
 // The tiles, smallest first. In microseconds: `c1` and `c2` are a panel of 128 with one and (where
 // LDS holds two) two workgroups on every compute unit, `ends` a workgroup's start and stores. They
-// and the constants of make_plan were fitted to the times of every tile and split of 239 products
-// drawn over M of 17 to 8192 and N, K of 64 to 16384, so that the plan's choice costs least: 1.3 %
-// more than the best of each on average, 18 % at most.
+// and the constants of make_plan were fitted to the times of every tile and split of 438 products
+// drawn over M of 17 to 8192 and N, K of 64 to 16384, so that the plan's choice costs least: 1.6 %
+// more than the best of each on average, 21 % at most (fitted to half of them, 2.1 % on the others).
+// Eight waves serve a tile better than four where one workgroup has a compute unit (2048^3 with
+// 128 x 128: 18.2 and 16.5 us at 2 stages), and 4 stages better than 2 there (13.4); in the form for
+// any rows each wave joins its own operands' words, and more waves join more (4096 x 4096 x 4097 with
+// 128 x 128 and 2 stages: 103 and 108). Tiles and rings whose going costs 0.2 % in all over the
+// drawn products are not here.
 struct I8Variant {
     const char *name;
-    I8Kernel aligned, any;
+    I8Kernel kernel;
     int bm, bn, threads;
     double c1, c2, ends;
 };
 
-template <int BM, int BN, int WGM, int WGN, int NSTG>
+template <int BM, int BN, int WGM, int WGN, int NSTG, bool ANY>
 constexpr I8Variant tile(const char *name, double c1, double c2, double ends)
 {
     typedef I8Tile<BM, BN, WGM, WGN, 128, NSTG> T;
-    return {name, &k_gemm_i8<T, false>, &k_gemm_i8<T, true>, BM, BN, T::NT, c1, c2, ends};
+    return {name, &k_gemm_i8<T, ANY>, BM, BN, T::NT, c1, c2, ends};
 }
 
-const I8Variant kVariants[] = {
-    tile<64, 32, 2, 1, 6>("i8_64x32", 0.18, 0.32, 2.6),
-    tile<64, 64, 2, 2, 4>("i8_64x64", 0.18, 0.40, 3.1),
-    tile<64, 128, 2, 2, 3>("i8_64x128", 0.25, 0.64, 3.2),
-    tile<128, 128, 2, 2, 2>("i8_128x128", 0.73, 0.82, 2.9),
-    tile<128, 256, 2, 4, 3>("i8_128x256", 0.74, 0.0, 3.6),
-    tile<256, 256, 4, 2, 2>("i8_256x256", 1.32, 0.0, 3.7),
+const I8Variant kAligned[] = {
+    tile<64, 32, 2, 1, 6, false>("i8_64x32", 0.192, 0.29, 2.6),
+    tile<64, 64, 2, 2, 4, false>("i8_64x64", 0.188, 0.39, 2.7),
+    tile<64, 128, 2, 4, 3, false>("i8_64x128_w8", 0.256, 0.61, 2.8),
+    tile<128, 128, 4, 2, 2, false>("i8_128x128", 0.563, 1.04, 2.3),
+    tile<128, 128, 4, 2, 4, false>("i8_128x128_s4", 0.50, 0.0, 2.7),
+    tile<128, 256, 2, 4, 3, false>("i8_128x256", 0.73, 0.0, 4.3),
+    tile<192, 256, 2, 4, 2, false>("i8_192x256", 1.03, 0.0, 4.7),
+    tile<256, 256, 4, 2, 2, false>("i8_256x256", 1.13, 0.0, 5.8),
+};
+const I8Variant kAny[] = {
+    tile<64, 32, 2, 1, 6, true>("i8_64x32", 0.316, 0.50, 2.5),
+    tile<64, 64, 2, 2, 4, true>("i8_64x64", 0.438, 0.65, 2.8),
+    tile<64, 128, 2, 2, 3, true>("i8_64x128", 0.427, 0.876, 3.1),
+    tile<64, 128, 2, 4, 3, true>("i8_64x128_w8", 0.433, 0.889, 3.05),
+    tile<128, 128, 4, 2, 4, true>("i8_128x128_s4", 0.70, 0.0, 3.35),
+    tile<192, 128, 2, 4, 3, true>("i8_192x128", 0.715, 0.0, 4.25),
+    tile<192, 256, 2, 4, 2, true>("i8_192x256", 1.36, 0.0, 5.7),
+    tile<256, 256, 4, 2, 2, true>("i8_256x256", 1.47, 0.0, 5.05),
 };
 // Few rows: 16 rows, all of K to a workgroup.
-const I8Variant kFewRows = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 1, 8, 4, true>>,
-                            &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 16, 512, 0.0, 0.0, 0.0};
+const I8Variant kRowsAligned = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 1, 8, 4, true>>, 16, 16, 512, 0.0, 0.0, 0.0};
+const I8Variant kRowsAny = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 32, 512, 0.0, 0.0, 0.0};
 
 struct I8Plan {
     const I8Variant *v;
-    I8Kernel kernel;
-    int bm, bn;
+    bool any;
     int tiles_m, tiles_n, splits, k_chunk;
     bool copy_a, copy_b;
     double cost;
@@ -75,8 +91,8 @@ I8Layout layout_of(int K, const void *A, int64_t lda, const void *B, int64_t ldb
     return {ok(A, lda), ok(B, ldb)};
 }
 
-constexpr double kLaunch = 1.6;          // us: a kernel's start and end
-constexpr double kStreamPerUs = 6.8e6;   // bytes of operands, from the last-level cache too
+constexpr double kLaunch = 2.0;          // us: a kernel's start and end
+constexpr double kStreamPerUs = 6.0e6;   // bytes of operands, from the last-level cache too
 constexpr double kMostCopied = 4.0e9;    // bytes of workspace a copy may ask for
 
 struct Rounds {
@@ -93,7 +109,7 @@ double tile_cost(const I8Variant &v, const Rounds &r, int64_t panels, int cus)
 {
     const double whole = v.c2 > 0 ? v.c2 : v.c1;
     const double tail = r.rest == 0 ? 0.0 : r.rest <= cus ? v.c1 : v.c2;
-    return (double(r.full) * whole + tail) * (double(panels) + 3.4) + double(r.all()) * v.ends;
+    return (double(r.full) * whole + tail) * (double(panels) + 1.25) + double(r.all()) * v.ends;
 }
 
 // The cheapest of: every tile, K whole or split; rows as they are, in the slower form for any
@@ -115,46 +131,41 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         return std::pair<int, int>(int(ceil_div(K, chunk)), int(std::min<int64_t>(chunk, K)));
     };
     const auto join_cost = [&](int splits) {
-        return splits == 1 ? 0.0 : 2.4 + double(splits + 1) * M * N * 4 / 2.5e6;
+        return splits == 1 ? 0.0 : 2.5 + double(splits + 1) * M * N * 4 / 2.6e6;
     };
     const int most = workspace ? int(std::min<int64_t>(16, std::max<int64_t>(1, panels / 4))) : 1;
     if (M <= 16) {
         // 8 waves share K in panels of 256 (128 in the form for any rows)
-        const int bn = any ? 32 : 16;
+        const I8Variant &v = any ? kRowsAny : kRowsAligned;
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
-            const int64_t groups = ceil_div(N, bn) * s;
+            const int64_t groups = ceil_div(N, v.bn) * s;
             // a panel of every wave takes this long when little else is in flight
             const double turn = any ? double(ceil_div(chunk, 1024)) * 1.4 : double(ceil_div(chunk, 2048)) * 0.8;
             const double step = double(ceil_div(groups, 2 * cus)) * turn;
             const double cost = kLaunch + 1.0 + std::max(step, bytes / 4.6e6 * (any ? 1.25 : 1.0)) +
                                 join_cost(s);
-            offer({&kFewRows, any ? kFewRows.any : kFewRows.aligned, 16, bn, 1,
-                   int(ceil_div(N, bn)), s, chunk, false, false, cost});
+            offer({&v, any, 1, int(ceil_div(N, v.bn)), s, chunk, false, false, cost});
         }
         return best;
     }
-    for (const I8Variant &v : kVariants) {
+    const auto offer_tile = [&](const I8Variant &v, bool in_any_form) {
+        const bool copies = any && !in_any_form;
         const int64_t tm = ceil_div(M, v.bm), tn = ceil_div(N, v.bn);
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             if (s > 1 && tm * tn * s > 2 * int64_t(cus)) break;
-            const int64_t depth = ceil_div(chunk, 128);
             const Rounds r = rounds_of(v, tm * tn * s, cus);
-            const double body = std::max(tile_cost(v, r, depth, cus), bytes / kStreamPerUs);
-            I8Plan p{&v, any ? v.any : v.aligned, v.bm, v.bn, int(tm), int(tn), s, chunk, false, false,
-                     kLaunch + body + join_cost(s)};
-            if (any) p.cost += 0.09 * body + 0.15 * double(depth) * double(r.all());
-            offer(p);
-            if (any && workspace && copied <= kMostCopied) {
-                p.kernel = v.aligned;
-                p.copy_a = !rows.a;
-                p.copy_b = !rows.b;
-                p.cost = kLaunch + body + join_cost(s) + 4.7 + 2.0 * copied / 5.9e6;
-                offer(p);
-            }
+            const double work = tile_cost(v, r, ceil_div(chunk, 128), cus), reads = bytes / kStreamPerUs;
+            const double body = std::max(work, reads) + 0.02 * std::min(work, reads);   // reads alone tie
+            offer({&v, in_any_form, int(tm), int(tn), s, chunk, copies && !rows.a, copies && !rows.b,
+                   kLaunch + body + join_cost(s) + (copies ? 5.0 + 2.0 * copied / 5.9e6 : 0.0)});
         }
-    }
+    };
+    if (!any || (workspace && copied <= kMostCopied))
+        for (const I8Variant &v : kAligned) offer_tile(v, false);
+    if (any)
+        for (const I8Variant &v : kAny) offer_tile(v, true);
     return best;
 }
 
@@ -317,7 +328,7 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     p.splits = plan.splits; p.k_chunk = plan.splits > 1 ? plan.k_chunk : p.K;
     const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(plan.tiles_n));
     p.group_mul = d.mul; p.group_shift = d.shift;
-    st = launch(plan.kernel, dim3(unsigned(int64_t(plan.tiles_m) * plan.tiles_n * plan.splits)),
+    st = launch(plan.v->kernel, dim3(unsigned(int64_t(plan.tiles_m) * plan.tiles_n * plan.splits)),
                 dim3(plan.v->threads), stream, p);
     if (st != SGEMM_OK || plan.splits == 1) return st;
     return launch(&k_gemm_i8_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
@@ -340,8 +351,8 @@ extern "C" int gemm_i8_plan_describe(int M, int N, int K, int64_t lda, int64_t l
                            "{\"name\": \"%s\", \"form\": \"%s\", \"copies\": [%s, %s], \"BM\": %d, "
                            "\"BN\": %d, \"threads\": %d, \"tiles\": [%d, %d], \"splits\": %d, "
                            "\"k_chunk\": %d, \"cost_us\": %.2f, \"workspace_bytes\": %lld}",
-                           p.v->name, p.kernel == p.v->aligned ? "aligned" : "any",
-                           p.copy_a ? "true" : "false", p.copy_b ? "true" : "false", p.bm, p.bn,
+                           p.v->name, p.any ? "any" : "aligned",
+                           p.copy_a ? "true" : "false", p.copy_b ? "true" : "false", p.v->bm, p.v->bn,
                            p.v->threads, p.tiles_m, p.tiles_n, p.splits, p.k_chunk, p.cost,
                            static_cast<long long>(space_of(p, M, N, K).bytes));
     return n < buflen ? SGEMM_OK : SGEMM_EINVAL_ARG;

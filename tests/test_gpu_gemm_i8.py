@@ -99,6 +99,43 @@ def test_product(torch, M, N, K, out):
     assert_guard(raw, C, M, N, N + 3)
 
 
+TILES = [("i8_64x32", "aligned", 19, 64, 672), ("i8_64x32", "any", 19, 65, 682),
+         ("i8_64x64", "aligned", 66, 4160, 672), ("i8_64x64", "any", 65, 4112, 759),
+         ("i8_64x128", "any", 4184, 195, 949),
+         ("i8_64x128_w8", "aligned", 197, 4250, 672), ("i8_64x128_w8", "any", 196, 4264, 664),
+         ("i8_128x128", "aligned", 4807, 1569, 672),
+         ("i8_128x128_s4", "aligned", 387, 4695, 688), ("i8_128x128_s4", "any", 4714, 399, 668),
+         ("i8_192x128", "any", 3618, 1029, 700), ("i8_128x256", "aligned", 4687, 772, 736),
+         ("i8_192x256", "aligned", 4638, 1684, 688), ("i8_192x256", "any", 3692, 1561, 665),
+         ("i8_256x256", "aligned", 4573, 2613, 672), ("i8_256x256", "any", 3676, 3101, 655)]
+
+
+@pytest.mark.parametrize("name,form,M,N,K", TILES)
+def test_every_tile(torch, name, form, M, N, K):
+    """A product for each tile of the plan (at 256 compute units), with edges in both
+    directions and a ring of panels that turns over."""
+    d = g.gemm_i8_plan_describe(M, N, K, num_cus=256)
+    assert (d["name"], d["form"], d["copies"]) == (name, form, [False, False])
+    rng = np.random.default_rng(M + N + K)
+    A, B = codes(rng, M, K), codes(rng, N, K)
+    sa = rng.uniform(1e-4, 1e-2, M).astype(np.float32)
+    sb = rng.uniform(1e-4, 1e-2, N).astype(np.float32)
+    bias = rng.standard_normal(N).astype(np.float32)
+    dA, dB = torch.from_numpy(A).cuda(), torch.from_numpy(B).cuda()
+    dsa, dsb, dbias = (torch.from_numpy(x).cuda() for x in (sa, sb, bias))
+    raw, C = guarded(torch, M, N, N + 1, torch.float32)
+    print(f"[i8] {name} {form} {M}x{N}x{K}", flush=True)
+    g.matmul_i8(dA, dsa, dB, dsb, bias=dbias, out=C)
+    torch.cuda.synchronize()
+    # sums of K products stay far below 2^53: exact in 64-bit floats
+    scaled = (A.astype(np.float64) @ B.astype(np.float64).T) * sa.astype(np.float64)[:, None] * sb
+    ref = scaled + bias
+    tol = 4 * U32 * (np.abs(scaled) + np.abs(bias)) + U32 * np.abs(ref) * (1 + 4 * U32)
+    worst = np.max(np.abs(C.cpu().numpy() - ref) - tol)
+    assert worst <= 0, f"off by {worst} more than the roundings"
+    assert_guard(raw, C, M, N, N + 1)
+
+
 @pytest.mark.parametrize("M,N,K,lda,ldb,ao,bo", [
     (70, 90, 256, 272, 260, 0, 0),        # aligned rows with padding: the direct loads
     (70, 90, 256, 257, 259, 0, 0),        # odd strides
