@@ -21,11 +21,12 @@ constexpr int kWorkspaceAlign = 16;
 
 typedef void (*I8Kernel)(I8Args);
 
-// The tiles, smallest first. In microseconds: `c1` and `c2` are a panel of 128 with one and (where
-// LDS holds two) two workgroups on every compute unit, `ends` a workgroup's start and stores. They
-// and the constants of make_plan were fitted to the times of every tile and split of 438 products
-// drawn over M of 17 to 8192 and N, K of 64 to 16384, so that the plan's choice costs least: 1.6 %
-// more than the best of each on average, 21 % at most (fitted to half of them, 2.1 % on the others).
+// The tiles, smallest first. In microseconds: `c1` and `c2` are a panel of 128 with one and two
+// workgroups on every compute unit, `ends` a workgroup's start and stores, `next` what each further
+// tile of a workgroup that goes on adds to its panels (its stores, mostly). They and the
+// constants of make_plan were fitted to the times of every tile and split of 577 products drawn over
+// M of 17 to 16384 and N, K of 64 to 16384, so that the plan's choice costs least: 1.4 % more than
+// the best of each on average, 17 % at most (an earlier fit to 219 of them: 2.1 % on 219 others).
 // Eight waves serve a tile better than four where one workgroup has a compute unit (2048^3 with
 // 128 x 128: 18.2 and 16.5 us at 2 stages), and 4 stages better than 2 there (13.4); in the form for
 // any rows each wave joins its own operands' words, and more waves join more (4096 x 4096 x 4097 with
@@ -35,39 +36,41 @@ struct I8Variant {
     const char *name;
     I8Kernel kernel;
     int bm, bn, threads;
-    double c1, c2, ends;
+    int at_once;     // workgroups on a compute unit
+    int loop;        // panels from which a workgroup goes on to another tile, or 0
+    double c1, c2, ends, next;
 };
 
 template <int BM, int BN, int WGM, int WGN, int NSTG, bool ANY>
-constexpr I8Variant tile(const char *name, double c1, double c2, double ends)
+constexpr I8Variant tile(const char *name, double c1, double c2, double ends, double next)
 {
     typedef I8Tile<BM, BN, WGM, WGN, 128, NSTG> T;
-    return {name, &k_gemm_i8<T, ANY>, BM, BN, T::NT, c1, c2, ends};
+    return {name, &k_gemm_i8<T, ANY>, BM, BN, T::NT, T::LOOP ? 1 : 2, T::LOOP && !ANY ? NSTG : 0, c1, c2, ends, next};
 }
 
 const I8Variant kAligned[] = {
-    tile<64, 32, 2, 1, 6, false>("i8_64x32", 0.192, 0.29, 2.6),
-    tile<64, 64, 2, 2, 4, false>("i8_64x64", 0.188, 0.39, 2.7),
-    tile<64, 128, 2, 4, 3, false>("i8_64x128_w8", 0.256, 0.61, 2.8),
-    tile<128, 128, 4, 2, 2, false>("i8_128x128", 0.563, 1.04, 2.3),
-    tile<128, 128, 4, 2, 4, false>("i8_128x128_s4", 0.50, 0.0, 2.7),
-    tile<128, 256, 2, 4, 3, false>("i8_128x256", 0.73, 0.0, 4.3),
-    tile<192, 256, 2, 4, 2, false>("i8_192x256", 1.03, 0.0, 4.7),
-    tile<256, 256, 4, 2, 2, false>("i8_256x256", 1.13, 0.0, 5.8),
+    tile<64, 32, 2, 1, 6, false>("i8_64x32", 0.189, 0.27, 2.31, 0.0),
+    tile<64, 64, 2, 2, 4, false>("i8_64x64", 0.200, 0.37, 1.84, 0.0),
+    tile<64, 128, 2, 4, 3, false>("i8_64x128_w8", 0.298, 0.52, 2.17, 0.0),
+    tile<128, 128, 4, 2, 2, false>("i8_128x128", 0.506, 0.95, 1.19, 0.0),
+    tile<128, 128, 4, 2, 4, false>("i8_128x128_s4", 0.408, 0.0, 2.04, 3.76),
+    tile<128, 256, 2, 4, 3, false>("i8_128x256", 0.644, 0.0, 2.83, 7.49),
+    tile<192, 256, 2, 4, 2, false>("i8_192x256", 0.962, 0.0, 3.46, 8.19),
+    tile<256, 256, 4, 2, 2, false>("i8_256x256", 1.125, 0.0, 2.20, 7.80),
 };
 const I8Variant kAny[] = {
-    tile<64, 32, 2, 1, 6, true>("i8_64x32", 0.316, 0.50, 2.5),
-    tile<64, 64, 2, 2, 4, true>("i8_64x64", 0.438, 0.65, 2.8),
-    tile<64, 128, 2, 2, 3, true>("i8_64x128", 0.427, 0.876, 3.1),
-    tile<64, 128, 2, 4, 3, true>("i8_64x128_w8", 0.433, 0.889, 3.05),
-    tile<128, 128, 4, 2, 4, true>("i8_128x128_s4", 0.70, 0.0, 3.35),
-    tile<192, 128, 2, 4, 3, true>("i8_192x128", 0.715, 0.0, 4.25),
-    tile<192, 256, 2, 4, 2, true>("i8_192x256", 1.36, 0.0, 5.7),
-    tile<256, 256, 4, 2, 2, true>("i8_256x256", 1.47, 0.0, 5.05),
+    tile<64, 32, 2, 1, 6, true>("i8_64x32", 0.285, 0.46, 1.80, 0.0),
+    tile<64, 64, 2, 2, 4, true>("i8_64x64", 0.368, 0.62, 1.85, 0.0),
+    tile<64, 128, 2, 2, 3, true>("i8_64x128", 0.418, 0.75, 2.19, 0.0),
+    tile<64, 128, 2, 4, 3, true>("i8_64x128_w8", 0.449, 0.78, 1.86, 0.0),
+    tile<128, 128, 4, 2, 4, true>("i8_128x128_s4", 0.631, 0.0, 2.33, 0.0),
+    tile<192, 128, 2, 4, 3, true>("i8_192x128", 0.709, 0.0, 2.92, 0.0),
+    tile<192, 256, 2, 4, 2, true>("i8_192x256", 1.349, 0.0, 3.69, 0.0),
+    tile<256, 256, 4, 2, 2, true>("i8_256x256", 1.544, 0.0, 2.56, 0.0),
 };
 // Few rows: 16 rows, all of K to a workgroup.
-const I8Variant kRowsAligned = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 1, 8, 4, true>>, 16, 16, 512, 0.0, 0.0, 0.0};
-const I8Variant kRowsAny = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 32, 512, 0.0, 0.0, 0.0};
+const I8Variant kRowsAligned = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 1, 8, 4, true>>, 16, 16, 512, 2, 0, 0.0, 0.0, 0.0, 0.0};
+const I8Variant kRowsAny = {"i8_rows16", &k_gemm_i8_rows<I8Rows<1, 2, 8, 2, false>>, 16, 32, 512, 2, 0, 0.0, 0.0, 0.0, 0.0};
 
 struct I8Plan {
     const I8Variant *v;
@@ -91,25 +94,25 @@ I8Layout layout_of(int K, const void *A, int64_t lda, const void *B, int64_t ldb
     return {ok(A, lda), ok(B, ldb)};
 }
 
-constexpr double kLaunch = 2.0;          // us: a kernel's start and end
-constexpr double kStreamPerUs = 6.0e6;   // bytes of operands, from the last-level cache too
+constexpr double kLaunch = 2.5;          // us: a kernel's start and end
+constexpr double kStreamPerUs = 6.4e6;   // bytes of operands, from the last-level cache too
 constexpr double kMostCopied = 4.0e9;    // bytes of workspace a copy may ask for
 
-struct Rounds {
-    int64_t full, rest;      // whole rounds of workgroups on every compute unit, what is left
-    int64_t all() const { return full + (rest > 0); }
-};
-Rounds rounds_of(const I8Variant &v, int64_t groups, int cus)
+// Whether workgroups go on to another tile, one to a compute unit.
+bool goes_on(const I8Variant &v, int64_t tiles, int splits, int64_t panels, int cus)
 {
-    const int64_t at_once = int64_t(cus) * (v.c2 > 0 ? 2 : 1);
-    return {groups / at_once, groups % at_once};
+    return splits == 1 && v.loop > 0 && panels >= v.loop && tiles > cus;
 }
-// Microseconds of rounds of workgroups of `panels` panels each.
-double tile_cost(const I8Variant &v, const Rounds &r, int64_t panels, int cus)
+// Microseconds of workgroups of `panels` panels each: whole rounds of them and what is left.
+double tile_cost(const I8Variant &v, int64_t groups, int splits, int64_t panels, int cus)
 {
-    const double whole = v.c2 > 0 ? v.c2 : v.c1;
-    const double tail = r.rest == 0 ? 0.0 : r.rest <= cus ? v.c1 : v.c2;
-    return (double(r.full) * whole + tail) * (double(panels) + 1.25) + double(r.all()) * v.ends;
+    const int64_t full = groups / (cus * v.at_once), rest = groups % (cus * v.at_once);
+    const int64_t rounds = full + (rest > 0);
+    if (goes_on(v, groups, splits, panels, cus))
+        return v.c1 * (double(rounds * panels) + 2.7) + v.ends + double(rounds - 1) * v.next;
+    const double whole = v.at_once == 2 ? v.c2 : v.c1;
+    const double tail = rest == 0 ? 0.0 : rest <= cus ? v.c1 : v.c2;
+    return (double(full) * whole + tail) * (double(panels) + 2.7) + double(rounds) * v.ends;
 }
 
 // The cheapest of: every tile, K whole or split; rows as they are, in the slower form for any
@@ -131,7 +134,7 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         return std::pair<int, int>(int(ceil_div(K, chunk)), int(std::min<int64_t>(chunk, K)));
     };
     const auto join_cost = [&](int splits) {
-        return splits == 1 ? 0.0 : 2.5 + double(splits + 1) * M * N * 4 / 2.6e6;
+        return splits == 1 ? 0.0 : 2.3 + double(splits + 1) * M * N * 4 / 1.9e6;
     };
     const int most = workspace ? int(std::min<int64_t>(16, std::max<int64_t>(1, panels / 4))) : 1;
     if (M <= 16) {
@@ -155,11 +158,10 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             if (s > 1 && tm * tn * s > 2 * int64_t(cus)) break;
-            const Rounds r = rounds_of(v, tm * tn * s, cus);
-            const double work = tile_cost(v, r, ceil_div(chunk, 128), cus), reads = bytes / kStreamPerUs;
+            const double work = tile_cost(v, tm * tn * s, s, ceil_div(chunk, 128), cus), reads = bytes / kStreamPerUs;
             const double body = std::max(work, reads) + 0.02 * std::min(work, reads);   // reads alone tie
             offer({&v, in_any_form, int(tm), int(tn), s, chunk, copies && !rows.a, copies && !rows.b,
-                   kLaunch + body + join_cost(s) + (copies ? 5.0 + 2.0 * copied / 5.9e6 : 0.0)});
+                   kLaunch + body + join_cost(s) + (copies ? 4.6 + 2.0 * copied / 6.8e6 : 0.0)});
         }
     };
     if (!any || (workspace && copied <= kMostCopied))
@@ -328,8 +330,9 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     p.splits = plan.splits; p.k_chunk = plan.splits > 1 ? plan.k_chunk : p.K;
     const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(plan.tiles_n));
     p.group_mul = d.mul; p.group_shift = d.shift;
-    st = launch(plan.v->kernel, dim3(unsigned(int64_t(plan.tiles_m) * plan.tiles_n * plan.splits)),
-                dim3(plan.v->threads), stream, p);
+    int64_t groups = int64_t(plan.tiles_m) * plan.tiles_n * plan.splits;
+    if (goes_on(*plan.v, groups, plan.splits, ceil_div(K, 128), cus)) groups = cus;
+    st = launch(plan.v->kernel, dim3(unsigned(groups)), dim3(plan.v->threads), stream, p);
     if (st != SGEMM_OK || plan.splits == 1) return st;
     return launch(&k_gemm_i8_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 }

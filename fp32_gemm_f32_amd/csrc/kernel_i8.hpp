@@ -97,6 +97,8 @@ template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Til
     static constexpr int ACH = BM * CPR / NT, BCH = BN * CPR / NT;   // chunks per thread
     static constexpr int A_BYTES = BM * BK, STAGE = (BM + BN) * BK;
     static constexpr int SN = (BN + 63) / 64 * 64;   // floats B's scales take in LDS, and the bias
+    // one workgroup to a compute unit: it goes on to another tile
+    static constexpr bool LOOP = NSTG * STAGE > 80 * 1024;
     static_assert(BM % 64 == 0, "A's scales are loaded 64 at a time");
     static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
     static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
@@ -264,40 +266,50 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
 {
     constexpr int STAGE = T::STAGE;
     constexpr int SCALES = (T::BM + 2 * T::SN) * 4;
-    static_assert(T::NSTG >= 2 && T::NSTG * STAGE + SCALES <= 160 * 1024, "LDS");
-    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * STAGE + SCALES];
+    constexpr bool LOOP = T::LOOP && !ANY;
+    static_assert(T::NSTG >= 2 && T::NSTG * STAGE + (LOOP ? 2 : 1) * SCALES <= 160 * 1024, "LDS");
+    __shared__ __attribute__((aligned(16))) char smem[T::NSTG * STAGE + (LOOP ? 2 : 1) * SCALES];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / T::WGN, wn = wave % T::WGN;
     const int tiles = p.tiles_m * p.tiles_n;
     const int split = p.splits == 1 ? 0 : int(blockIdx.x) / tiles;
-    int tm, tn;
-    i8_tile(p, int(blockIdx.x) - split * tiles, tm, tn);
-    const int m0 = tm * T::BM, n0 = tn * T::BN;
     const int k0 = split * p.k_chunk, k1 = min(p.K, k0 + p.k_chunk);
     const int panels = (k1 - k0 + T::BK - 1) / T::BK;
     const int kn = k1 - k0;                          // values of k in this split
-    const int8_t *At = p.A + m0 * p.lda + k0;
-    const int8_t *Bt = p.B + n0 * p.ldb + k0;
-    const uint32_t a_low = ANY ? uint32_t(reinterpret_cast<uintptr_t>(At)) & 3 : 0;
-    const uint32_t b_low = ANY ? uint32_t(reinterpret_cast<uintptr_t>(Bt)) & 3 : 0;
-    At -= a_low;
-    Bt -= b_low;
 
-    // this thread's chunks: LDS chunk i * NT + tid
+    // the tile that loads go to: this thread's chunks, LDS chunk i * NT + tid
     const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
     const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
-    uint32_t a_off[T::ACH], b_off[T::BCH];
+    int m0, n0;
+    const int8_t *At, *Bt;
+    uint32_t a_low = 0, b_low = 0, a_off[T::ACH], b_off[T::BCH];
+    auto aim = [&](int tile) __attribute__((always_inline)) {
+        int tm, tn;
+        i8_tile(p, tile, tm, tn);
+        m0 = tm * T::BM;
+        n0 = tn * T::BN;
+        At = p.A + m0 * p.lda + k0;
+        Bt = p.B + n0 * p.ldb + k0;
+        if constexpr (ANY) {
+            a_low = uint32_t(reinterpret_cast<uintptr_t>(At)) & 3;
+            b_low = uint32_t(reinterpret_cast<uintptr_t>(Bt)) & 3;
+            At -= a_low;
+            Bt -= b_low;
+        }
 #pragma unroll
-    for (int i = 0; i < T::ACH; ++i) {
-        const int r = prow + i * (T::NT / T::CPR);
-        a_off[i] = m0 + r < p.M ? (a_low + uint32_t(r * p.lda) + q * 16) & ~3u : kOob;
-    }
+        for (int i = 0; i < T::ACH; ++i) {
+            const int r = prow + i * (T::NT / T::CPR);
+            a_off[i] = m0 + r < p.M ? (a_low + uint32_t(r * p.lda) + q * 16) & ~3u : kOob;
+        }
 #pragma unroll
-    for (int i = 0; i < T::BCH; ++i) {
-        const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
-        b_off[i] = n0 + r < p.N ? (b_low + uint32_t(r * p.ldb) + q * 16) & ~3u : kOob;
-    }
+        for (int i = 0; i < T::BCH; ++i) {
+            const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
+            b_off[i] = n0 + r < p.N ? (b_low + uint32_t(r * p.ldb) + q * 16) & ~3u : kOob;
+        }
+    };
+    int tile = int(blockIdx.x) - split * tiles;
+    aim(tile);
     i32x16 acc[T::RB][T::CB];
 #pragma unroll
     for (int i = 0; i < T::RB; ++i)
@@ -364,8 +376,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     };
 
     const int8_t *const a_end = p.A + (p.M - 1) * p.lda + p.K, *const b_end = p.B + (p.N - 1) * p.ldb + p.K;
-    auto issue = [&](int panel) __attribute__((always_inline)) {
-        char *st = smem + (panel % T::NSTG) * STAGE;
+    auto issue = [&](int panel, char *st) __attribute__((always_inline)) {
         const int k = panel * T::BK;
         const int8_t *const ak = At + k, *const bk = Bt + k;
         const uint32_t an = ANY ? i8_range(ak, a_end) : kFullRange;
@@ -388,23 +399,27 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     constexpr int LOOK = ANY ? 2 : 1;
     // ahead of the panels, so that the first wait covers them: the epilogue's scales and bias (1024^3
     // 6.2 to 5.7 us against loading them there)
-    char *const scales = smem + T::NSTG * STAGE;
-    for (int i = wave; p.splits == 1 && i < (T::BM + 2 * T::SN) / 64; i += T::NT / 64) {
-        char *to = scales + i * 256;
-        const int at = i * 64;
-        if (at < T::BM) i8_load_floats(p.sa + m0, at, min(p.M - m0, T::BM), lane, to);
-        else if (at < T::BM + T::SN) i8_load_floats(p.sb + n0, at - T::BM, min(p.N - n0, T::BN), lane, to);
-        else if (p.bias) i8_load_floats(p.bias + n0, at - T::BM - T::SN, min(p.N - n0, T::BN), lane, to);
-    }
+    char *scales = smem + T::NSTG * STAGE;
+    auto issue_scales = [&](char *at_lds) __attribute__((always_inline)) {
+        for (int i = wave; p.splits == 1 && i < (T::BM + 2 * T::SN) / 64; i += T::NT / 64) {
+            char *to = at_lds + i * 256;
+            const int at = i * 64;
+            if (at < T::BM) i8_load_floats(p.sa + m0, at, min(p.M - m0, T::BM), lane, to);
+            else if (at < T::BM + T::SN) i8_load_floats(p.sb + n0, at - T::BM, min(p.N - n0, T::BN), lane, to);
+            else if (p.bias) i8_load_floats(p.bias + n0, at - T::BM - T::SN, min(p.N - n0, T::BN), lane, to);
+        }
+    };
+    issue_scales(scales);
 #pragma unroll
-    for (int i = 0; i < T::NSTG; ++i) issue(i);
+    for (int i = 0; i < T::NSTG; ++i) issue(i, smem + i * STAGE);
     wait_vmcnt<(T::NSTG - 1) * LPP>();
     asm volatile("s_barrier" ::: "memory");
     static_for<0, LOOK>([&](auto tc) __attribute__((always_inline)) { read(smem, tc); });
     int stage = 0;
     const int full = ANY ? kn / T::BK : panels;      // panels without a masked step
+    int behind = 0;                                  // panels between a panel read and that of its tile
     auto run = [&](int panel, auto mask) __attribute__((always_inline)) {
-        const char *st = smem + stage * STAGE;
+        char *st = smem + stage * STAGE;
         stage = stage + 1 == T::NSTG ? 0 : stage + 1;
         const char *next = smem + stage * STAGE;
         static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
@@ -417,7 +432,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
             }
             if constexpr (t + LOOK < T::STEPS) read(st, std::integral_constant<int, t + LOOK>{});
             else read(next, std::integral_constant<int, t + LOOK - T::STEPS>{});
-            if constexpr (turn) issue(panel + T::NSTG);
+            if constexpr (turn) issue(panel + T::NSTG - behind, st);
             multiply(tc, mask, kn - panel * T::BK - 16 * (ANY ? t + T::STEPS * fhi : 2 * t + fhi));
             // operand reads behind the first MFMAs, the loads behind the others
             constexpr int ops = (T::RB + T::CB) * (ANY && (t + LOOK) % T::STEPS % (T::STEPS - 1) == 0 ? 2 : 1);
@@ -435,11 +450,46 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
             });
         });
     };
-    for (int panel = 0; panel < full; ++panel) run(panel, std::false_type{});
-    if constexpr (ANY)
-        if (full < panels) run(full, std::true_type{});
-    wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
-    i8_epilogue<T>(p, acc, reinterpret_cast<const float *>(scales), m0, n0, split, wm, wn);
+    if constexpr (!LOOP) {
+        for (int panel = 0; panel < full; ++panel) run(panel, std::false_type{});
+        if constexpr (ANY)
+            if (full < panels) run(full, std::true_type{});
+        wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
+        i8_epilogue<T>(p, acc, reinterpret_cast<const float *>(scales), m0, n0, split, wm, wn);
+    } else {
+        // The last NSTG panels of a tile load the first of the next, so that its stores and the start
+        // of the next run under each other: 8192 x 8192 x 256 to bf16 47 to 39 us, x 2048 131 to 124 (the
+        // grid has fewer workgroups than tiles only where K has NSTG panels). Not waiting for
+        // the stores before the panels behind them gave 1 % at most, and the same for tiles of
+        // which two share a compute unit nothing: they overlap as they are.
+        for (;;) {
+            const int cm0 = m0, cn0 = n0;
+            const float *const ready = reinterpret_cast<const float *>(scales);
+            tile += int(gridDim.x);
+            const bool more = p.splits == 1 && tile < tiles;
+            int panel = 0;
+            for (int part = 0; part < 2; ++part) {
+                const int end = part == 0 ? panels - T::NSTG : panels;
+                for (; panel < end; ++panel) run(panel, std::false_type{});
+                if (part == 0 && more) {
+                    aim(tile);
+                    behind = panels;
+                    scales = smem + T::NSTG * STAGE + (scales == smem + T::NSTG * STAGE ? SCALES : 0);
+                    issue_scales(scales);
+                }
+            }
+            if (!more) wait_vmcnt<0>();
+            i8_epilogue<T>(p, acc, ready, cm0, cn0, split, wm, wn);
+            if (!more) break;
+            behind = 0;
+            // the next switch loads scales where this tile's were: a turn, or this, lies between
+            if (panels == T::NSTG) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+                for (int j = 0; j < T::CB; ++j) acc[i][j] = i32x16(0);
+        }
+    }
 }
 
 // ------------------------------------------------------------------ rows put in place ---
