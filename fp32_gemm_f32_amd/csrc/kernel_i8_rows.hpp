@@ -23,8 +23,8 @@ namespace sgemm {
 //    loaded by words and moved into place (load_words).
 //  * Rows past M and columns past N repeat the last one; their sums are not stored. Chunks
 //    past K are zero (load_tail).
-// Bound by reading B: 1 x 8192 x 8192 takes 14.1 us (4.8 TB/s with the launch) at 1 x 1 blocks and
-// panels of 256; panels of 512 17.1, 2 column blocks 19.3, the tile kernel at 64 x 64 20.7. Rows
+// Bound by reading B: 1 x 8192 x 8192 takes 13.6 us (4.9 TB/s with the launch) at 1 x 1 blocks and
+// panels of 256; before its scales were loaded first 14.1, and beside that panels of 512 17.1, 2 column blocks 19.3, the tile kernel at 64 x 64 20.7. Rows
 // off a word's boundary: 17.9 with 2 column blocks and panels of 128, 18.5 with 1.
 template <int RB_, int CB_, int WAVES_, int U_, bool ALIGNED_> struct I8Rows {
     static constexpr int RB = RB_, CB = CB_, WAVES = WAVES_, U = U_;
