@@ -218,10 +218,17 @@ template <int DT>
 int quantize(int M, int K, const void *X, int64_t ldx, int8_t *Q, int64_t ldq, float *scales,
              void *stream)
 {
-    constexpr int W = 16 / (DT == SGEMM_DTYPE_F32 ? 4 : 2);
+    constexpr int SIZE = DT == SGEMM_DTYPE_F32 ? 4 : 2, W = 16 / SIZE;
+    const auto rows_from = [&](int64_t row) { return static_cast<const char *>(X) + row * ldx * SIZE; };
     const auto run = [&](auto kern, int rows_per_group) {
-        return launch(kern, dim3(unsigned(ceil_div(M, rows_per_group))), dim3(256), stream, M, K, X,
-                      ldx, Q, ldq, scales);
+        const int64_t most = most_groups(256) * rows_per_group;
+        for (int64_t r = 0; r < M; r += most) {
+            const int rows = int(std::min<int64_t>(most, M - r));
+            const int st = launch(kern, dim3(unsigned(ceil_div(rows, rows_per_group))), dim3(256), stream, rows, K,
+                                  rows_from(r), ldx, Q + r * ldq, ldq, scales + r);
+            if (st != SGEMM_OK) return st;
+        }
+        return int(SGEMM_OK);
     };
     const int64_t chunks = ceil_div(K, W);
     if (chunks <= 8) return run(&k_quantize_rows<DT, 1, 8>, 32);
@@ -235,8 +242,13 @@ int quantize(int M, int K, const void *X, int64_t ldx, int8_t *Q, int64_t ldq, f
     if (chunks <= 2048) return run(&k_quantize_rows<DT, 8, 256>, 1);
     if constexpr (DT == SGEMM_DTYPE_F32)
         if (chunks <= 4096 && M >= 512) return run(&k_quantize_rows<DT, 16, 256>, 1);
-    return launch(&k_quantize_long_rows<DT>, dim3(unsigned(M)), dim3(1024), stream, K, X, ldx, Q,
-                  ldq, scales);
+    const int64_t most = most_groups(1024);
+    for (int64_t r = 0; r < M; r += most) {
+        const int st = launch(&k_quantize_long_rows<DT>, dim3(unsigned(std::min<int64_t>(most, M - r))), dim3(1024),
+                              stream, K, rows_from(r), ldx, Q + r * ldq, ldq, scales + r);
+        if (st != SGEMM_OK) return st;
+    }
+    return SGEMM_OK;
 }
 
 }  // namespace

@@ -24,6 +24,10 @@ int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, void *stream, Args... 
     return e == hipSuccess ? SGEMM_OK : SGEMM_ELAUNCH;
 }
 
+// The most workgroups one launch may have: HIP takes fewer than 2^32 work items in a dimension. What
+// needs more goes out in several launches, each over its own rows or columns.
+inline int64_t most_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
+
 // Compute units of the current device, looked up once per device.
 inline int device_cus(int *out)
 {
