@@ -124,13 +124,10 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
         if (workspace_bytes == 0) r = RowSplit{1, V, 0};
         else if (workspace_bytes < need) return SGEMM_EINVAL_ARG;
     }
-    if (int64_t(M) * r.splits > kMaxGroups) return SGEMM_ETOO_LARGE;
     RowArgs p{};
-    p.logits = logits; p.ld = ld; p.tokens = tokens; p.token_bytes = token_bytes;
-    p.logprobs = logprobs; p.entropy = entropy; p.lse = lse;
-    p.top_logprobs = top_logprobs; p.top_tokens = top_tokens;
+    p.ld = ld; p.token_bytes = token_bytes;
     p.parts = static_cast<char *>(workspace); p.part_bytes = r.part_bytes;
-    p.M = M; p.V = V; p.top = top; p.splits = r.splits; p.part_len = r.part_len;
+    p.V = V; p.top = top; p.splits = r.splits; p.part_len = r.part_len;
     const int64_t groups = int64_t(M) * r.splits;
     const bool past_caches = streamed(M, V, dtype);
     RowLaunch pass;
@@ -145,9 +142,22 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
         pass = pass_kernel<SGEMM_DTYPE_F16>(top > 0, groups, r.part_len, cus, past_caches);
         join = join_kernel<SGEMM_DTYPE_F16>(top > 0);
     }
-    st = launch(pass.kernel, dim3(unsigned(groups)), dim3(pass.threads), stream, p);
-    if (st != SGEMM_OK || r.splits == 1) return st;
-    return launch(join, dim3(unsigned(M)), dim3(256), stream, p);
+    // rows that are split are fewer than the compute units: they take one turn
+    const int64_t most = most_groups(pass.threads) / r.splits;
+    for (int64_t row = 0; row < M; row += most) {
+        p.M = int(std::min<int64_t>(most, M - row));
+        p.logits = static_cast<const char *>(logits) + row * ld * size;
+        p.tokens = static_cast<const char *>(tokens) + row * token_bytes;
+        p.logprobs = logprobs + row;
+        p.entropy = entropy ? entropy + row : nullptr;
+        p.lse = lse ? lse + row : nullptr;
+        p.top_logprobs = top_logprobs + row * top;
+        p.top_tokens = top_tokens + row * top;
+        st = launch(pass.kernel, dim3(unsigned(int64_t(p.M) * r.splits)), dim3(pass.threads), stream, p);
+        if (st == SGEMM_OK && r.splits > 1) st = launch(join, dim3(unsigned(p.M)), dim3(256), stream, p);
+        if (st != SGEMM_OK) return st;
+    }
+    return SGEMM_OK;
 }
 
 extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dtype, int64_t ld,

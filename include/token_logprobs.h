@@ -43,8 +43,7 @@ extern "C" {
  * tokens: M indices of token_bytes (4 or 8) each. logprobs, entropy, lse: M floats each;
  * entropy and lse may be NULL. top: 0 to 64 and at most V (else SGEMM_EINVAL_ARG);
  * top_logprobs: M x top floats, top_tokens: M x top int64, packed, not NULL where top > 0.
- * V must be at least 1 where M is (else SGEMM_EINVAL_DIM). At most 2^30 workgroups (rows times
- * the parts of each; any M up to 2^26), else SGEMM_ETOO_LARGE.
+ * V must be at least 1 where M is (else SGEMM_EINVAL_DIM).
  *
  * workspace: few rows are split over workgroups along V and joined by a second kernel.
  * Caller-owned device memory of token_logprobs_workspace_size bytes, 16-byte aligned;

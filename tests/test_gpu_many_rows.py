@@ -41,3 +41,21 @@ def test_quantize(torch):
         assert torch.equal(scales[w], (peak / 127).float())
         inverse = (127 / peak).float()
         assert torch.equal(q[w], (x[w].float() * inverse[:, None]).round().clamp(-127, 127).to(torch.int8))
+
+
+def test_logprobs(torch):
+    M, V, top = ITEMS // 256 + 1029, 5, 2          # a row to a workgroup of 256
+    x = torch.empty(M, V, dtype=torch.float16, device="cuda").normal_()
+    tok = torch.arange(M, dtype=torch.int32, device="cuda") % 7 - 1        # some below 0, some past V
+    print(f"[many rows] logprobs {M}x{V}", flush=True)
+    r = g.token_logprobs(x, tok, top=top)
+    for w in windows(ITEMS // 256, M):
+        one = g.token_logprobs(x[w].contiguous(), tok[w].contiguous(), top=top)
+        for name, a, b in zip(one._fields, r, one):
+            assert torch.equal(a[w].nan_to_num(7.0), b.nan_to_num(7.0)), name
+        want = x[w].double().log_softmax(1)
+        given = (tok[w] >= 0) & (tok[w] < V)
+        at = want[given].gather(1, tok[w][given].long()[:, None])[:, 0]
+        # (logs of sums of five terms: a few steps of FP32)
+        assert (r.logprobs[w][given].double() - at).abs().max() <= 32 * 2.0 ** -24 * 8
+        assert torch.equal(r.logprobs[w].isnan(), tok[w] >= V) and (r.logprobs[w][tok[w] < 0] == 0).all()
