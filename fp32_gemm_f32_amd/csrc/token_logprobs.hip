@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kMaxTop = TOKEN_LOGPROBS_MAX_TOP;
 static_assert(kMaxTop == 64, "a wave's list holds one key per lane");
-constexpr int64_t kMaxGroups = int64_t(1) << 30;
 
 int ceil_div(int64_t a, int64_t b) { return int((a + b - 1) / b); }
 
@@ -187,17 +186,29 @@ extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dty
         if (overlaps(d, r)) return SGEMM_EALIAS;
 
     GradArgs p{};
-    p.logits = logits; p.grad = grad; p.tokens = tokens; p.token_bytes = token_bytes;
-    p.lse = lse; p.entropy = entropy; p.g_logprob = g_logprob; p.g_entropy = g_entropy;
-    p.g_lse = g_lse; p.ld = ld; p.ldg = ldg; p.M = M; p.V = V;
+    p.token_bytes = token_bytes; p.ld = ld; p.ldg = ldg; p.V = V;
     p.part_len = 16384 / size;
     p.parts = ceil_div(V, p.part_len);
-    if (int64_t(M) * p.parts > kMaxGroups) return SGEMM_ETOO_LARGE;
     const bool past_caches = streamed(M, V, dtype);
     auto kern = dtype == SGEMM_DTYPE_F32
                     ? (past_caches ? &k_row_gradient<SGEMM_DTYPE_F32, true> : &k_row_gradient<SGEMM_DTYPE_F32, false>)
                 : dtype == SGEMM_DTYPE_BF16
                     ? (past_caches ? &k_row_gradient<SGEMM_DTYPE_BF16, true> : &k_row_gradient<SGEMM_DTYPE_BF16, false>)
                     : (past_caches ? &k_row_gradient<SGEMM_DTYPE_F16, true> : &k_row_gradient<SGEMM_DTYPE_F16, false>);
-    return launch(kern, dim3(unsigned(M * int64_t(p.parts))), dim3(kGradThreads), stream, p);
+    const int64_t most = most_groups(kGradThreads) / p.parts;      // 31 rows at least: parts < 2^20
+    const auto from = [](const float *v, int64_t row) { return v ? v + row : nullptr; };
+    for (int64_t row = 0; row < M; row += most) {
+        p.M = int(std::min<int64_t>(most, M - row));
+        p.logits = static_cast<const char *>(logits) + row * ld * size;
+        p.grad = static_cast<char *>(grad) + row * ldg * size;
+        p.tokens = static_cast<const char *>(tokens) + row * token_bytes;
+        p.lse = lse + row;
+        p.entropy = from(entropy, row);
+        p.g_logprob = from(g_logprob, row);
+        p.g_entropy = from(g_entropy, row);
+        p.g_lse = from(g_lse, row);
+        const int st = launch(kern, dim3(unsigned(int64_t(p.M) * p.parts)), dim3(kGradThreads), stream, p);
+        if (st != SGEMM_OK) return st;
+    }
+    return SGEMM_OK;
 }

@@ -59,3 +59,25 @@ def test_logprobs(torch):
         # (logs of sums of five terms: a few steps of FP32)
         assert (r.logprobs[w][given].double() - at).abs().max() <= 32 * 2.0 ** -24 * 8
         assert torch.equal(r.logprobs[w].isnan(), tok[w] >= V) and (r.logprobs[w][tok[w] < 0] == 0).all()
+
+
+def test_gradient(torch):
+    M, V = ITEMS // 256 + 1029, 5                  # a row to a workgroup of 256
+    x = torch.empty(M, V, dtype=torch.float16, device="cuda").normal_()
+    out = torch.full((M, V), 99.0, dtype=torch.float16, device="cuda")
+    tok = torch.arange(M, device="cuda") % 6 - 1
+    r = g.token_logprobs(x, tok)
+    k = torch.rand(M, device="cuda")
+    print(f"[many rows] gradient {M}x{V}", flush=True)
+    g.token_logprobs_backward(x, tok, r.lse, r.entropy, k, k, out=out)
+    for w in windows(ITEMS // 256, M):
+        rows = [t[w].contiguous() for t in (x, tok, r.lse, r.entropy, k, k)]
+        assert torch.equal(out[w], g.token_logprobs_backward(*rows))
+        given = (tok[w] >= 0)[:, None]
+        hot = torch.nn.functional.one_hot(tok[w].clamp_min(0), V) * given
+        logp = x[w].double().log_softmax(1)
+        p = logp.exp()
+        h = -(p * logp).sum(1, keepdim=True)
+        want = k[w].double()[:, None] * (hot - p * given - p * (logp + h))
+        # values of up to 3 or so: half a step of FP16, and sums of a few terms in FP32
+        assert (out[w].double() - want).abs().max() <= 4 * 2.0 ** -11
