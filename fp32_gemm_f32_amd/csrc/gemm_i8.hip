@@ -143,6 +143,7 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             const int64_t groups = ceil_div(N, v.bn) * s;
+            if (s > 1 && groups > most_groups(v.threads)) break;     // splits take one launch
             // a panel of every wave takes this long when little else is in flight
             const double turn = any ? double(ceil_div(chunk, 1024)) * 1.4 : double(ceil_div(chunk, 2048)) * 0.8;
             const double step = double(ceil_div(groups, 2 * cus)) * turn;
@@ -312,9 +313,6 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     p.A = A; p.B = B; p.sa = a_scales; p.sb = b_scales; p.bias = bias; p.C = C;
     p.lda = lda; p.ldb = ldb; p.ldc = ldc;
     p.M = M; p.N = N; p.K = K; p.c_dtype = c_dtype;
-    // (2560 x 13056 x 512 to f32, 256 x 256 tiles: rows on lines of 64 bytes 44.5 to 42.0 us, off
-    // them 50.6 to 54.8, as each row of a tile ends in parts of a line)
-    p.stream = reinterpret_cast<uintptr_t>(C) % 64 == 0 && ldc * dtype_bytes(c_dtype) % 64 == 0;
     if (K == 0)
         return launch(&k_gemm_i8_empty, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 
@@ -338,14 +336,41 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
         p.K = int(ld16);
     }
     p.partial = static_cast<int *>(workspace);
-    p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
     p.splits = plan.splits; p.k_chunk = plan.splits > 1 ? plan.k_chunk : p.K;
-    const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(plan.tiles_n));
-    p.group_mul = d.mul; p.group_shift = d.shift;
-    int64_t groups = int64_t(plan.tiles_m) * plan.tiles_n * plan.splits;
-    if (goes_on(*plan.v, groups, plan.splits, ceil_div(K, 128), cus)) groups = cus;
-    st = launch(plan.v->kernel, dim3(unsigned(groups)), dim3(plan.v->threads), stream, p);
-    if (st != SGEMM_OK || plan.splits == 1) return st;
+    const I8Variant &v = *plan.v;
+    const bool loops = goes_on(v, int64_t(plan.tiles_m) * plan.tiles_n, plan.splits, ceil_div(K, 128), cus);
+    // C in parts that one launch each may take, almost always one: no more workgroups than
+    // most_groups, rows and columns that a tile past the last of 2^31 - 1 would carry out of an int
+    // (split products are one part: make_plan gives them few tiles)
+    const int64_t most = loops ? INT64_MAX : most_groups(v.threads), most_rows = int64_t(1) << 30;
+    const int64_t part_m = std::min({int64_t(plan.tiles_m), most, most_rows / v.bm});
+    const int64_t part_n = std::min({int64_t(plan.tiles_n), most / part_m, most_rows / v.bn});
+    const int csize = dtype_bytes(c_dtype);
+    const I8Args whole = p;
+    for (int64_t tm = 0; tm < plan.tiles_m; tm += part_m)
+        for (int64_t tn = 0; tn < plan.tiles_n; tn += part_n) {
+            const int64_t m = tm * v.bm, n = tn * v.bn;
+            p.tiles_m = int(std::min(part_m, plan.tiles_m - tm));
+            p.tiles_n = int(std::min(part_n, plan.tiles_n - tn));
+            p.M = int(std::min<int64_t>(M - m, part_m * v.bm));
+            p.N = int(std::min<int64_t>(N - n, part_n * v.bn));
+            p.A = whole.A + m * p.lda;
+            p.B = whole.B + n * p.ldb;
+            p.sa = a_scales + m;
+            p.sb = b_scales + n;
+            p.bias = bias ? bias + n : nullptr;
+            p.C = static_cast<char *>(C) + (m * ldc + n) * csize;
+            // (2560 x 13056 x 512 to f32, 256 x 256 tiles: rows on lines of 64 bytes 44.5 to 42.0 us, off
+            // them 50.6 to 54.8, as each row of a tile ends in parts of a line)
+            p.stream = reinterpret_cast<uintptr_t>(p.C) % 64 == 0 && ldc * csize % 64 == 0;
+            const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
+            p.group_mul = d.mul; p.group_shift = d.shift;
+            int64_t groups = int64_t(p.tiles_m) * p.tiles_n * plan.splits;
+            if (loops) groups = std::min<int64_t>(groups, cus);
+            st = launch(v.kernel, dim3(unsigned(groups)), dim3(v.threads), stream, p);
+            if (st != SGEMM_OK) return st;
+        }
+    if (plan.splits == 1) return SGEMM_OK;
     return launch(&k_gemm_i8_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 }
 

@@ -81,3 +81,57 @@ def test_gradient(torch):
         want = k[w].double()[:, None] * (hot - p * given - p * (logp + h))
         # values of up to 3 or so: half a step of FP16, and sums of a few terms in FP32
         assert (out[w].double() - want).abs().max() <= 4 * 2.0 ** -11
+
+
+def product_reference(a, sa, b, sb, bias):
+    """The definition for few columns of K: exact sums, and the size its roundings are relative to."""
+    s = (a.double()[:, None, :] * b.double()[None, :, :]).sum(2)
+    scaled = s * sa.double()[:, None] * sb.double()
+    return scaled + bias.double(), scaled.abs() + bias.double().abs()
+
+
+def test_few_rows_by_many_columns(torch):
+    M, K = 2, 16
+    border = ITEMS // 512 * 16                     # 16 columns to a workgroup of 512
+    N = border + 1029
+    a = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda")
+    b = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+    sa, sb, bias = torch.rand(M, device="cuda"), torch.rand(N, device="cuda"), torch.randn(N, device="cuda") * 1e4
+    out = torch.full((M, N), float("nan"), device="cuda")
+    print(f"[many columns] product {M}x{N}x{K}", flush=True)
+    g.matmul_i8(a, sa, b, sb, bias=bias, out=out)
+    for w in windows(border, N):
+        want, size = product_reference(a, sa, b[w], sb[w], bias[w])
+        assert ((out[:, w].double() - want).abs() <= 5 * 2.0 ** -24 * size).all()
+    assert torch.isfinite(out).all()
+
+
+def test_tiles_of_many_columns(torch):
+    M, K = 17, 1
+    border = 1 << 30                               # what one launch takes of them
+    N = border + 1029
+    a = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda")
+    b = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+    sa, sb = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    print(f"[many columns] product {M}x{N}x{K}", flush=True)
+    g.gemm_i8(M, N, K, a.data_ptr(), K, sa.data_ptr(), b.data_ptr(), K, sb.data_ptr(), 0, out.data_ptr(), 1, N,
+              stream=torch.cuda.current_stream().cuda_stream)
+    for w in windows(border, N):
+        s = a.float() * b[w].float().t()
+        assert torch.equal(out[:, w], (s * (sa[:, None] * sb[w])).to(torch.bfloat16))
+
+
+def test_tiles_of_many_rows(torch):
+    """As many rows as an int counts: the last tile reaches past them."""
+    M, N, K = 2 ** 31 - 5, 2, 1
+    a = torch.randint(-128, 128, (M, K), dtype=torch.int8, device="cuda")
+    b = torch.tensor([[3], [-5]], dtype=torch.int8, device="cuda")
+    sa, sb = torch.rand(M, device="cuda"), torch.rand(N, device="cuda")
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    print(f"[many rows] product {M}x{N}x{K}", flush=True)
+    g.gemm_i8(M, N, K, a.data_ptr(), K, sa.data_ptr(), b.data_ptr(), K, sb.data_ptr(), 0, out.data_ptr(), 1, N,
+              stream=torch.cuda.current_stream().cuda_stream)
+    for w in windows(1 << 30, M):
+        s = a[w].float() * b.float().t()
+        assert torch.equal(out[w], (s * (sa[w, None] * sb)).to(torch.bfloat16))
