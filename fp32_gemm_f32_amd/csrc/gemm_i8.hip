@@ -81,6 +81,7 @@ struct I8Plan {
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // What the plan has to know of an operand: rows on word boundaries, K whole chunks.
 struct I8Layout {
@@ -126,6 +127,8 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
     const bool any = !(rows.a && rows.b);
     const double bytes = double(M) * K + double(N) * K;
     const double copied = (rows.a ? 0.0 : double(M) * K) + (rows.b ? 0.0 : double(N) * K);
+    // what a copy takes of the workspace: rows of whole chunks, up to 16 bytes for one of K = 1
+    const double space = (rows.a ? 0.0 : double(M) * round16(K)) + (rows.b ? 0.0 : double(N) * round16(K));
     const auto offer = [&](const I8Plan &p) {
         if (best.v == nullptr || p.cost < best.cost) best = p;
     };
@@ -165,14 +168,12 @@ I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
                    kLaunch + body + join_cost(s) + (copies ? 4.6 + 2.0 * copied / 6.8e6 : 0.0)});
         }
     };
-    if (!any || (workspace && copied <= kMostCopied))
+    if (!any || (workspace && space <= kMostCopied))
         for (const I8Variant &v : kAligned) offer_tile(v, false);
     if (any)
         for (const I8Variant &v : kAny) offer_tile(v, true);
     return best;
 }
-
-int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // Workspace: the splits' sums, then the copies.
 struct I8Space {
