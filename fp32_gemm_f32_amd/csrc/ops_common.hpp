@@ -94,7 +94,14 @@ template <> struct Elem<SGEMM_DTYPE_BF16> {
 template <> struct Elem<SGEMM_DTYPE_F16> {
     typedef _Float16 type;
     __device__ static float widen(_Float16 x) { return static_cast<float>(x); }
-    __device__ static _Float16 narrow(float x) { return static_cast<_Float16>(x); }
+    // x is rounded to FP32 before, and to FP16 here. The empty asm keeps the two apart: the compiler
+    // otherwise makes one v_fma_mixlo_f16 of a multiply-add and this, which rounds once, in some
+    // kernels (and for some elements) and not in others.
+    __device__ static _Float16 narrow(float x)
+    {
+        asm("" : "+v"(x));
+        return static_cast<_Float16>(x);
+    }
 };
 
 // W consecutive elements at an address aligned to one element only: the compiler makes one
