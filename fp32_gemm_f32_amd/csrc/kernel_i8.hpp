@@ -32,11 +32,12 @@ struct I8Args {
     bool stream;           // C's rows start on lines of 64 bytes: store past the caches
 };
 
-// C's value from the exact integer sum: one rounding to FP32, one each for the scales'
-// product, the scaling and the bias.
+// C's value from the exact integer sum: one rounding to FP32, one of the scales' product, and one
+// of both the scaling and the bias, said outright so that every kernel's are the same bits whatever
+// the compiler may contract.
 __device__ inline float i8_value(int sum, float sa, float sb, float bias)
 {
-    return static_cast<float>(sum) * (sa * sb) + bias;
+    return __builtin_fmaf(static_cast<float>(sum), sa * sb, bias);
 }
 
 template <int DT, int W, bool STREAM = false>

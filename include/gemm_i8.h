@@ -60,9 +60,10 @@ int gemm_i8_quantize_rows(int M, int K,
  * C[i*ldc + j] = (sum_{k<K} A[i*lda + k] * B[j*ldb + k]) * (a_scales[i] * b_scales[j]) + bias[j]
  * for 0 <= i < M, 0 <= j < N. A is M x K and B is N x K, both row-major (a row of B is one
  * output channel's weights); any values of int8, -128 too. The sum is exact in 32-bit
- * integers, then rounded once to FP32, scaled (the product of the scales is rounded first)
- * and offset in FP32, and rounded once to C's type c_dtype. bias is NULL or N floats. The
- * result does not depend on the plan: any tiling and split gives the same bits.
+ * integers and rounded once to FP32, the product of the scales is rounded once, and the two
+ * are multiplied and offset with one rounding (a fused multiply-add; zeros without a bias),
+ * then rounded once to C's type c_dtype. bias is NULL or N floats. The result does not depend
+ * on the plan: any tiling and split gives the same bits.
  *
  * Limits: K <= 131071 (so that K * 128 * 128 stays below 2^31), 256 rows of A or B below 2^31
  * bytes (lda, ldb < 8388608), fewer than 2^30 blocks of 16 x 16 in C, else SGEMM_ETOO_LARGE.
