@@ -583,6 +583,9 @@ def _logprobs_forward(logits, tokens, top: int):
         return done
     import torch
 
+    if torch.autograd.forward_ad.unpack_dual(logits).tangent is not None:
+        raise NotImplementedError("token_logprobs has no forward-mode derivative: logits must not "
+                                  "carry a tangent")
     code = _dtype_code(logits.dtype)
     logits = _rows(logits, "logits")
     M, V = logits.shape
@@ -689,7 +692,8 @@ def token_logprobs(logits, tokens, top: int = 0) -> TokenLogprobs:
     more gives NaN. Alternatives of equal logits come by ascending index.
 
     logprobs, entropy and lse carry gradients to logits where it requires them
-    (token_logprobs_backward, in one pass too); the alternatives carry none. In a graph capture
+    (token_logprobs_backward, in one pass too); the alternatives carry none. There is no
+    forward-mode derivative (logits with a tangent are refused). In a graph capture
     call token_logprobs_backward itself rather than .backward(): autograd accumulates into a leaf
     on the stream it first saw it on, which a capture must not wait for."""
     import torch

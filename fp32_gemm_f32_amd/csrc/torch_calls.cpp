@@ -174,7 +174,8 @@ PyObject *token_logprobs_(PyObject *, PyObject *const *args, Py_ssize_t n)
     const int code = dtype_code(x->scalar_type());
     const at::Device device = x->device();
     const long top = PyLong_AsLong(args[2]);
-    if (!m.ok || code < 0 || top < 0 || top > TOKEN_LOGPROBS_MAX_TOP) {
+    // (a forward-mode tangent would be lost: the Python layer refuses it)
+    if (!m.ok || code < 0 || top < 0 || top > TOKEN_LOGPROBS_MAX_TOP || x->_fw_grad(0).defined()) {
         PyErr_Clear();
         return none();
     }
