@@ -27,7 +27,8 @@ Raw layer (same names and arguments as the C ABI; pointers are integers):
     gemm_i8_workspace_size(M, N, K, A=0, lda=K, B=0, ldb=K) -> int
     gemm_i8_plan_describe(M, N, K, lda=K, ldb=K, num_cus=0) -> dict
     token_logprobs_raw(...), token_logprobs_workspace_size(M, V, dtype, top) -> int,
-    token_logprobs_backward_raw(...): token_logprobs.h's arguments in their order
+    token_logprobs_backward_raw(...): token_logprobs.h's arguments in their order, lse_low (of the
+    forms that have it) by name
 Tensor layer (torch tensors on the GPU, launched on torch's current stream):
     matmul(A, B, out=None, kernel="auto", variant=-1) -> C
     quantize_rows(X, out=None, scales=None) -> (Q, scales)
@@ -35,7 +36,7 @@ Tensor layer (torch tensors on the GPU, launched on torch's current stream):
     linear_i8(X, B, b_scales, bias=None, out_dtype=None) -> C
     token_logprobs(logits, tokens, top=0) -> TokenLogprobs (differentiable in logits)
     token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy=None,
-                            grad_lse=None, out=None) -> gradient of the logits
+                            grad_lse=None, out=None, lse_low=None) -> gradient of the logits
 """
 from __future__ import annotations
 
@@ -131,6 +132,10 @@ def _load():
         lib.token_logprobs_workspace_size.restype = z
         lib.token_logprobs_backward.argtypes = [i, i, p, i, l, p, i, p, p, p, p, p, p, l, p]
         lib.token_logprobs_backward.restype = i
+        lib.token_logprobs_low.argtypes = [i, i, p, i, l, p, i, p, p, p, p, i, p, p, p, z, p]
+        lib.token_logprobs_low.restype = i
+        lib.token_logprobs_backward_low.argtypes = [i, i, p, i, l, p, i, p, p, p, p, p, p, p, l, p]
+        lib.token_logprobs_backward_low.restype = i
         lib.sgemm_f32_abi_version.argtypes = []
         lib.sgemm_f32_abi_version.restype = i
         _lib = lib
@@ -301,11 +306,12 @@ def gemm_i8_plan_describe(M, N, K, lda=None, ldb=None, num_cus=0) -> dict:
 
 def token_logprobs_raw(M, V, logits, dtype, ld, tokens, token_bytes, logprobs, entropy, lse, top=0,
                        top_logprobs=0, top_tokens=0, workspace=0, workspace_bytes=0,
-                       stream=0) -> None:
-    _check(_load().token_logprobs(M, V, logits or None, dtype, ld, tokens or None, token_bytes,
-                                  logprobs or None, entropy or None, lse or None, top,
-                                  top_logprobs or None, top_tokens or None, workspace or None,
-                                  workspace_bytes, stream or None), "token_logprobs")
+                       stream=0, lse_low=0) -> None:
+    _check(_load().token_logprobs_low(M, V, logits or None, dtype, ld, tokens or None, token_bytes,
+                                      logprobs or None, entropy or None, lse or None,
+                                      lse_low or None, top, top_logprobs or None,
+                                      top_tokens or None, workspace or None, workspace_bytes,
+                                      stream or None), "token_logprobs")
 
 
 def token_logprobs_workspace_size(M, V, dtype, top) -> int:
@@ -313,11 +319,13 @@ def token_logprobs_workspace_size(M, V, dtype, top) -> int:
 
 
 def token_logprobs_backward_raw(M, V, logits, dtype, ld, tokens, token_bytes, lse, entropy,
-                                g_logprob, g_entropy, g_lse, grad, ldg, stream=0) -> None:
-    _check(_load().token_logprobs_backward(M, V, logits or None, dtype, ld, tokens or None,
-                                           token_bytes, lse or None, entropy or None,
-                                           g_logprob or None, g_entropy or None, g_lse or None,
-                                           grad or None, ldg, stream or None),
+                                g_logprob, g_entropy, g_lse, grad, ldg, stream=0,
+                                lse_low=0) -> None:
+    _check(_load().token_logprobs_backward_low(M, V, logits or None, dtype, ld, tokens or None,
+                                               token_bytes, lse or None, lse_low or None,
+                                               entropy or None, g_logprob or None,
+                                               g_entropy or None, g_lse or None, grad or None,
+                                               ldg, stream or None),
            "token_logprobs_backward")
 
 
@@ -577,8 +585,9 @@ def _tokens(tokens, M: int, device):
     return _vector(tokens, M, tokens.dtype, "tokens"), (8 if tokens.dtype == torch.int64 else 4)
 
 
-def _logprobs_forward(logits, tokens, top: int):
-    done = (_calls or _load_calls()).token_logprobs(logits, tokens, top)
+def _logprobs_forward(logits, tokens, top: int, low: bool = False):
+    """TokenLogprobs' fields and lse_low, which is None unless asked for."""
+    done = (_calls or _load_calls()).token_logprobs(logits, tokens, top, low)
     if done is not None:
         return done
     import torch
@@ -599,6 +608,7 @@ def _logprobs_forward(logits, tokens, top: int):
     if top:
         top_logprobs = torch.empty((M, top), dtype=torch.float32, device=dev)
         top_tokens = torch.empty((M, top), dtype=torch.int64, device=dev)
+    lse_low = torch.empty((M,), dtype=torch.float32, device=dev) if low else None
     with _Device(dev) as stream:
         ws_bytes = token_logprobs_workspace_size(M, V, code, top)
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
@@ -606,21 +616,26 @@ def _logprobs_forward(logits, tokens, top: int):
                            token_bytes, logprobs.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
                            top, top_logprobs.data_ptr() if top else 0,
                            top_tokens.data_ptr() if top else 0,
-                           0 if ws is None else ws.data_ptr(), ws_bytes, stream)
-    return logprobs, entropy, lse, top_logprobs, top_tokens
+                           0 if ws is None else ws.data_ptr(), ws_bytes, stream,
+                           lse_low.data_ptr() if low else 0)
+    return logprobs, entropy, lse, top_logprobs, top_tokens, lse_low
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy=None,
-                            grad_lse=None, out=None):
+                            grad_lse=None, out=None, lse_low=None):
     """The gradient with respect to logits of
     sum(grad_logprobs * logprobs + grad_entropy * entropy + grad_lse * lse), from the lse and
     entropy that token_logprobs returned for these logits; a gradient that is None counts as
     zeros (entropy may be None where grad_entropy is). out may be logits itself: the gradient
-    then takes its place."""
+    then takes its place. No gradient flows through it.
+
+    The probabilities are exp(logits - lse), and off by lse's rounding to FP32: 1e-6 for logits of
+    ordinary size, 0.2 % at 60000, and a row of the type's lowest value loses them altogether.
+    lse_low (M,) float32 is what that rounding left off (token_logprobs.h): autograd keeps and passes it."""
     if out is None:
         done = (_calls or _load_calls()).token_logprobs_backward(logits, tokens, lse, entropy,
                                                                  grad_logprobs, grad_entropy,
-                                                                 grad_lse)
+                                                                 grad_lse, lse_low)
         if done is not None:
             return done
     import torch
@@ -633,11 +648,12 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_en
     tokens, token_bytes = _tokens(tokens, M, dev)
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
-    _on_gpu(dev, lse, entropy, grad_logprobs, grad_entropy, grad_lse)
+    _on_gpu(dev, lse, entropy, grad_logprobs, grad_entropy, grad_lse, lse_low)
     vectors = [None if t is None else _vector(t.detach(), M, torch.float32, name)
                for t, name in ((lse, "lse"), (entropy, "entropy"),
                                (grad_logprobs, "grad_logprobs"),
-                               (grad_entropy, "grad_entropy"), (grad_lse, "grad_lse"))]
+                               (grad_entropy, "grad_entropy"), (grad_lse, "grad_lse"),
+                               (lse_low, "lse_low"))]
     if vectors[0] is None:
         raise ValueError("lse is needed")
     out = (torch.empty((M, V), dtype=logits.dtype, device=dev) if out is None
@@ -645,8 +661,9 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_en
     with _Device(dev) as stream:
         token_logprobs_backward_raw(M, V, logits.data_ptr(), code, _ld_of(logits),
                                     tokens.data_ptr(), token_bytes,
-                                    *(0 if t is None else t.data_ptr() for t in vectors),
-                                    out.data_ptr(), _ld_of(out), stream)
+                                    *(0 if t is None else t.data_ptr() for t in vectors[:5]),
+                                    out.data_ptr(), _ld_of(out), stream,
+                                    0 if lse_low is None else vectors[5].data_ptr())
     return out
 
 
@@ -664,21 +681,21 @@ def _autograd_function():
         class TokenLogprobsFunction(torch.autograd.Function):
             @staticmethod
             def forward(ctx, logits, tokens, top):
-                out = _logprobs_forward(logits, tokens, top)
-                ctx.save_for_backward(logits, tokens, out[2], out[1])
+                *out, lse_low = _logprobs_forward(logits, tokens, top, True)
+                ctx.save_for_backward(logits, tokens, out[2], out[1], lse_low)
                 ctx.set_materialize_grads(False)
                 if top:
                     ctx.mark_non_differentiable(*out[3:])
-                return out
+                return tuple(out)
 
             @staticmethod
             @once_differentiable
             def backward(ctx, g_logprobs, g_entropy, g_lse, *_):
                 if g_logprobs is None and g_entropy is None and g_lse is None:
                     return None, None, None
-                logits, tokens, lse, entropy = ctx.saved_tensors
-                return token_logprobs_backward(logits, tokens, lse, entropy, g_logprobs,
-                                               g_entropy, g_lse), None, None
+                logits, tokens, lse, entropy, lse_low = ctx.saved_tensors
+                return token_logprobs_backward(logits, tokens, lse, entropy, g_logprobs, g_entropy,
+                                               g_lse, lse_low=lse_low), None, None
 
         _autograd = TokenLogprobsFunction
     return _autograd
@@ -700,4 +717,4 @@ def token_logprobs(logits, tokens, top: int = 0) -> TokenLogprobs:
 
     if logits.requires_grad and torch.is_grad_enabled():
         return TokenLogprobs(*_autograd_function().apply(logits, tokens, top))
-    return TokenLogprobs(*_logprobs_forward(logits, tokens, top))
+    return TokenLogprobs(*_logprobs_forward(logits, tokens, top)[:5])

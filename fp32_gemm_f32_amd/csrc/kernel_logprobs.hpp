@@ -29,7 +29,7 @@ struct RowArgs {
     const void *logits;
     int64_t ld;
     const void *tokens;
-    float *logprobs, *entropy, *lse, *top_logprobs;
+    float *logprobs, *entropy, *lse, *lse_low, *top_logprobs;
     int64_t *top_tokens;
     char *parts;          // splits > 1: part s of row i at (i * splits + s) * part_bytes
     int64_t part_bytes;
@@ -346,7 +346,14 @@ __device__ inline void write_row(const RowArgs &p, int64_t row, const RowStats &
     if (token.t >= p.V) lp = __builtin_nanf("");
     p.logprobs[row] = token.t < 0 ? 0.0f : lp;
     if (p.entropy) p.entropy[row] = none ? 0.0f : logs - kLn2 * (st.d / st.s);
-    if (p.lse) p.lse[row] = none ? kNegInf : st.m + logs;
+    const float lse = none ? kNegInf : st.m + logs;
+    if (p.lse) p.lse[row] = lse;
+    if (p.lse_low) {
+        // m + log s - lse without rounding (the terms of a sum's error, for either order of size)
+        const float part = lse - st.m;
+        const float low = (st.m - (lse - part)) + (logs - part);
+        p.lse_low[row] = none || __builtin_fabsf(lse) < 64.0f ? 0.0f : low;
+    }
 }
 __device__ inline void write_top(const RowArgs &p, int64_t row, const RowStats &st, int r,
                                  uint64_t key)
@@ -568,7 +575,7 @@ struct GradArgs {
     const void *logits;
     void *grad;
     const void *tokens;
-    const float *lse, *entropy, *g_logprob, *g_entropy, *g_lse;
+    const float *lse, *lse_low, *entropy, *g_logprob, *g_entropy, *g_lse;
     int64_t ld, ldg;
     int M, V, token_bytes, parts, part_len;
 };
@@ -591,6 +598,7 @@ __global__ __launch_bounds__(kGradThreads) void k_row_gradient(GradArgs p)
 
     const int64_t t = token_of(p.tokens, p.token_bytes, row);
     float lse = p.lse[row];
+    const float low = p.lse_low ? p.lse_low[row] : 0.0f;
     float g = p.g_logprob && t >= 0 ? p.g_logprob[row] : 0.0f;
     float h = p.g_entropy ? p.g_entropy[row] : 0.0f;
     const float entropy = p.g_entropy ? p.entropy[row] : 0.0f;
@@ -599,7 +607,7 @@ __global__ __launch_bounds__(kGradThreads) void k_row_gradient(GradArgs p)
     if (lse == kNegInf) { lse = 0.0f; g = 0.0f; a = 0.0f; h = 0.0f; }   // p = 0 throughout
     const int64_t at = t - first;                         // the token's element of the part
     auto value = [&](float v, bool is_token) __attribute__((always_inline)) {
-        const float logp = v - lse;
+        const float logp = (v - lse) - low;
         const float pr = __builtin_amdgcn_exp2f(logp * kLog2e);
         const float w = __builtin_fmaf(h, __builtin_fmaxf(logp, -1000.0f) + entropy, a);
         const float dx = -pr * w;

@@ -89,6 +89,16 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
                               int64_t *top_tokens, void *workspace, size_t workspace_bytes,
                               void *stream)
 {
+    return token_logprobs_low(M, V, logits, dtype, ld, tokens, token_bytes, logprobs, entropy, lse, nullptr, top,
+                              top_logprobs, top_tokens, workspace, workspace_bytes, stream);
+}
+
+extern "C" int token_logprobs_low(int M, int V, const void *logits, int dtype, int64_t ld,
+                                  const void *tokens, int token_bytes, float *logprobs,
+                                  float *entropy, float *lse, float *lse_low, int top,
+                                  float *top_logprobs, int64_t *top_tokens, void *workspace,
+                                  size_t workspace_bytes, void *stream)
+{
     if (M < 0 || V < 0 || (M > 0 && V == 0)) return SGEMM_EINVAL_DIM;
     if (ld < std::max(V, 1)) return SGEMM_EINVAL_LD;
     if (!known_dtype(dtype) || (token_bytes != 4 && token_bytes != 8) || top < 0 ||
@@ -102,12 +112,13 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
                           region(entropy, 1, entropy ? M : 0, M, 4),
                           region(lse, 1, lse ? M : 0, M, 4),
                           region(top_logprobs, M, top, top, 4),
-                          region(top_tokens, M, top, top, 8)};
+                          region(top_tokens, M, top, top, 8),
+                          region(lse_low, 1, lse_low ? M : 0, M, 4)};
     if (bad_region(x, size) || bad_region(t, token_bytes) || bad_region(out[0], 4) ||
         bad_region(out[1], 4) || bad_region(out[2], 4) || bad_region(out[3], 4) ||
-        bad_region(out[4], 8) || bad_region(w, 16))
+        bad_region(out[4], 8) || bad_region(out[5], 4) || bad_region(w, 16))
         return SGEMM_EINVAL_PTR;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 6; ++i) {
         if (overlaps(out[i], x) || overlaps(out[i], t) || overlaps(out[i], w)) return SGEMM_EALIAS;
         for (int j = 0; j < i; ++j)
             if (overlaps(out[i], out[j])) return SGEMM_EALIAS;
@@ -150,6 +161,7 @@ extern "C" int token_logprobs(int M, int V, const void *logits, int dtype, int64
         p.logprobs = logprobs + row;
         p.entropy = entropy ? entropy + row : nullptr;
         p.lse = lse ? lse + row : nullptr;
+        p.lse_low = lse_low ? lse_low + row : nullptr;
         p.top_logprobs = top_logprobs + row * top;
         p.top_tokens = top_tokens + row * top;
         st = launch(pass.kernel, dim3(unsigned(int64_t(p.M) * r.splits)), dim3(pass.threads), stream, p);
@@ -165,6 +177,17 @@ extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dty
                                        const float *g_entropy, const float *g_lse, void *grad,
                                        int64_t ldg, void *stream)
 {
+    return token_logprobs_backward_low(M, V, logits, dtype, ld, tokens, token_bytes, lse, nullptr, entropy,
+                                       g_logprob, g_entropy, g_lse, grad, ldg, stream);
+}
+
+extern "C" int token_logprobs_backward_low(int M, int V, const void *logits, int dtype, int64_t ld,
+                                           const void *tokens, int token_bytes, const float *lse,
+                                           const float *lse_low, const float *entropy,
+                                           const float *g_logprob, const float *g_entropy,
+                                           const float *g_lse, void *grad, int64_t ldg,
+                                           void *stream)
+{
     if (M < 0 || V < 0 || (M > 0 && V == 0)) return SGEMM_EINVAL_DIM;
     if (ld < std::max(V, 1) || ldg < std::max(V, 1)) return SGEMM_EINVAL_LD;
     if (!known_dtype(dtype) || (token_bytes != 4 && token_bytes != 8)) return SGEMM_EINVAL_ARG;
@@ -176,9 +199,10 @@ extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dty
                          region(entropy, 1, g_entropy ? M : 0, M, 4),
                          region(g_logprob, 1, g_logprob ? M : 0, M, 4),
                          region(g_entropy, 1, g_entropy ? M : 0, M, 4),
-                         region(g_lse, 1, g_lse ? M : 0, M, 4)};
+                         region(g_lse, 1, g_lse ? M : 0, M, 4),
+                         region(lse_low, 1, lse_low ? M : 0, M, 4)};
     if (bad_region(x, size) || bad_region(d, size)) return SGEMM_EINVAL_PTR;
-    for (int i = 0; i < 6; ++i)
+    for (int i = 0; i < 7; ++i)
         if (bad_region(in[i], i == 0 ? token_bytes : 4)) return SGEMM_EINVAL_PTR;
     const bool in_place = grad == logits && ldg == ld;
     if (!in_place && overlaps(d, x)) return SGEMM_EALIAS;
@@ -203,6 +227,7 @@ extern "C" int token_logprobs_backward(int M, int V, const void *logits, int dty
         p.grad = static_cast<char *>(grad) + row * ldg * size;
         p.tokens = static_cast<const char *>(tokens) + row * token_bytes;
         p.lse = lse + row;
+        p.lse_low = from(lse_low, row);
         p.entropy = from(entropy, row);
         p.g_logprob = from(g_logprob, row);
         p.g_entropy = from(g_entropy, row);

@@ -163,12 +163,14 @@ int token_bytes(const at::Tensor &t, int64_t n, const at::Device &device)
     return vector(t, n, at::kLong, device) ? 8 : vector(t, n, at::kInt, device) ? 4 : 0;
 }
 
-// token_logprobs(logits, tokens, top) -> (logprobs, entropy, lse, values, indices) or None
+// token_logprobs(logits, tokens, top, low) -> (logprobs, entropy, lse, values, indices, lse_low) or
+// None; the last three are None where top, and low, are 0
 PyObject *token_logprobs_(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 3 || !PyLong_Check(args[2])) return none();
+    if (n != 4 || !PyLong_Check(args[2])) return none();
     const at::Tensor *x = plain(args[0]), *tokens = plain(args[1]);
+    const bool low = args[3] == Py_True;
     if (!x || !tokens) return none();
     const Matrix m(*x);
     const int code = dtype_code(x->scalar_type());
@@ -181,7 +183,7 @@ PyObject *token_logprobs_(PyObject *, PyObject *const *args, Py_ssize_t n)
     }
     const int bytes_each = token_bytes(*tokens, m.rows, device);
     if (!bytes_each) return none();
-    at::Tensor out[5], space;
+    at::Tensor out[6], space;
     int status;
     {
         pybind11::gil_scoped_release release;
@@ -191,30 +193,31 @@ PyObject *token_logprobs_(PyObject *, PyObject *const *args, Py_ssize_t n)
             out[3] = empty({m.rows, top}, at::kFloat, device);
             out[4] = empty({m.rows, top}, at::kLong, device);
         }
+        if (low) out[5] = empty({m.rows}, at::kFloat, device);
         const size_t bytes = token_logprobs_workspace_size(m.rows, m.cols, code, int(top));
         if (bytes) space = empty({int64_t(bytes)}, at::kByte, device);
         float *f[4] = {};
         for (int i = 0; i < (top ? 4 : 3); ++i) f[i] = static_cast<float *>(out[i].data_ptr());
-        status = token_logprobs(m.rows, m.cols, x->data_ptr(), code, m.ld, tokens->data_ptr(), bytes_each,
-                                f[0], f[1], f[2], int(top), f[3],
-                                top ? static_cast<int64_t *>(out[4].data_ptr()) : nullptr,
-                                bytes ? space.data_ptr() : nullptr, bytes, place.stream);
+        status = token_logprobs_low(m.rows, m.cols, x->data_ptr(), code, m.ld, tokens->data_ptr(), bytes_each,
+                                    f[0], f[1], f[2], low ? static_cast<float *>(out[5].data_ptr()) : nullptr,
+                                    int(top), f[3], top ? static_cast<int64_t *>(out[4].data_ptr()) : nullptr,
+                                    bytes ? space.data_ptr() : nullptr, bytes, place.stream);
     }
     if (status != SGEMM_OK) return none();
-    PyObject *r = PyTuple_New(5);
+    PyObject *r = PyTuple_New(6);
     if (!r) return nullptr;
-    for (int i = 0; i < 5; ++i)
-        PyTuple_SET_ITEM(r, i, i < 3 || top ? THPVariable_Wrap(out[i]) : Py_NewRef(Py_None));
+    for (int i = 0; i < 6; ++i)
+        PyTuple_SET_ITEM(r, i, out[i].defined() ? THPVariable_Wrap(out[i]) : Py_NewRef(Py_None));
     return r;
     END_HANDLE_TH_ERRORS
 }
 
-// token_logprobs_backward(logits, tokens, lse, entropy, g_logprobs, g_entropy, g_lse) -> gradient
-// or None; each of the last four may be None
+// token_logprobs_backward(logits, tokens, lse, entropy, g_logprobs, g_entropy, g_lse, lse_low) ->
+// gradient or None; each of the last five may be None
 PyObject *token_logprobs_backward_(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 7) return none();
+    if (n != 8) return none();
     const at::Tensor *x = plain(args[0]), *tokens = plain(args[1]);
     if (!x || !tokens) return none();
     const Matrix m(*x);
@@ -223,8 +226,9 @@ PyObject *token_logprobs_backward_(PyObject *, PyObject *const *args, Py_ssize_t
     if (!m.ok || code < 0) return none();
     const int bytes_each = token_bytes(*tokens, m.rows, device);
     const MaybeVector lse(args[2], m.rows, device), entropy(args[3], m.rows, device),
-        g0(args[4], m.rows, device), g1(args[5], m.rows, device), g2(args[6], m.rows, device);
-    if (!bytes_each || !lse.ok || !lse.t || !entropy.ok || !g0.ok || !g1.ok || !g2.ok ||
+        g0(args[4], m.rows, device), g1(args[5], m.rows, device), g2(args[6], m.rows, device),
+        low(args[7], m.rows, device);
+    if (!bytes_each || !lse.ok || !lse.t || !entropy.ok || !g0.ok || !g1.ok || !g2.ok || !low.ok ||
         (g1.t && !entropy.t))
         return none();
     at::Tensor grad;
@@ -233,9 +237,10 @@ PyObject *token_logprobs_backward_(PyObject *, PyObject *const *args, Py_ssize_t
         pybind11::gil_scoped_release release;
         const Place place(device);
         grad = empty({m.rows, m.cols}, x->scalar_type(), device);
-        status = token_logprobs_backward(m.rows, m.cols, x->data_ptr(), code, m.ld, tokens->data_ptr(),
-                                         bytes_each, lse.data(), entropy.data(), g0.data(), g1.data(),
-                                         g2.data(), grad.data_ptr(), std::max(m.cols, 1), place.stream);
+        status = token_logprobs_backward_low(m.rows, m.cols, x->data_ptr(), code, m.ld, tokens->data_ptr(),
+                                             bytes_each, lse.data(), low.data(), entropy.data(), g0.data(),
+                                             g1.data(), g2.data(), grad.data_ptr(), std::max(m.cols, 1),
+                                             place.stream);
     }
     return status == SGEMM_OK ? THPVariable_Wrap(grad) : none();
     END_HANDLE_TH_ERRORS

@@ -59,6 +59,19 @@ int token_logprobs(int M, int V,
                    void *workspace, size_t workspace_bytes,
                    void *stream);
 
+/*
+ * token_logprobs, and what rounding lse to FP32 leaves off it: lse + lse_low is m + log s with the
+ * error of log s alone, however large m is. lse_low holds M floats, or is NULL; 0 where |lse| < 64,
+ * whose rounding, 2^-19 at most, is within the exponential's own error.
+ */
+int token_logprobs_low(int M, int V,
+                       const void *logits, int dtype, int64_t ld,
+                       const void *tokens, int token_bytes,
+                       float *logprobs, float *entropy, float *lse, float *lse_low,
+                       int top, float *top_logprobs, int64_t *top_tokens,
+                       void *workspace, size_t workspace_bytes,
+                       void *stream);
+
 /* Bytes of workspace token_logprobs uses for this shape on the current device (0: none,
  * also for arguments it would refuse and where no device answers). */
 size_t token_logprobs_workspace_size(int M, int V, int dtype, int top);
@@ -81,6 +94,22 @@ int token_logprobs_backward(int M, int V,
                             const float *g_lse,
                             void *grad, int64_t ldg,
                             void *stream);
+
+/*
+ * The same with lse_low (M floats as token_logprobs_low wrote them, or NULL for zeros) taken off too:
+ *     p_j  = exp(x_j - lse - lse_low)
+ * For logits far from 0 an FP32 lse alone is too coarse: at 60000 its rounding moves every p_j by 0.2 %,
+ * and a row of nothing but the type's lowest value (a mask that leaves nothing) would get p_j = 1
+ * where 1 / V is meant.
+ */
+int token_logprobs_backward_low(int M, int V,
+                                const void *logits, int dtype, int64_t ld,
+                                const void *tokens, int token_bytes,
+                                const float *lse, const float *lse_low, const float *entropy,
+                                const float *g_logprob, const float *g_entropy,
+                                const float *g_lse,
+                                void *grad, int64_t ldg,
+                                void *stream);
 
 #ifdef __cplusplus
 }
