@@ -1,5 +1,6 @@
-"""Build the HIP library libsgemm_f32.so in-tree for gfx950 with hipcc, and the host extension
-_torch_calls.so that the tensor layer calls it through.
+"""Build the HIP library libsgemm_f32.so in-tree for gfx950 with hipcc, and, where torch is
+installed, the host extension _torch_calls.so that the tensor layer calls it through. The C ABI needs
+the library alone.
 
     python -m fp32_gemm_f32_amd.build           # build
     python -m fp32_gemm_f32_amd.build --asm     # also write the gfx950 assembly
@@ -91,11 +92,17 @@ def build(asm: bool = False, verbose: bool = False) -> str:
     return OUT
 
 
-def build_calls(verbose: bool = False) -> str:
-    """Build the extension module _torch_calls (host code) against the library and torch."""
+def build_calls(verbose: bool = False) -> str | None:
+    """Build the extension module _torch_calls (host code) against the library and torch; None where
+    there is no torch, and so no tensor layer to serve."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: built without _torch_calls, which the tensor layer needs",
+              file=sys.stderr)
+        return None
     from torch.utils.cpp_extension import include_paths, library_paths
 
     out = os.path.join(PKG, "_torch_calls.so")
