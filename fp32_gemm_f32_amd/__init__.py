@@ -42,6 +42,7 @@ from __future__ import annotations
 
 import ctypes
 import json
+import math
 import os
 from typing import NamedTuple
 
@@ -570,8 +571,9 @@ def matmul_i8(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
 def linear_i8(X, B, b_scales, bias=None, out_dtype=None):
     """quantize_rows(X), then its product with the 8-bit weights B (N, K) of scales b_scales:
     a projection of activations X (..., K) in 8 bits. The result has X's type unless
-    out_dtype says otherwise."""
-    q, scales = quantize_rows(X if X.dim() == 2 else X.reshape(-1, X.shape[-1]))
+    out_dtype says otherwise. No gradient flows through it."""
+    # (the number of rows is given, not left to reshape: with K = 0 it cannot tell)
+    q, scales = quantize_rows(X if X.dim() == 2 else X.reshape(math.prod(X.shape[:-1]), X.shape[-1]))
     C = matmul_i8(q, scales, B, b_scales, bias=bias, out_dtype=out_dtype or X.dtype)
     return C if X.dim() == 2 else C.view(*X.shape[:-1], B.shape[0])
 
