@@ -633,7 +633,8 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_en
 
     The probabilities are exp(logits - lse), and off by lse's rounding to FP32: 1e-6 for logits of
     ordinary size, 0.2 % at 60000, and a row of the type's lowest value loses them altogether.
-    lse_low (M,) float32 is what that rounding left off (token_logprobs.h): autograd keeps and passes it."""
+    lse_low (M,) float32 is what that rounding left off: token_logprobs_raw writes it where asked,
+    and autograd keeps and passes it."""
     if out is None:
         done = (_calls or _load_calls()).token_logprobs_backward(logits, tokens, lse, entropy,
                                                                  grad_logprobs, grad_entropy,

@@ -118,8 +118,10 @@ double tile_cost(const I8Variant &v, int64_t groups, int splits, int64_t panels,
 
 // The cheapest of: every tile, K whole or split; rows as they are, in the slower form for any
 // alignment, or copied into place first. That form costs a quarter to a half more (measured at
-// 8192 x 8192 x 8193 585 against 466 us for 8192^3, 4096 x 4096 x 4097 80 against 63 for 4096^3, 1023 x
-// 1025 x 1027 9.4 against 5.5 for 1024^3); the copy costs a launch and its traffic, and the workspace.
+// 8192 x 8192 x 8193 563 against 442 us for 8192^3, 4096 x 4096 x 4097 76 against 61 for 4096^3, 1023 x
+// 1025 x 1027 9.4 against 5.3 for 1024^3); the copy costs a launch and its traffic, and the workspace
+// (526 and 81 us for the first two with it: the plan takes it for both, for the second wrongly by 6 %).
+// The cost orders choices and is no time: it knows no clock under load (368 for 8192 x 8192 x 8193).
 I8Plan make_plan(int M, int N, int K, I8Layout rows, int cus, bool workspace)
 {
     I8Plan best{};

@@ -88,8 +88,8 @@ __device__ inline void i8_store_as(int dtype, void *C, int64_t at, const float (
 //    place (join_words) before it is multiplied. In the panel that holds K's end A's
 //    values past it are zeroed there, so B's do not count. Words are loaded only where one
 //    of their bytes may be the matrix's (the resource ends with its last row).
-// Large products are bound by power: 8192^3 to bf16 takes 445 to 470 us from card to card (2340 to
-// 2470 TOP/s) with the matrix pipes busy 73 % of the cycles at 1.57 GHz. Small ones by the latency of
+// Large products are bound by power: 8192^3 to bf16 takes 442 us once the clock has settled (2490
+// TOP/s; 497 over a process's first launches) with the matrix pipes busy 75 % of the cycles at 1.59 GHz. Small ones by the latency of
 // a start, the first panels and the stores (1024^3 5.5 us), few rows by reading B (48 x 16384 x
 // 4096 13.0 us, 5.1 TB/s).
 template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Tile {

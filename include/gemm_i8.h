@@ -97,7 +97,8 @@ size_t gemm_i8_workspace_size(int M, int N, int K, const int8_t *A, int64_t lda,
 /*
  * Writes a one-line JSON description of the plan gemm_i8 runs, given its workspace, for
  * operands of this shape at 4-byte aligned addresses into buf: tile, form, copies, splits,
- * workspace bytes, the cost the choice was made by. num_cus > 0 plans for that many compute
+ * workspace bytes, the cost the choice was made by (in microseconds of a card at full clock,
+ * which large products do not hold: an order, not a time). num_cus > 0 plans for that many compute
  * units (no GPU needed), otherwise the current device's. Returns SGEMM_OK or a negative
  * status (SGEMM_EINVAL_ARG: the buffer is too small).
  */
