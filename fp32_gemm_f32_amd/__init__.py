@@ -29,6 +29,15 @@ Raw layer (same names and arguments as the C ABI; pointers are integers):
     token_logprobs_raw(...), token_logprobs_workspace_size(M, V, dtype, top) -> int,
     token_logprobs_backward_raw(...): token_logprobs.h's arguments in their order, lse_low (of the
     forms that have it) by name
+    gemm_mx4_quantize(M, K, X, x_dtype, ldx, Q, ldq, scales, lds, stream=0)
+    gemm_mx4_dequantize(M, K, Q, ldq, scales, lds, Y, y_dtype, ldy, stream=0)
+    gemm_mx4(M, N, K, A, lda, a_scales, lda_scales, B, ldb, b_scales, ldb_scales, bias, C, c_dtype,
+             ldc, workspace=0, workspace_bytes=0, stream=0)
+    gemm_mx4_workspace_size(M, N, K, A=0, lda=.., a_scales=0, .., B=0, .., b_scales=0, ..) -> int
+    gemm_mx4_plan_describe(M, N, K, num_cus=0) -> dict
+    beam_step_raw(...), beam_step_workspace_size(B, W, V, dtype, top) -> int,
+    reorder_beams_raw(B, W, beams, beam_bytes, states, stream=0): beam_search.h's arguments in their
+    order, a state a tuple of beam_state's fields
 Tensor layer (torch tensors on the GPU, launched on torch's current stream):
     matmul(A, B, out=None, kernel="auto", variant=-1) -> C
     quantize_rows(X, out=None, scales=None) -> (Q, scales)
@@ -37,6 +46,12 @@ Tensor layer (torch tensors on the GPU, launched on torch's current stream):
     token_logprobs(logits, tokens, top=0) -> TokenLogprobs (differentiable in logits)
     token_logprobs_backward(logits, tokens, lse, entropy, grad_logprobs, grad_entropy=None,
                             grad_lse=None, out=None, lse_low=None) -> gradient of the logits
+    quantize_mx4(X, out=None, scales=None) -> (Q, scales)
+    dequantize_mx4(Q, scales, dtype=None, columns=None, out=None) -> values
+    matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None) -> C
+    linear_mx4(X, B, b_scales, bias=None, out_dtype=None) -> C
+    beam_step(logits, scores, top=None, finished=None, pad_token=0) -> BeamStep
+    reorder_beams(states, beams, out=None) -> states of the chosen beams
 """
 from __future__ import annotations
 
@@ -137,6 +152,22 @@ def _load():
         lib.token_logprobs_low.restype = i
         lib.token_logprobs_backward_low.argtypes = [i, i, p, i, l, p, i, p, p, p, p, p, p, p, l, p]
         lib.token_logprobs_backward_low.restype = i
+        lib.gemm_mx4_quantize.argtypes = [i, i, p, i, l, p, l, p, l, p]
+        lib.gemm_mx4_quantize.restype = i
+        lib.gemm_mx4_dequantize.argtypes = [i, i, p, l, p, l, p, i, l, p]
+        lib.gemm_mx4_dequantize.restype = i
+        lib.gemm_mx4.argtypes = [i, i, i, p, l, p, l, p, l, p, l, p, p, i, l, p, z, p]
+        lib.gemm_mx4.restype = i
+        lib.gemm_mx4_workspace_size.argtypes = [i, i, i, p, l, p, l, p, l, p, l]
+        lib.gemm_mx4_workspace_size.restype = z
+        lib.gemm_mx4_plan_describe.argtypes = [i, i, i, i, ctypes.c_char_p, i]
+        lib.gemm_mx4_plan_describe.restype = i
+        lib.beam_step.argtypes = [i, i, i, p, i, l, p, p, l, i, p, p, p, p, z, p]
+        lib.beam_step.restype = i
+        lib.beam_step_workspace_size.argtypes = [i, i, i, i, i]
+        lib.beam_step_workspace_size.restype = z
+        lib.reorder_beams.argtypes = [i, i, p, i, p, i, p]
+        lib.reorder_beams.restype = i
         lib.sgemm_f32_abi_version.argtypes = []
         lib.sgemm_f32_abi_version.restype = i
         _lib = lib
@@ -328,6 +359,63 @@ def token_logprobs_backward_raw(M, V, logits, dtype, ld, tokens, token_bytes, ls
                                                g_entropy or None, g_lse or None, grad or None,
                                                ldg, stream or None),
            "token_logprobs_backward")
+
+
+def gemm_mx4_quantize(M, K, X, x_dtype, ldx, Q, ldq, scales, lds, stream=0) -> None:
+    _check(_load().gemm_mx4_quantize(M, K, X or None, x_dtype, ldx, Q or None, ldq, scales or None, lds,
+                                     stream or None), "gemm_mx4_quantize")
+
+
+def gemm_mx4_dequantize(M, K, Q, ldq, scales, lds, Y, y_dtype, ldy, stream=0) -> None:
+    _check(_load().gemm_mx4_dequantize(M, K, Q or None, ldq, scales or None, lds, Y or None, y_dtype, ldy,
+                                       stream or None), "gemm_mx4_dequantize")
+
+
+def gemm_mx4(M, N, K, A, lda, a_scales, lda_scales, B, ldb, b_scales, ldb_scales, bias, C, c_dtype, ldc,
+             workspace=0, workspace_bytes=0, stream=0) -> None:
+    _check(_load().gemm_mx4(M, N, K, A or None, lda, a_scales or None, lda_scales, B or None, ldb,
+                            b_scales or None, ldb_scales, bias or None, C or None, c_dtype, ldc,
+                            workspace or None, workspace_bytes, stream or None), "gemm_mx4")
+
+
+def gemm_mx4_workspace_size(M, N, K, A=0, lda=None, a_scales=0, lda_scales=None, B=0, ldb=None, b_scales=0,
+                            ldb_scales=None) -> int:
+    """For packed operands at aligned addresses unless told otherwise."""
+    row, blocks = K // 2, (K + 31) // 32
+    return _load().gemm_mx4_workspace_size(
+        M, N, K, A or None, row if lda is None else lda, a_scales or None,
+        blocks if lda_scales is None else lda_scales, B or None, row if ldb is None else ldb,
+        b_scales or None, blocks if ldb_scales is None else ldb_scales)
+
+
+def gemm_mx4_plan_describe(M, N, K, num_cus=0) -> dict:
+    buf = ctypes.create_string_buffer(512)
+    _check(_load().gemm_mx4_plan_describe(M, N, K, num_cus, buf, len(buf)), "gemm_mx4_plan_describe")
+    return json.loads(buf.value.decode())
+
+
+def beam_step_raw(B, W, V, logits, dtype, ld, scores, finished, pad_token, top, out_scores, out_beams,
+                  out_tokens, workspace=0, workspace_bytes=0, stream=0) -> None:
+    _check(_load().beam_step(B, W, V, logits or None, dtype, ld, scores or None, finished or None, pad_token,
+                             top, out_scores or None, out_beams or None, out_tokens or None,
+                             workspace or None, workspace_bytes, stream or None), "beam_step")
+
+
+def beam_step_workspace_size(B, W, V, dtype, top) -> int:
+    return _load().beam_step_workspace_size(B, W, V, dtype, top)
+
+
+class _BeamState(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p)] + [
+        (name, ctypes.c_int64) for name in ("src_row", "dst_row", "count1", "src_step1", "dst_step1", "count2",
+                                            "src_step2", "dst_step2", "run")]
+
+
+def reorder_beams_raw(B, W, beams, beam_bytes, states, stream=0) -> None:
+    """states: tuples of beam_state's fields."""
+    table = (_BeamState * max(len(states), 1))(*(_BeamState(*s) for s in states))
+    _check(_load().reorder_beams(B, W, beams or None, beam_bytes, table, len(states), stream or None),
+           "reorder_beams")
 
 
 # ------------------------------------------------------------------ tensor layer ----------
@@ -721,3 +809,274 @@ def token_logprobs(logits, tokens, top: int = 0) -> TokenLogprobs:
     if logits.requires_grad and torch.is_grad_enabled():
         return TokenLogprobs(*_autograd_function().apply(logits, tokens, top))
     return TokenLogprobs(*_logprobs_forward(logits, tokens, top)[:5])
+
+
+# ------------------------------------------------------- 4-bit product, beam search
+
+def _padded(rows: int, cols: int, device):
+    """Rows of bytes whose starts the product's kernels load without a copy: (rows, cols), packed where
+    4 divides cols, else 16-byte aligned rows."""
+    import torch
+
+    if cols % 4 == 0 or rows < 2:
+        return torch.empty((rows, cols), dtype=torch.uint8, device=device)
+    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
+
+
+def quantize_mx4(X, out=None, scales=None):
+    """(Q, scales): X (M, K) in microscaled 4-bit floating point (E2M1 elements, a power of two for each
+    32 of a row). Q is (M, ceil(K / 2)) uint8, element 2 i of a row in the low half of byte i; scales
+    (M, ceil(K / 32)) uint8, s for 2^(s - 127). X is float32, bfloat16 or float16; a row is a token of
+    activations or an output channel of weights. The codes are defined to the bit (gemm_mx4.h).
+    Where 4 does not divide a row's bytes the result is a view of padded rows, which the product reads
+    in place. No gradient flows through it."""
+    if out is None and scales is None:
+        done = (_calls or _load_calls()).quantize_mx4(X)
+        if done is not None:
+            return done
+    import torch
+
+    code = _dtype_code(X.dtype)
+    X = _rows(X.detach(), "X")
+    M, K = X.shape
+    row, blocks = (K + 1) // 2, (K + 31) // 32
+    out = _padded(M, row, X.device) if out is None else _out(out, (M, row), torch.uint8, X.device, "out")
+    scales = (_padded(M, blocks, X.device) if scales is None
+              else _out(scales, (M, blocks), torch.uint8, X.device, "scales"))
+    with _Device(X.device) as stream:
+        gemm_mx4_quantize(M, K, X.data_ptr(), code, _ld_of(X), out.data_ptr(), _ld_of(out),
+                          scales.data_ptr(), _ld_of(scales), stream)
+    return out, scales
+
+
+def _packed_rows(q, scales, name: str):
+    """A packed matrix and its scales, as the kernels read them."""
+    import torch
+
+    if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{name} and its scales must be uint8, got {q.dtype} and {scales.dtype}")
+    q, scales = _rows(q, name), _rows(scales, f"{name}'s scales")
+    _on_gpu(q.device, scales)
+    if scales.shape[0] != q.shape[0] or scales.shape[1] != (q.shape[1] + 15) // 16:
+        raise ValueError(f"{name}'s scales must have shape ({q.shape[0]}, {(q.shape[1] + 15) // 16}), "
+                         f"got {tuple(scales.shape)}")
+    return q, scales
+
+
+def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
+    """The values that Q (M, R) uint8 with its scales stands for: (M, columns) of dtype (float32 by
+    default, bfloat16 or float16), columns 2 R unless it is given as 2 R - 1. No gradient flows through
+    it."""
+    import torch
+
+    if out is None:
+        done = (_calls or _load_calls()).dequantize_mx4(Q, scales, 0 if dtype is None else _dtype_code(dtype),
+                                                        -1 if columns is None else columns)
+        if done is not None:
+            return done
+    Q, scales = _packed_rows(Q, scales, "Q")
+    M, R = Q.shape
+    if columns is None:
+        columns = 2 * R
+    if (columns + 1) // 2 != R or columns < 0:
+        raise ValueError(f"rows of {R} bytes hold {2 * R} or {2 * R - 1} columns, not {columns}")
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    code = _dtype_code(dtype)
+    out = (torch.empty((M, columns), dtype=dtype, device=Q.device) if out is None
+           else _out(out, (M, columns), dtype, Q.device, "out"))
+    with _Device(Q.device) as stream:
+        gemm_mx4_dequantize(M, columns, Q.data_ptr(), _ld_of(Q), scales.data_ptr(), _ld_of(scales),
+                            out.data_ptr(), code, _ld_of(out), stream)
+    return out
+
+
+def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
+    """C[i, j] = sum_k A[i, k] B[j, k] + bias[j] of the values that quantize_mx4's operands stand for, on
+    the matrix cores in 4 bits, summed in FP32. A is (M, R) and B (N, R) uint8 of 2 R elements a row (a
+    row of B is an output channel), their scales (M or N, ceil(R / 16)) uint8, bias (N,) float32. C is
+    out_dtype (float32 by default, bfloat16 or float16). The workspace (for a split K, or for
+    operands off a word's boundary) is a torch allocation made here. No gradient flows through
+    it."""
+    import torch
+
+    if out is None:
+        done = (_calls or _load_calls()).matmul_mx4(A, a_scales, B, b_scales, bias,
+                                                    0 if out_dtype is None else _dtype_code(out_dtype))
+        if done is not None:
+            return done
+    A, a_scales = _packed_rows(A, a_scales, "A")
+    B, b_scales = _packed_rows(B, b_scales, "B")
+    M, R = A.shape
+    N, R2 = B.shape
+    if R != R2:
+        raise ValueError(f"rows of A and B differ in length: {R} vs {R2} bytes")
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    code = _dtype_code(out_dtype)
+    dev = A.device
+    _on_gpu(dev, B, bias)
+    bias = None if bias is None else _vector(bias.detach(), N, torch.float32, "bias")
+    out = (torch.empty((M, N), dtype=out_dtype, device=dev) if out is None
+           else _out(out, (M, N), out_dtype, dev, "out"))
+    operands = (A.data_ptr(), _ld_of(A), a_scales.data_ptr(), _ld_of(a_scales),
+                B.data_ptr(), _ld_of(B), b_scales.data_ptr(), _ld_of(b_scales))
+    with _Device(dev) as stream:
+        ws_bytes = gemm_mx4_workspace_size(M, N, 2 * R, *operands)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        gemm_mx4(M, N, 2 * R, *operands, 0 if bias is None else bias.data_ptr(), out.data_ptr(), code,
+                 _ld_of(out), 0 if ws is None else ws.data_ptr(), ws_bytes, stream)
+    return out
+
+
+def linear_mx4(X, B, b_scales, bias=None, out_dtype=None):
+    """quantize_mx4(X), then its product with the 4-bit weights B (N, ceil(K / 2)) of scales b_scales: a
+    projection of activations X (..., K). The result has X's type unless out_dtype says otherwise. No
+    gradient flows through it."""
+    if X.dim() == 2:
+        done = (_calls or _load_calls()).linear_mx4(X, B, b_scales, bias,
+                                                    -1 if out_dtype is None else _dtype_code(out_dtype))
+        if done is not None:
+            return done
+    # (the number of rows is given, not left to reshape: with K = 0 it cannot tell)
+    q, scales = quantize_mx4(X if X.dim() == 2 else X.reshape(math.prod(X.shape[:-1]), X.shape[-1]))
+    C = matmul_mx4(q, scales, B, b_scales, bias=bias, out_dtype=out_dtype or X.dtype)
+    return C if X.dim() == 2 else C.view(*X.shape[:-1], B.shape[0])
+
+
+class BeamStep(NamedTuple):
+    """What beam_step returns for B requests: scores (B, top) float32, beams and tokens (B, top) int64,
+    in descending order of the scores; score -infinity, beam -1 and token -1 where there is none."""
+    scores: object
+    beams: object
+    tokens: object
+
+
+def beam_step(logits, scores, top=None, finished=None, pad_token: int = 0) -> BeamStep:
+    """One step of a beam search: the `top` best continuations (beam, token) of each request by
+    scores[b, w] + log softmax(logits[b W + w])[token], in one pass over the logits. logits is (B W, V)
+    float32, bfloat16 or float16, a row for each beam; scores (B, W) float32, the logarithms of the
+    beams' probabilities so far. top is W unless given; W and top are at most 64.
+
+    finished (B, W) bool marks beams that have ended: such a beam offers itself alone, with its score
+    and pad_token. Continuations of probability 0 (logits or scores of -infinity) and of rows that
+    hold a NaN or +infinity do not count. Of equal totals the lower beam comes first, of a beam's equal
+    logits the lower token. No gradient flows through it."""
+    done = (_calls or _load_calls()).beam_step(logits, scores, -1 if top is None else top, finished, pad_token)
+    if done is not None:
+        return BeamStep(*done)
+    import torch
+
+    code = _dtype_code(logits.dtype)
+    if scores.dim() != 2:
+        raise ValueError(f"scores must be 2-D, got {scores.dim()}-D")
+    B, W = scores.shape
+    logits = _rows(logits.detach(), "logits")
+    dev = logits.device
+    if logits.shape[0] != B * W:
+        raise ValueError(f"logits must have {B * W} rows, one for each beam, got {logits.shape[0]}")
+    V = logits.shape[1]
+    top = W if top is None else top
+    if scores.dtype != torch.float32:
+        raise TypeError(f"scores must be float32, got {scores.dtype}")
+    if finished is not None and finished.dtype != torch.bool:
+        raise TypeError(f"finished must be bool, got {finished.dtype}")
+    if finished is not None and tuple(finished.shape) != (B, W):
+        raise ValueError(f"finished must have shape ({B}, {W}), got {tuple(finished.shape)}")
+    if not 1 <= W <= 64 or not 1 <= top <= 64:
+        raise ValueError(f"a request has 1 to 64 beams and as many continuations, got {W} and {top}")
+    _on_gpu(dev, scores, finished)
+    scores = scores.detach().resolve_neg().contiguous()
+    finished = None if finished is None else finished.contiguous()
+    out = BeamStep(torch.empty((B, top), dtype=torch.float32, device=dev),
+                   torch.empty((B, top), dtype=torch.int64, device=dev),
+                   torch.empty((B, top), dtype=torch.int64, device=dev))
+    with _Device(dev) as stream:
+        ws_bytes = beam_step_workspace_size(B, W, V, code, top)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
+        beam_step_raw(B, W, V, logits.data_ptr(), code, _ld_of(logits), scores.data_ptr(),
+                      0 if finished is None else finished.data_ptr(), pad_token, top,
+                      *(t.data_ptr() for t in out), 0 if ws is None else ws.data_ptr(), ws_bytes, stream)
+    return out
+
+
+def _beam_state(src, dst):
+    """beam_state's fields for two tensors of one shape, None where they have more than two dimensions
+    of pieces."""
+    size = src.element_size()
+    dims = []                                        # [count, src step, dst step], outermost first
+    for n, a, b in zip(src.shape[1:], src.stride()[1:], dst.stride()[1:]):
+        if n == 1:
+            continue
+        if dims and dims[-1][1] == n * a * size and dims[-1][2] == n * b * size:
+            dims[-1] = [dims[-1][0] * n, a * size, b * size]
+        else:
+            dims.append([n, a * size, b * size])
+    run = size
+    if dims and dims[-1][1:] == [size, size]:
+        run *= dims.pop()[0]
+    if len(dims) > 2:
+        return None
+    dims = [[1, 0, 0]] * (2 - len(dims)) + dims
+    return (src.data_ptr(), dst.data_ptr(), src.stride(0) * size if src.shape[0] > 1 else 0,
+            dst.stride(0) * size if src.shape[0] > 1 else 0, *dims[0], *dims[1], run)
+
+
+def reorder_beams(states, beams, out=None):
+    """The states of the beams that a step chose: row b W + w of each result is row b W + beams[b, w] of
+    its state. states is a tensor or a sequence of tensors of any type whose first dimension is B W (key
+    and value caches, also views of their first positions; tokens so far), beams (B, W) int64 or
+    int32; an index outside 0 to W - 1 stands for w itself. All are moved in one launch.
+
+    Results are new tensors, or written to out: tensors of the same shapes and types, for which
+    out=states reorders in place and leaves rows that stay alone. An out must not overlap itself or
+    another state. No gradient flows through it."""
+    done = (_calls or _load_calls()).reorder_beams(states, beams, out)
+    if done is not None:
+        return done
+    import torch
+
+    single = isinstance(states, torch.Tensor)
+    sources = [states] if single else list(states)
+    targets = None if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
+    if beams.dtype not in (torch.int64, torch.int32):
+        raise TypeError(f"beams must be int64 or int32, got {beams.dtype}")
+    if beams.dim() != 2:
+        raise ValueError(f"beams must be 2-D, got {beams.dim()}-D")
+    if not beams.is_cuda:
+        raise ValueError("beams must be on a GPU")
+    B, W = beams.shape
+    if W > 64:
+        raise ValueError(f"a request has at most 64 beams, got {W}")
+    dev = beams.device
+    _on_gpu(dev, *sources)
+    beams = beams.resolve_neg().contiguous()
+    for t in sources:
+        if t.dim() < 1 or t.shape[0] != B * W:
+            raise ValueError(f"a state's first dimension must be {B * W}, got shape {tuple(t.shape)}")
+    if targets is None:
+        sources = [t.detach().resolve_conj().resolve_neg() for t in sources]
+        targets = [torch.empty(t.shape, dtype=t.dtype, device=dev) for t in sources]
+        whole = [_beam_state(s, t) for s, t in zip(sources, targets)]
+        sources = [s if w is not None else s.contiguous() for s, w in zip(sources, whole)]
+    else:
+        if len(targets) != len(sources):
+            raise ValueError(f"{len(sources)} states, but {len(targets)} in out")
+        _on_gpu(dev, *targets)
+        for s, t in zip(sources, targets):
+            if s.shape != t.shape or s.dtype != t.dtype:
+                raise ValueError(f"out must match its state: {tuple(s.shape)} {s.dtype}, got "
+                                 f"{tuple(t.shape)} {t.dtype}")
+            if s.is_neg() != t.is_neg() or s.is_conj() != t.is_conj():
+                raise ValueError("out must match its state: one is a negated or conjugated view")
+    table = []
+    for s, t in zip(sources, targets):
+        if s.numel():
+            fields = _beam_state(s, t)
+            if fields is None:
+                raise ValueError(f"a state of strides {s.stride()} has more than two dimensions of pieces: make "
+                                 "it contiguous")
+            table.append(fields)
+    with _Device(dev) as stream:
+        reorder_beams_raw(B, W, beams.data_ptr(), beams.element_size(), table, stream)
+    return targets[0] if single else targets

@@ -30,7 +30,9 @@ SOURCES = [(os.path.join(CSRC, "sgemm_f32.hip"), True),
            (os.path.join(CSRC, "sgemm_regpanel.hip"), False),
            (os.path.join(CSRC, "sgemm_persist.hip"), False),
            (os.path.join(CSRC, "gemm_i8.hip"), False),
-           (os.path.join(CSRC, "token_logprobs.hip"), True)]
+           (os.path.join(CSRC, "token_logprobs.hip"), True),
+           (os.path.join(CSRC, "gemm_mx4.hip"), False),
+           (os.path.join(CSRC, "beam_search.hip"), True)]
 ARCH = "gfx950"
 
 

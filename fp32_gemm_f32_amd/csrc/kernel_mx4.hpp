@@ -1,0 +1,233 @@
+// kernel_mx4.hpp -- kernels of gemm_mx4.h: the quantiser to microscaled 4-bit elements, its inverse,
+// and what the kernels of the product share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "kernel_mfma.hpp"
+#include "ops_common.hpp"
+
+namespace sgemm {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// ------------------------------------------------------------------ elements -----------
+// 2^(byte - 127) as FP32 (0 is the denormal 2^-127).
+__device__ inline float mx4_unit(uint32_t byte)
+{
+    return byte == 255 ? __builtin_nanf("") : __builtin_bit_cast(float, byte == 0 ? 0x00400000u : byte << 23);
+}
+// The scale's byte of a block whose largest magnitude has these bits as FP32: its exponent less the
+// format's own largest (2), 255 where it is no number. (A denormal's exponent reads as 0.)
+__device__ inline uint32_t mx4_scale(uint32_t peak)
+{
+    const int e = int(peak >> 23);
+    return e == 255 ? 255u : uint32_t(max(e - 2, 0));
+}
+
+// 8 elements over `unit` as codes, the first in the lowest bits: gfx950's conversion rounds to
+// nearest even and saturates, for every value and power of two.
+template <typename T> __device__ inline uint32_t mx4_encode(const Pack<T, 8> &x, float unit)
+{
+    uint32_t q = 0;
+    const auto pair = [&](auto i) __attribute__((always_inline)) {
+        constexpr int e = 2 * decltype(i)::value;
+        if constexpr (sizeof(T) == 4) {
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, x.v[e], x.v[e + 1], unit, e / 2);
+        } else if constexpr (__is_same(T, __bf16)) {
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, bf16x2{x.v[e], x.v[e + 1]}, unit, e / 2);
+        } else {
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, f16x2{x.v[e], x.v[e + 1]}, unit, e / 2);
+        }
+    };
+    static_for<0, 4>(pair);
+    return q;
+}
+template <typename T> __device__ inline Pack<T, 8> mx4_decode(uint32_t q, float unit)
+{
+    Pack<T, 8> x;
+    static_for<0, 4>([&](auto i) __attribute__((always_inline)) {
+        constexpr int e = 2 * decltype(i)::value;
+        if constexpr (sizeof(T) == 4) {
+            const auto v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, unit, e / 2);
+            x.v[e] = v[0];
+            x.v[e + 1] = v[1];
+        } else if constexpr (__is_same(T, __bf16)) {
+            const auto v = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, unit, e / 2);
+            x.v[e] = v[0];
+            x.v[e + 1] = v[1];
+        } else {
+            const auto v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, unit, e / 2);
+            x.v[e] = v[0];
+            x.v[e + 1] = v[1];
+        }
+    });
+    return x;
+}
+
+// t / d == mulhi(t, mul) >> shift for t < 2^31.
+struct Mx4Divisor {
+    uint32_t mul;
+    int shift;
+};
+__device__ inline int mx4_divide(int t, Mx4Divisor d) { return int(__umulhi(uint32_t(t), d.mul) >> d.shift); }
+
+struct Mx4RowArgs {
+    const void *X;             // (the inverse: the values written)
+    int64_t ldx;
+    uint8_t *Q;
+    int64_t ldq;
+    uint8_t *scales;
+    int64_t lds;
+    int M, K, units;           // units of 8 elements to a row, whole blocks of them
+    Mx4Divisor by_units;
+};
+
+// Four lanes share a block, 8 elements each. HBM-bound: 2 or 4 bytes in and 17 / 32 out of an element.
+template <int DT>
+__global__ __launch_bounds__(256) void k_mx4_quantize(Mx4RowArgs p)
+{
+    typedef typename Elem<DT>::type T;
+    const int e = int(blockIdx.x) * 256 + int(threadIdx.x);
+    const int row = mx4_divide(e, p.by_units), unit = e - row * p.units, k = unit * 8;
+    const bool mine = row < p.M;
+    const T *x = static_cast<const T *>(p.X) + row * p.ldx + k;
+    Pack<T, 8> v;
+    if (mine && k + 8 <= p.K) {
+        v = load_pack<T, 8>(x);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v.v[j] = mine && k + j < p.K ? x[j] : T(0.0f);
+    }
+    uint32_t peak = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        peak = max(peak, __builtin_bit_cast(uint32_t, Elem<DT>::widen(v.v[j])) & 0x7fffffffu);
+    const auto moved = [](uint32_t a, auto ctrl) {
+        return uint32_t(__builtin_amdgcn_update_dpp(0, int(a), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    peak = max(peak, moved(peak, std::integral_constant<int, 0xb1>{}));     // lane ^ 1
+    peak = max(peak, moved(peak, std::integral_constant<int, 0x4e>{}));     // lane ^ 2
+    const uint32_t s = mx4_scale(peak);
+    const uint32_t q = s == 255 ? 0 : mx4_encode<T>(v, mx4_unit(s));
+    if (!mine) return;
+    uint8_t *out = p.Q + row * p.ldq + k / 2;
+    const int bytes = (p.K + 1) / 2 - k / 2;
+    if (bytes >= 4) {
+        *reinterpret_cast<Pack<uint32_t, 1> *>(out) = Pack<uint32_t, 1>{{q}};
+    } else {
+        for (int j = 0; j < bytes; ++j) out[j] = uint8_t(q >> 8 * j);
+    }
+    if (unit % 4 == 0 && k < p.K) p.scales[row * p.lds + unit / 4] = uint8_t(s);
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_mx4_dequantize(Mx4RowArgs p)
+{
+    typedef typename Elem<DT>::type T;
+    const int e = int(blockIdx.x) * 256 + int(threadIdx.x);
+    const int row = mx4_divide(e, p.by_units), unit = e - row * p.units, k = unit * 8;
+    if (row >= p.M || k >= p.K) return;
+    const uint8_t *in = p.Q + row * p.ldq + k / 2;
+    const float size = mx4_unit(p.scales[row * p.lds + unit / 4]);
+    T *y = static_cast<T *>(const_cast<void *>(p.X)) + row * p.ldx + k;
+    if (k + 8 <= p.K) {
+        store_pack(y, mx4_decode<T>(load_pack<uint32_t, 1>(reinterpret_cast<const uint32_t *>(in)).v[0], size));
+    } else {
+        uint32_t q = 0;
+        for (int j = 0; j < (p.K - k + 1) / 2; ++j) q |= uint32_t(in[j]) << 8 * j;
+        const Pack<T, 8> v = mx4_decode<T>(q, size);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (k + j < p.K) y[j] = v.v[j];
+    }
+}
+
+// ------------------------------------------------------------------ the product ---------
+struct Mx4Args {
+    const uint8_t *A, *B, *sa, *sb;
+    const float *bias;         // or NULL
+    void *C;
+    float *partial;            // splits > 1: sums of split s at partial + s * M * N
+    int64_t lda, ldb, ldsa, ldsb, ldc;
+    int M, N, KB;              // KB: bytes to a row, K / 2
+    int c_dtype, tiles_m, tiles_n;
+    int splits, chunk;         // split s covers bytes [s * chunk, min(KB, (s + 1) * chunk))
+};
+
+template <int DT, int W, bool STREAM = false>
+__device__ inline void mx4_store(void *C, int64_t at, const float (&v)[W], int valid)
+{
+    typedef typename Elem<DT>::type T;
+    T *c = static_cast<T *>(C) + at;
+    if (valid >= W) {
+        Pack<T, W> p;
+#pragma unroll
+        for (int j = 0; j < W; ++j) p.v[j] = Elem<DT>::narrow(v[j]);
+        if constexpr (STREAM) store_pack_stream(c, p);
+        else store_pack(c, p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            if (j < valid) c[j] = Elem<DT>::narrow(v[j]);
+    }
+}
+__device__ inline void mx4_store_one(int dtype, void *C, int64_t at, float x)
+{
+    const float v[1] = {x};
+    if (dtype == SGEMM_DTYPE_BF16) mx4_store<SGEMM_DTYPE_BF16, 1>(C, at, v, 1);
+    else if (dtype == SGEMM_DTYPE_F16) mx4_store<SGEMM_DTYPE_F16, 1>(C, at, v, 1);
+    else mx4_store<SGEMM_DTYPE_F32, 1>(C, at, v, 1);
+}
+
+// 16 bytes of a row from byte k on; zeros from byte kn on, and no byte past it is read. A row of 16
+// bytes and more is read at its last 16, which are moved into place.
+__device__ inline i32x4 mx4_load_tail(const uint8_t *row, int k, int kn)
+{
+    unsigned __int128 v = 0;
+    if (k < kn) {
+        if (kn >= 16) {
+            const int at = min(k, kn - 16);
+            const Pack<int, 4> w = load_pack<int, 4>(reinterpret_cast<const int *>(row + at));
+            v = __builtin_bit_cast(unsigned __int128, w) >> (8 * (k - at));
+        } else {
+            for (int e = kn - 1; e >= k; --e) v = v << 8 | row[e];
+        }
+    }
+    return __builtin_bit_cast(i32x4, v);
+}
+__device__ inline i32x4 mx4_load16(const uint8_t *p)
+{
+    return __builtin_bit_cast(i32x4, load_pack<int, 4>(reinterpret_cast<const int *>(p)));
+}
+
+// Adds the splits' sums in their order; one thread per element of C, strided over the grid.
+__global__ __launch_bounds__(256) void k_mx4_join(Mx4Args p)
+{
+    const int64_t total = int64_t(p.M) * p.N;
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < total; e += int64_t(gridDim.x) * 256) {
+        const int64_t m = e / p.N;
+        const int n = int(e - m * p.N);
+        float sum = 0.0f;
+        for (int s = 0; s < p.splits; ++s) sum += p.partial[s * total + e];
+        mx4_store_one(p.c_dtype, p.C, m * p.ldc + n, p.bias ? sum + p.bias[n] : sum);
+    }
+}
+
+// K == 0: the empty sum plus the bias.
+__global__ __launch_bounds__(256) void k_mx4_empty(Mx4Args p)
+{
+    const int64_t total = int64_t(p.M) * p.N;
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < total; e += int64_t(gridDim.x) * 256) {
+        const int64_t m = e / p.N;
+        const int n = int(e - m * p.N);
+        mx4_store_one(p.c_dtype, p.C, m * p.ldc + n, p.bias ? p.bias[n] : 0.0f);
+    }
+}
+
+}  // namespace sgemm

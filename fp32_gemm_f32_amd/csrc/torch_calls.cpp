@@ -17,7 +17,9 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "beam_search.h"
 #include "gemm_i8.h"
+#include "gemm_mx4.h"
 #include "sgemm_dtype.h"
 #include "sgemm_f32.h"
 #include "token_logprobs.h"
@@ -246,6 +248,309 @@ PyObject *token_logprobs_backward_(PyObject *, PyObject *const *args, Py_ssize_t
     END_HANDLE_TH_ERRORS
 }
 
+// ---- 4-bit operands
+
+// Rows of bytes as the Python layer's _padded allocates them: their distance.
+int64_t padded(int64_t rows, int64_t cols) { return cols % 4 == 0 || rows < 2 ? std::max<int64_t>(cols, 1) : (cols + 15) / 16 * 16; }
+at::Tensor empty_padded(int64_t rows, int64_t cols, const at::Device &device)
+{
+    const int64_t ld = padded(rows, cols);
+    if (ld == cols || cols == 0) return empty({rows, cols}, at::kByte, device);
+    return empty({rows, ld}, at::kByte, device).narrow(1, 0, cols);
+}
+
+// A packed matrix with its scales.
+struct Packed {
+    Matrix q, s;
+    const uint8_t *data = nullptr, *scales = nullptr;
+    bool ok;
+    Packed(const at::Tensor &t, const at::Tensor &u) : q(t), s(u)
+    {
+        ok = q.ok && s.ok && t.scalar_type() == at::kByte && u.scalar_type() == at::kByte &&
+             t.device() == u.device() && s.rows == q.rows && s.cols == (int64_t(q.cols) + 15) / 16 &&
+             q.cols <= INT_MAX / 2;
+        if (!ok) return;
+        data = static_cast<const uint8_t *>(t.data_ptr());
+        scales = static_cast<const uint8_t *>(u.data_ptr());
+    }
+};
+
+int quantize_into(const at::Tensor &x, const Matrix &m, int code, const at::Tensor &q, const at::Tensor &scales,
+                  void *stream)
+{
+    return gemm_mx4_quantize(m.rows, m.cols, x.data_ptr(), code, m.ld, static_cast<uint8_t *>(q.data_ptr()),
+                             padded(m.rows, q.size(1)), static_cast<uint8_t *>(scales.data_ptr()),
+                             padded(m.rows, scales.size(1)), stream);
+}
+int64_t packed_columns(int64_t k) { return (k + 1) / 2; }
+int64_t packed_blocks(int64_t k) { return (k + 31) / 32; }
+
+// quantize_mx4(X) -> (Q, scales) or None
+PyObject *quantize_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    const at::Tensor *x = n == 1 ? plain(args[0]) : nullptr;
+    if (!x) return none();
+    const Matrix m(*x);
+    const int code = dtype_code(x->scalar_type());
+    if (!m.ok || code < 0) return none();
+    at::Tensor q, scales;
+    int status;
+    {
+        pybind11::gil_scoped_release release;
+        const Place place(x->device());
+        q = empty_padded(m.rows, packed_columns(m.cols), x->device());
+        scales = empty_padded(m.rows, packed_blocks(m.cols), x->device());
+        status = quantize_into(*x, m, code, q, scales, place.stream);
+    }
+    if (status != SGEMM_OK) return none();
+    return PyTuple_Pack(2, py::reinterpret_steal<py::object>(THPVariable_Wrap(q)).ptr(),
+                        py::reinterpret_steal<py::object>(THPVariable_Wrap(scales)).ptr());
+    END_HANDLE_TH_ERRORS
+}
+
+// dequantize_mx4(Q, scales, type, columns or -1) -> values or None
+PyObject *dequantize_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 4 || !PyLong_CheckExact(args[2]) || !PyLong_CheckExact(args[3])) return none();
+    const at::Tensor *q = plain(args[0]), *scales = plain(args[1]);
+    if (!q || !scales) return none();
+    const Packed p(*q, *scales);
+    const int code = int(PyLong_AsLong(args[2]));
+    long columns = PyLong_AsLong(args[3]);
+    if (PyErr_Occurred()) PyErr_Clear();
+    if (!p.ok || code < 0 || code > 2) return none();
+    if (columns == -1) columns = 2L * p.q.cols;
+    if (columns < 0 || packed_columns(columns) != p.q.cols) return none();
+    at::Tensor y;
+    int status;
+    {
+        pybind11::gil_scoped_release release;
+        const Place place(q->device());
+        y = empty({p.q.rows, columns}, scalar_type(code), q->device());
+        status = gemm_mx4_dequantize(p.q.rows, int(columns), p.data, p.q.ld, p.scales, p.s.ld, y.data_ptr(), code,
+                                     std::max<int64_t>(columns, 1), place.stream);
+    }
+    return status == SGEMM_OK ? THPVariable_Wrap(y) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// The product of packed A (given by its parts) and B into a new tensor.
+int product_mx4(const uint8_t *a, int64_t lda, const uint8_t *sa, int64_t ldsa, int M, const Packed &b, int K,
+                const MaybeVector &bias, int code, const at::Device &device, void *stream, at::Tensor &c)
+{
+    at::Tensor space;
+    c = empty({M, b.q.rows}, scalar_type(code), device);
+    const size_t bytes = gemm_mx4_workspace_size(M, b.q.rows, K, a, lda, sa, ldsa, b.data, b.q.ld, b.scales, b.s.ld);
+    if (bytes) space = empty({int64_t(bytes)}, at::kByte, device);
+    return gemm_mx4(M, b.q.rows, K, a, lda, sa, ldsa, b.data, b.q.ld, b.scales, b.s.ld, bias.data(), c.data_ptr(),
+                    code, std::max(b.q.rows, 1), bytes ? space.data_ptr() : nullptr, bytes, stream);
+}
+
+// matmul_mx4(A, a_scales, B, b_scales, bias or None, type of C) -> C or None
+PyObject *matmul_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 6) return none();
+    const at::Tensor *a = plain(args[0]), *sa = plain(args[1]), *b = plain(args[2]), *sb = plain(args[3]);
+    if (!a || !sa || !b || !sb) return none();
+    const at::Device device = a->device();
+    const Packed pa(*a, *sa), pb(*b, *sb);
+    const int code = int(PyLong_AsLong(args[5]));
+    if (!pa.ok || !pb.ok || pa.q.cols != pb.q.cols || b->device() != device || code < 0 || code > 2) return none();
+    const MaybeVector bias(args[4], pb.q.rows, device);
+    if (!bias.ok) return none();
+    at::Tensor c;
+    int status;
+    {
+        pybind11::gil_scoped_release release;
+        const Place place(device);
+        status = product_mx4(pa.data, pa.q.ld, pa.scales, pa.s.ld, pa.q.rows, pb, 2 * pa.q.cols, bias, code, device,
+                             place.stream, c);
+    }
+    return status == SGEMM_OK ? THPVariable_Wrap(c) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// linear_mx4(X, B, b_scales, bias or None, type of C or -1) -> C or None
+PyObject *linear_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 5) return none();
+    const at::Tensor *x = plain(args[0]), *b = plain(args[1]), *sb = plain(args[2]);
+    if (!x || !b || !sb) return none();
+    const at::Device device = x->device();
+    const Matrix m(*x);
+    const Packed pb(*b, *sb);
+    const int type = dtype_code(x->scalar_type());
+    int code = int(PyLong_AsLong(args[4]));
+    if (code == -1) code = type;
+    if (!m.ok || !pb.ok || type < 0 || code < 0 || code > 2 || b->device() != device ||
+        pb.q.cols != packed_columns(m.cols))
+        return none();
+    const MaybeVector bias(args[3], pb.q.rows, device);
+    if (!bias.ok) return none();
+    at::Tensor q, scales, c;
+    int status;
+    {
+        pybind11::gil_scoped_release release;
+        const Place place(device);
+        q = empty_padded(m.rows, pb.q.cols, device);
+        scales = empty_padded(m.rows, pb.s.cols, device);
+        status = quantize_into(*x, m, type, q, scales, place.stream);
+        if (status == SGEMM_OK)
+            status = product_mx4(static_cast<const uint8_t *>(q.data_ptr()), padded(m.rows, pb.q.cols),
+                                 static_cast<const uint8_t *>(scales.data_ptr()), padded(m.rows, pb.s.cols), m.rows,
+                                 pb, 2 * pb.q.cols, bias, code, device, place.stream, c);
+    }
+    return status == SGEMM_OK ? THPVariable_Wrap(c) : none();
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- beam search
+
+// beam_step(logits, scores, top or -1, finished or None, pad_token) -> (scores, beams, tokens) or None
+PyObject *beam_step_(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 5 || !PyLong_CheckExact(args[2]) || !PyLong_CheckExact(args[4])) return none();
+    const at::Tensor *x = plain(args[0]), *scores = plain(args[1]);
+    const at::Tensor *finished = args[3] == Py_None ? nullptr : plain(args[3]);
+    if (!x || !scores || (args[3] != Py_None && !finished)) return none();
+    const Matrix m(*x);
+    const int code = dtype_code(x->scalar_type());
+    const at::Device device = x->device();
+    const auto per_beam = [&](const at::Tensor &t, at::ScalarType type) {
+        return t.scalar_type() == type && t.dim() == 2 && t.is_contiguous() && t.device() == device && !t.is_neg() &&
+               t.size(0) <= INT_MAX && t.size(1) <= BEAM_MAX;
+    };
+    long top = PyLong_AsLong(args[2]);
+    const long long pad_token = PyLong_AsLongLong(args[4]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return none();
+    }
+    if (!m.ok || code < 0 || !per_beam(*scores, at::kFloat)) return none();
+    const int64_t B = scores->size(0), W = scores->size(1);
+    if (finished && (!per_beam(*finished, at::kBool) || finished->size(0) != B || finished->size(1) != W))
+        return none();
+    if (top == -1) top = W;
+    if (m.rows != B * W || W < 1 || top < 1 || top > BEAM_MAX) return none();
+    at::Tensor out[3], space;
+    int status;
+    {
+        pybind11::gil_scoped_release release;
+        const Place place(device);
+        out[0] = empty({B, top}, at::kFloat, device);
+        out[1] = empty({B, top}, at::kLong, device);
+        out[2] = empty({B, top}, at::kLong, device);
+        const size_t bytes = beam_step_workspace_size(int(B), int(W), m.cols, code, int(top));
+        if (bytes) space = empty({int64_t(bytes)}, at::kByte, device);
+        status = beam_step(int(B), int(W), m.cols, x->data_ptr(), code, m.ld,
+                           static_cast<const float *>(scores->data_ptr()),
+                           finished ? static_cast<const uint8_t *>(finished->data_ptr()) : nullptr, pad_token, int(top),
+                           static_cast<float *>(out[0].data_ptr()), static_cast<int64_t *>(out[1].data_ptr()),
+                           static_cast<int64_t *>(out[2].data_ptr()), bytes ? space.data_ptr() : nullptr, bytes,
+                           place.stream);
+    }
+    if (status != SGEMM_OK) return none();
+    return PyTuple_Pack(3, py::reinterpret_steal<py::object>(THPVariable_Wrap(out[0])).ptr(),
+                        py::reinterpret_steal<py::object>(THPVariable_Wrap(out[1])).ptr(),
+                        py::reinterpret_steal<py::object>(THPVariable_Wrap(out[2])).ptr());
+    END_HANDLE_TH_ERRORS
+}
+
+// beam_state's fields for two tensors of one shape; false where they have more than two dimensions of
+// pieces.
+bool state_of(const at::Tensor &src, const at::Tensor &dst, beam_state &s)
+{
+    const int64_t size = int64_t(src.element_size());
+    struct Dim { int64_t n, src, dst; } dims[3];
+    int count = 0;
+    for (int64_t d = 1; d < src.dim(); ++d) {
+        const int64_t n = src.size(d), a = src.stride(d) * size, b = dst.stride(d) * size;
+        if (n == 1) continue;
+        if (count > 0 && dims[count - 1].src == n * a && dims[count - 1].dst == n * b) {
+            dims[count - 1] = {dims[count - 1].n * n, a, b};
+        } else {
+            if (count == 3) return false;
+            dims[count++] = {n, a, b};
+        }
+    }
+    s.run = size;
+    if (count > 0 && dims[count - 1].src == size && dims[count - 1].dst == size) s.run *= dims[--count].n;
+    if (count > 2) return false;
+    const Dim none = {1, 0, 0};
+    const Dim d1 = count == 2 ? dims[0] : none, d2 = count > 0 ? dims[count - 1] : none;
+    s.src = src.data_ptr();
+    s.dst = dst.data_ptr();
+    s.src_row = src.size(0) > 1 ? src.stride(0) * size : 0;
+    s.dst_row = src.size(0) > 1 ? dst.stride(0) * size : 0;
+    s.count1 = d1.n; s.src_step1 = d1.src; s.dst_step1 = d1.dst;
+    s.count2 = d2.n; s.src_step2 = d2.src; s.dst_step2 = d2.dst;
+    return true;
+}
+
+// reorder_beams(states, beams, out or None) -> out, or None: sequences of tensors only
+PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 3) return none();
+    const at::Tensor *beams = plain(args[1]);
+    const auto listed = [](PyObject *o) { return PyList_CheckExact(o) || PyTuple_CheckExact(o); };
+    if (!beams || !listed(args[0]) || (args[2] != Py_None && !listed(args[2]))) return none();
+    if (beams->dim() != 2 || !beams->is_contiguous() || !beams->is_cuda() || beams->is_neg() ||
+        beams->size(0) > INT_MAX || beams->size(1) > BEAM_MAX ||
+        (beams->scalar_type() != at::kLong && beams->scalar_type() != at::kInt))
+        return none();
+    const at::Device device = beams->device();
+    const int64_t rows = beams->size(0) * beams->size(1);
+    const Py_ssize_t count = PySequence_Fast_GET_SIZE(args[0]);
+    const bool given = args[2] != Py_None;
+    if (given && PySequence_Fast_GET_SIZE(args[2]) != count) return none();
+    std::vector<at::Tensor> src, dst;
+    std::vector<beam_state> states;
+    src.reserve(size_t(count));
+    dst.reserve(size_t(count));
+    states.reserve(size_t(count));
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor *t = plain(PySequence_Fast_GET_ITEM(args[0], i));
+        if (!t || t->device() != device || t->layout() != at::kStrided || t->dim() < 1 || t->size(0) != rows ||
+            t->is_neg() || t->is_conj())
+            return none();
+        src.push_back(*t);
+        if (!given) continue;
+        const at::Tensor *o = plain(PySequence_Fast_GET_ITEM(args[2], i));
+        if (!o || o->device() != device || o->layout() != at::kStrided || o->scalar_type() != t->scalar_type() ||
+            o->sizes() != t->sizes() || o->is_neg() || o->is_conj())
+            return none();
+        dst.push_back(*o);
+    }
+    int status;
+    bool fits = true;
+    {
+        pybind11::gil_scoped_release release;
+        const Place place(device);
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            if (!given) dst.push_back(empty(src[i].sizes(), src[i].scalar_type(), device));
+            beam_state s;
+            if (src[i].numel() == 0) continue;
+            if (!state_of(src[i], dst[i], s)) { fits = false; break; }
+            states.push_back(s);
+        }
+        status = !fits ? int(SGEMM_EINVAL_DIM) : reorder_beams(int(beams->size(0)), int(beams->size(1)), beams->data_ptr(), int(beams->element_size()),
+                               states.data(), int(states.size()), place.stream);
+    }
+    if (status != SGEMM_OK) return none();
+    PyObject *r = PyList_New(count);
+    if (!r) return nullptr;
+    for (Py_ssize_t i = 0; i < count; ++i)
+        PyList_SET_ITEM(r, i, given ? Py_NewRef(PySequence_Fast_GET_ITEM(args[2], i)) : THPVariable_Wrap(dst[i]));
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
 template <typename F> PyCFunction fast(F *f)
 {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f));
@@ -255,6 +560,12 @@ PyMethodDef kMethods[] = {
     {"matmul_i8", fast(&matmul_i8), METH_FASTCALL, nullptr},
     {"token_logprobs", fast(&token_logprobs_), METH_FASTCALL, nullptr},
     {"token_logprobs_backward", fast(&token_logprobs_backward_), METH_FASTCALL, nullptr},
+    {"quantize_mx4", fast(&quantize_mx4), METH_FASTCALL, nullptr},
+    {"dequantize_mx4", fast(&dequantize_mx4), METH_FASTCALL, nullptr},
+    {"matmul_mx4", fast(&matmul_mx4), METH_FASTCALL, nullptr},
+    {"linear_mx4", fast(&linear_mx4), METH_FASTCALL, nullptr},
+    {"beam_step", fast(&beam_step_), METH_FASTCALL, nullptr},
+    {"reorder_beams", fast(&reorder_beams_), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
