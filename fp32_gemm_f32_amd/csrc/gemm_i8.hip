@@ -329,7 +329,7 @@ extern "C" int gemm_i8(int M, int N, int K, const int8_t *A, int64_t lda, const 
     if (plan.copy_a || plan.copy_b) {
         const int64_t ld16 = round16(K);
         const int per = int(std::max<int64_t>(1, 2048 / (ld16 / 16)));
-        I8Rows16 a16{}, b16{};
+        Rows16 a16{}, b16{};
         if (plan.copy_a) a16 = {A, static_cast<int8_t *>(workspace) + space.a, lda, M, per, int(ceil_div(M, per))};
         if (plan.copy_b) b16 = {B, static_cast<int8_t *>(workspace) + space.b, ldb, N, per, int(ceil_div(N, per))};
         st = launch(&k_gemm_i8_align, dim3(unsigned(a16.blocks + b16.blocks)), dim3(256), stream, a16, b16, K);

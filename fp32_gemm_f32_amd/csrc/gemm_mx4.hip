@@ -5,10 +5,12 @@
 #include <algorithm>
 #include <cstdint>
 #include <cstdio>
+#include <utility>
 
 #include "gemm_mx4.h"
 #include "kernel_mx4.hpp"
 #include "kernel_mx4_rows.hpp"
+#include "kernel_mx4_tiles.hpp"
 #include "ops_common.hpp"
 
 namespace sgemm {
@@ -51,24 +53,136 @@ int by_rows(Kernel kern, int M, int K, Elements *X, int size, int64_t ldx, const
     return SGEMM_OK;
 }
 
-struct Mx4Plan {
-    int tiles_m, tiles_n, splits, chunk;
+typedef void (*Mx4Kernel)(Mx4Args);
+
+// The tiles, smallest first. In microseconds: `c1` and `c2` are a panel of 256 elements with one and two
+// workgroups on every compute unit, `ends` a workgroup's start and stores, `next` what each further
+// tile of a workgroup that goes on adds to its panels.
+struct Mx4Variant {
+    const char *name;
+    Mx4Kernel kernel;
+    int bm, bn, threads;
+    int at_once;     // workgroups on a compute unit
+    int loop;        // panels from which a workgroup goes on to another tile, or 0
+    double c1, c2, ends, next;
 };
-Mx4Plan make_plan(int M, int N, int K, int cus)
+template <int BM, int BN, int WGM, int WGN, int NSTG>
+constexpr Mx4Variant tile(const char *name, double c1, double c2, double ends, double next)
 {
-    Mx4Plan p{};
-    const int kb = K / 2, turns = int(ceil_div(kb, kMx4Turn));
-    p.tiles_m = int(ceil_div(M, 16));
-    p.tiles_n = int(ceil_div(N, 16));
-    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
-    int want = int(std::min<int64_t>(std::max<int64_t>(1, 2 * cus / tiles), std::max(1, turns / kWaves)));
-    want = std::min(want, 16);
-    const int64_t chunk = ceil_div(turns, want) * kMx4Turn;
-    p.splits = int(ceil_div(kb, chunk));
-    p.chunk = int(std::min<int64_t>(chunk, kb));
-    return p;
+    typedef Mx4Tile<BM, BN, WGM, WGN, NSTG> T;
+    return {name, &k_mx4_tiles<T>, BM, BN, T::NT, T::LOOP ? 1 : 2, T::LOOP ? NSTG : 0, c1, c2, ends, next};
 }
-size_t space_of(const Mx4Plan &p, int M, int N) { return p.splits > 1 ? size_t(p.splits) * M * N * 4 : 0; }
+const Mx4Variant kTiles[] = {
+    tile<64, 32, 2, 1, 6>("mx4_64x32", 0.189, 0.27, 2.31, 0.0),
+    tile<64, 64, 2, 2, 4>("mx4_64x64", 0.200, 0.37, 1.84, 0.0),
+    tile<64, 128, 2, 4, 3>("mx4_64x128", 0.298, 0.52, 2.17, 0.0),
+    tile<128, 128, 4, 2, 2>("mx4_128x128", 0.506, 0.95, 1.19, 0.0),
+    tile<128, 128, 4, 2, 4>("mx4_128x128_s4", 0.408, 0.0, 2.04, 3.76),
+    tile<128, 256, 2, 4, 2>("mx4_128x256", 0.644, 0.0, 2.83, 7.49),
+    tile<192, 256, 2, 4, 2>("mx4_192x256", 0.962, 0.0, 3.46, 8.19),
+    tile<256, 256, 4, 2, 2>("mx4_256x256", 1.125, 0.0, 2.20, 7.80),
+};
+// Few rows: 16 rows and columns, turns of 512 elements to a wave.
+const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0};
+
+// The operands, and which of them can be loaded as they lie: rows on word boundaries.
+struct Mx4Operands {
+    const uint8_t *p[4];      // A, B, and their scales
+    int64_t ld[4];
+    bool ready(int i) const { return ld[i] % 4 == 0 && reinterpret_cast<uintptr_t>(p[i]) % 4 == 0; }
+};
+
+struct Mx4Plan {
+    const Mx4Variant *v;
+    int tiles_m, tiles_n, splits, chunk;
+    bool copy[4];
+    double cost;
+};
+
+constexpr double kLaunch = 2.5;          // us: a kernel's start and end
+constexpr double kStreamPerUs = 6.4e6;   // bytes of operands, from the last-level cache too
+
+// Whether workgroups go on to another tile, one to a compute unit.
+bool goes_on(const Mx4Variant &v, int64_t tiles, int splits, int64_t panels, int cus)
+{
+    return splits == 1 && v.loop > 0 && panels >= v.loop && tiles > cus;
+}
+// Microseconds of workgroups of `panels` panels each: whole rounds of them and what is left.
+double tile_cost(const Mx4Variant &v, int64_t groups, int splits, int64_t panels, int cus)
+{
+    const int64_t full = groups / (cus * v.at_once), rest = groups % (cus * v.at_once);
+    const int64_t rounds = full + (rest > 0);
+    if (goes_on(v, groups, splits, panels, cus))
+        return v.c1 * (double(rounds * panels) + 2.7) + v.ends + double(rounds - 1) * v.next;
+    const double whole = v.at_once == 2 ? v.c2 : v.c1;
+    const double tail = rest == 0 ? 0.0 : rest <= cus ? v.c1 : v.c2;
+    return (double(full) * whole + tail) * (double(panels) + 2.7) + double(rounds) * v.ends;
+}
+
+// The cheapest of every tile, K whole or split. (The cost orders choices and is no time.)
+Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
+{
+    Mx4Plan best{};
+    const int kb = K / 2;
+    const double bytes = (double(M) + double(N)) * K * 17 / 32;
+    const auto offer = [&](const Mx4Plan &p) {
+        if (best.v == nullptr || p.cost < best.cost) best = p;
+    };
+    const auto splits_of = [&](int want) {
+        const int64_t chunk = ceil_div(ceil_div(kb, 256), want) * 256;
+        return std::pair<int, int>(int(ceil_div(kb, chunk)), int(std::min<int64_t>(chunk, kb)));
+    };
+    const auto join_cost = [&](int splits) {
+        return splits == 1 ? 0.0 : 2.3 + double(splits + 1) * M * N * 4 / 1.9e6;
+    };
+    const int most = int(std::min<int64_t>(16, std::max<int64_t>(1, kb / 512)));
+    if (M <= 16) {
+        for (int want = 1; want <= most; ++want) {
+            const auto [s, chunk] = splits_of(want);
+            const int64_t groups = ceil_div(N, kRows.bn) * s;
+            if (s > 1 && groups > most_groups(kRows.threads)) break;     // splits take one launch
+            const double turn = double(ceil_div(chunk, kMx4Turn * kWaves)) * 0.8;
+            const double step = double(ceil_div(groups, 2 * cus)) * turn;
+            offer({&kRows, 1, int(ceil_div(N, kRows.bn)), s, chunk, {},
+                   kLaunch + 1.0 + std::max(step, bytes / 4.6e6) + join_cost(s)});
+        }
+        return best;
+    }
+    bool copy[4];
+    double copied = 0.0;
+    for (int i = 0; i < 4; ++i) {
+        copy[i] = !x.ready(i);
+        if (copy[i]) copied += double(i % 2 == 0 ? M : N) * K / (i < 2 ? 2 : 32);
+    }
+    for (const Mx4Variant &v : kTiles) {
+        const int64_t tm = ceil_div(M, v.bm), tn = ceil_div(N, v.bn);
+        for (int want = 1; want <= most; ++want) {
+            const auto [s, chunk] = splits_of(want);
+            if (s > 1 && tm * tn * s > 2 * int64_t(cus)) break;
+            const double work = tile_cost(v, tm * tn * s, s, ceil_div(chunk, 128), cus), reads = bytes / kStreamPerUs;
+            const double body = std::max(work, reads) + 0.02 * std::min(work, reads);   // reads alone tie
+            offer({&v, int(tm), int(tn), s, chunk, {copy[0], copy[1], copy[2], copy[3]},
+                   kLaunch + body + join_cost(s) + (copied > 0.0 ? 4.6 + 2.0 * copied / 6.8e6 : 0.0)});
+        }
+    }
+    return best;
+}
+
+// Workspace: the splits' sums, then the copies.
+struct Mx4Space {
+    int64_t at[4], bytes;     // offsets of the copies, the whole
+};
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+Mx4Space space_of(const Mx4Plan &p, int M, int N, int K)
+{
+    Mx4Space s{};
+    s.bytes = p.splits > 1 ? round16(int64_t(p.splits) * M * N * 4) : 0;
+    for (int i = 0; i < 4; ++i) {
+        s.at[i] = s.bytes;
+        if (p.copy[i]) s.bytes += int64_t(i % 2 == 0 ? M : N) * round16(ceil_div(K, i < 2 ? 2 : 32));
+    }
+    return s;
+}
 
 bool shape_in_limits(int M, int N, int64_t lda, int64_t lda_scales, int64_t ldb, int64_t ldb_scales)
 {
@@ -126,14 +240,14 @@ extern "C" size_t gemm_mx4_workspace_size(int M, int N, int K, const uint8_t *A,
                                           int64_t lda_scales, const uint8_t *B, int64_t ldb,
                                           const uint8_t *b_scales, int64_t ldb_scales)
 {
-    (void)A; (void)B; (void)a_scales; (void)b_scales;
     const int kb = K / 2, blocks = int(ceil_div(K, 32));
     if (M <= 0 || N <= 0 || K <= 0 || K % 2 || lda < kb || ldb < kb || lda_scales < blocks || ldb_scales < blocks ||
         !shape_in_limits(M, N, lda, lda_scales, ldb, ldb_scales))
         return 0;
     int cus = 0;
     if (device_cus(&cus) != SGEMM_OK) return 0;
-    return space_of(make_plan(M, N, K, cus), M, N);
+    const Mx4Operands x = {{A, B, a_scales, b_scales}, {lda, ldb, lda_scales, ldb_scales}};
+    return size_t(space_of(make_plan(M, N, K, x, cus), M, N, K).bytes);
 }
 
 extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, const uint8_t *a_scales,
@@ -168,33 +282,63 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
     int cus = 0;
     int st = device_cus(&cus);
     if (st != SGEMM_OK) return st;
-    const Mx4Plan plan = make_plan(M, N, K, cus);
-    if (workspace_bytes < space_of(plan, M, N)) return SGEMM_EINVAL_ARG;
+    Mx4Operands x = {{A, B, a_scales, b_scales}, {lda, ldb, lda_scales, ldb_scales}};
+    const Mx4Plan plan = make_plan(M, N, K, x, cus);
+    const Mx4Space space = space_of(plan, M, N, K);
+    if (workspace_bytes < size_t(space.bytes)) return SGEMM_EINVAL_ARG;
+    Mx4Copies copies{};
+    int copy_blocks = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (!plan.copy[i]) continue;
+        const int rows = i % 2 == 0 ? M : N, bytes = i < 2 ? kb : blocks;
+        const int64_t ld16 = round16(bytes);
+        const int per = int(std::max<int64_t>(1, 2048 / (ld16 / 16)));
+        int8_t *to = static_cast<int8_t *>(workspace) + space.at[i];
+        copies.rows[i] = {reinterpret_cast<const int8_t *>(x.p[i]), to, x.ld[i], rows, per, int(ceil_div(rows, per))};
+        copies.bytes[i] = bytes;
+        copy_blocks += copies.rows[i].blocks;
+        x.p[i] = reinterpret_cast<const uint8_t *>(to);
+        x.ld[i] = ld16;
+    }
+    if (copy_blocks > 0) {
+        st = launch(&k_mx4_align, dim3(unsigned(copy_blocks)), dim3(256), stream, copies);
+        if (st != SGEMM_OK) return st;
+    }
+    p.lda = x.ld[0]; p.ldb = x.ld[1]; p.ldsa = x.ld[2]; p.ldsb = x.ld[3];
     p.partial = static_cast<float *>(workspace);
-    p.splits = plan.splits; p.chunk = plan.chunk;
-    // C in parts that one launch each may take, almost always one (split products have few tiles)
-    const int64_t most = most_groups(64 * kWaves);
-    const int64_t part_m = std::min<int64_t>(plan.tiles_m, most), part_n = std::min<int64_t>(plan.tiles_n, most / part_m);
-    const Mx4Args whole = p;
+    p.splits = plan.splits; p.chunk = plan.splits > 1 ? plan.chunk : kb;
+    const Mx4Variant &v = *plan.v;
+    const bool loops = goes_on(v, int64_t(plan.tiles_m) * plan.tiles_n, plan.splits, ceil_div(kb, 128), cus);
+    // C in parts that one launch each may take, almost always one: no more workgroups than
+    // most_groups, rows and columns that a tile past the last of 2^31 - 1 would carry out of an int
+    // (split products are one part: make_plan gives them few tiles)
+    const int64_t most = loops ? INT64_MAX : most_groups(v.threads), most_rows = int64_t(1) << 30;
+    const int64_t part_m = std::min({int64_t(plan.tiles_m), most, most_rows / v.bm});
+    const int64_t part_n = std::min({int64_t(plan.tiles_n), most / part_m, most_rows / v.bn});
+    const int csize = dtype_bytes(c_dtype);
     for (int64_t tm = 0; tm < plan.tiles_m; tm += part_m)
         for (int64_t tn = 0; tn < plan.tiles_n; tn += part_n) {
-            const int64_t m = tm * 16, n = tn * 16;
+            const int64_t m = tm * v.bm, n = tn * v.bn;
             p.tiles_m = int(std::min(part_m, plan.tiles_m - tm));
             p.tiles_n = int(std::min(part_n, plan.tiles_n - tn));
-            p.M = int(std::min<int64_t>(M - m, part_m * 16));
-            p.N = int(std::min<int64_t>(N - n, part_n * 16));
-            p.A = whole.A + m * lda;
-            p.B = whole.B + n * ldb;
-            p.sa = whole.sa + m * lda_scales;
-            p.sb = whole.sb + n * ldb_scales;
+            p.M = int(std::min<int64_t>(M - m, part_m * v.bm));
+            p.N = int(std::min<int64_t>(N - n, part_n * v.bn));
+            p.A = x.p[0] + m * p.lda;
+            p.B = x.p[1] + n * p.ldb;
+            p.sa = x.p[2] + m * p.ldsa;
+            p.sb = x.p[3] + n * p.ldsb;
             p.bias = bias ? bias + n : nullptr;
-            p.C = static_cast<char *>(C) + (m * ldc + n) * dtype_bytes(c_dtype);
-            st = launch(&k_mx4_rows<kWaves>, dim3(unsigned(int64_t(p.tiles_m) * p.tiles_n * plan.splits)),
-                        dim3(64 * kWaves), stream, p);
+            p.C = static_cast<char *>(C) + (m * ldc + n) * csize;
+            p.stream = reinterpret_cast<uintptr_t>(p.C) % 64 == 0 && ldc * csize % 64 == 0;
+            const Mx4Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
+            p.group_mul = d.mul; p.group_shift = d.shift;
+            int64_t groups = int64_t(p.tiles_m) * p.tiles_n * plan.splits;
+            if (loops) groups = std::min<int64_t>(groups, cus);
+            st = launch(v.kernel, dim3(unsigned(groups)), dim3(v.threads), stream, p);
             if (st != SGEMM_OK) return st;
         }
     if (plan.splits == 1) return SGEMM_OK;
-    return launch(&k_mx4_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, whole);
+    return launch(&k_mx4_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 }
 
 extern "C" int gemm_mx4_plan_describe(int M, int N, int K, int num_cus, char *buf, int buflen)
@@ -208,9 +352,11 @@ extern "C" int gemm_mx4_plan_describe(int M, int N, int K, int num_cus, char *bu
         const int st = device_cus(&cus);
         if (st != SGEMM_OK) return st;
     }
-    const Mx4Plan p = make_plan(M, N, K, cus);
+    const Mx4Plan p = make_plan(M, N, K, {{}, {4, 4, 4, 4}}, cus);
     const int n = snprintf(buf, size_t(buflen),
-                           "{\"name\": \"mx4_rows16\", \"tiles\": [%d, %d], \"splits\": %d, \"workspace_bytes\": %lld}",
-                           p.tiles_m, p.tiles_n, p.splits, static_cast<long long>(space_of(p, M, N)));
+                           "{\"name\": \"%s\", \"BM\": %d, \"BN\": %d, \"threads\": %d, \"tiles\": [%d, %d], "
+                           "\"splits\": %d, \"chunk\": %d, \"cost_us\": %.2f, \"workspace_bytes\": %lld}",
+                           p.v->name, p.v->bm, p.v->bn, p.v->threads, p.tiles_m, p.tiles_n, p.splits, 2 * p.chunk, p.cost,
+                           static_cast<long long>(space_of(p, M, N, K).bytes));
     return n < buflen ? SGEMM_OK : SGEMM_EINVAL_ARG;
 }

@@ -6,12 +6,11 @@
 
 #include <cstdint>
 
-#include "kernel_mfma.hpp"
+#include "byte_tiles.hpp"
 #include "ops_common.hpp"
 
 namespace sgemm {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 struct I8Args {
@@ -26,7 +25,7 @@ struct I8Args {
     int M, N, K;
     int c_dtype;
     int tiles_m, tiles_n;
-    uint32_t group_mul;    // division by kGroupM * tiles_n without dividing: see i8_tile
+    uint32_t group_mul;    // division by kGroupM * tiles_n without dividing: see tile_of
     int group_shift;
     int splits, k_chunk;   // split s covers k in [s * k_chunk, min(K, (s + 1) * k_chunk))
     bool stream;           // C's rows start on lines of 64 bytes: store past the caches
@@ -38,32 +37,6 @@ struct I8Args {
 __device__ inline float i8_value(int sum, float sa, float sb, float bias)
 {
     return __builtin_fmaf(static_cast<float>(sum), sa * sb, bias);
-}
-
-template <int DT, int W, bool STREAM = false>
-__device__ inline void i8_store(void *C, int64_t at, const float (&v)[W], int valid)
-{
-    typedef typename Elem<DT>::type T;
-    T *c = static_cast<T *>(C) + at;
-    if (valid >= W) {
-        Pack<T, W> p;
-#pragma unroll
-        for (int j = 0; j < W; ++j) p.v[j] = Elem<DT>::narrow(v[j]);
-        if constexpr (STREAM) store_pack_stream(c, p);
-        else store_pack(c, p);
-    } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (j < valid) c[j] = Elem<DT>::narrow(v[j]);
-    }
-}
-
-template <int W>
-__device__ inline void i8_store_as(int dtype, void *C, int64_t at, const float (&v)[W], int valid)
-{
-    if (dtype == SGEMM_DTYPE_BF16) i8_store<SGEMM_DTYPE_BF16, W>(C, at, v, valid);
-    else if (dtype == SGEMM_DTYPE_F16) i8_store<SGEMM_DTYPE_F16, W>(C, at, v, valid);
-    else i8_store<SGEMM_DTYPE_F32, W>(C, at, v, valid);
 }
 
 // ------------------------------------------------------------------ the tile kernel ----
@@ -92,77 +65,11 @@ __device__ inline void i8_store_as(int dtype, void *C, int64_t at, const float (
 // TOP/s; 497 over a process's first launches) with the matrix pipes busy 75 % of the cycles at 1.59 GHz. Small ones by the latency of
 // a start, the first panels and the stores (1024^3 5.5 us), few rows by reading B (48 x 16384 x
 // 4096 13.0 us, 5.1 TB/s).
-template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_> struct I8Tile {
-    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, BK = BK_, NSTG = NSTG_;
-    static constexpr int NT = 64 * WGM * WGN;
-    static constexpr int WM = BM / WGM, WN = BN / WGN;
-    static constexpr int RB = WM / 32, CB = WN / 32;
-    static constexpr int CPR = BK / 16;              // chunks per row
-    static constexpr int STEPS = BK / 32;            // MFMA steps per panel
-    static constexpr int ACH = BM * CPR / NT, BCH = BN * CPR / NT;   // chunks per thread
-    static constexpr int A_BYTES = BM * BK, STAGE = (BM + BN) * BK;
-    static constexpr int SN = (BN + 63) / 64 * 64;   // floats B's scales take in LDS, and the bias
-    // one workgroup to a compute unit: it goes on to another tile
-    static constexpr bool LOOP = NSTG * STAGE > 80 * 1024;
-    static_assert(BM % 64 == 0, "A's scales are loaded 64 at a time");
-    static_assert(BM * CPR % NT == 0 && BN * CPR % NT == 0, "whole chunks per thread");
-    static_assert(NT / CPR % a_swizzle_period<CPR>() == 0, "one swizzle per thread");
+template <int BM_, int BN_, int WGM_, int WGN_, int BK_, int NSTG_>
+struct I8Tile : ByteTile<BM_, BN_, WGM_, WGN_, BK_, NSTG_> {
+    static constexpr int SN = (BN_ + 63) / 64 * 64;  // floats B's scales take in LDS, and the bias
+    static_assert(BM_ % 64 == 0, "A's scales are loaded 64 at a time");
 };
-
-// Global row of B (within the tile) at LDS row p.
-template <typename T> __device__ inline int i8_b_row(int p)
-{
-    const int w = p / T::WN, r = p % T::WN;
-    return w * T::WN + T::CB * (r % 32) + r / 32;
-}
-
-// ---- rows of any alignment
-// 16 bytes at any address from the aligned words that hold them: four words from the one
-// that holds the first byte, and the one that holds the last.
-struct Unaligned {
-    i32x4 body;
-    int last;
-};
-__device__ inline Unaligned load_words(const int8_t *base, uint32_t first, uint32_t last)
-{
-    return {*reinterpret_cast<const i32x4 *>(base + first), *reinterpret_cast<const int *>(base + last)};
-}
-// Moves them into place; the low two bits of `shift` are the address's.
-__device__ inline i32x4 join_words(const Unaligned &w, uint32_t shift)
-{
-    return i32x4{int(__builtin_amdgcn_alignbyte(w.body[1], w.body[0], shift)),
-                 int(__builtin_amdgcn_alignbyte(w.body[2], w.body[1], shift)),
-                 int(__builtin_amdgcn_alignbyte(w.body[3], w.body[2], shift)),
-                 int(__builtin_amdgcn_alignbyte(w.last, w.body[3], shift))};
-}
-// The first `left` of 16 bytes, zeros behind them.
-__device__ inline i32x4 keep_bytes(i32x4 v, int left)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int n = left - 4 * i;
-        v[i] = n >= 4 ? v[i] : n <= 0 ? 0 : v[i] & ((1 << 8 * n) - 1);
-    }
-    return v;
-}
-
-// The chunk of 16 bytes at k of a row that ends at kn, which the chunk may cross or lie past:
-// zeros from there on, and no byte past kn is read. A row of 16 bytes and more is read at
-// its last 16, which are moved into place.
-__device__ inline i32x4 load_tail(const int8_t *row, int k, int kn)
-{
-    unsigned __int128 v = 0;
-    if (k < kn) {
-        if (kn >= 16) {
-            const int at = min(k, kn - 16);
-            const Pack<int, 4> w = load_pack<int, 4>(reinterpret_cast<const int *>(row + at));
-            v = __builtin_bit_cast(unsigned __int128, w) >> (8 * (k - at));
-        } else {
-            for (int e = kn - 1; e >= k; --e) v = v << 8 | uint8_t(row[e]);
-        }
-    }
-    return __builtin_bit_cast(i32x4, v);
-}
 
 // Stores a wave's accumulators (or, in the split form, its sums): this lane's rows
 // 8 (v / 4) + v % 4 + 4 (l / 32) of each row block, columns CB (l % 32) + 0 .. CB - 1 of the
@@ -213,7 +120,7 @@ __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)
 #pragma unroll
                 for (int j = 0; j < T::CB; ++j) x[j] = i8_value(acc[i][j][v], sa[i][v], sb[j], bias[j]);
                 if (m < p.M)
-                    i8_store<decltype(dt)::value, T::CB, decltype(stream)::value>(p.C, m * p.ldc + col, x, valid);
+                    store_values<decltype(dt)::value, T::CB, decltype(stream)::value>(p.C, m * p.ldc + col, x, valid);
             }
     };
     auto store = [&](auto dt) __attribute__((always_inline)) {
@@ -223,47 +130,6 @@ __device__ __forceinline__ void i8_epilogue(const I8Args &p, const i32x16 (&acc)
     if (p.c_dtype == SGEMM_DTYPE_BF16) store(std::integral_constant<int, SGEMM_DTYPE_BF16>{});
     else if (p.c_dtype == SGEMM_DTYPE_F16) store(std::integral_constant<int, SGEMM_DTYPE_F16>{});
     else store(std::integral_constant<int, SGEMM_DTYPE_F32>{});
-}
-
-// Size of the resource that covers [from, end), `end` rounded up to a whole word.
-__device__ inline uint32_t i8_range(const int8_t *from, const int8_t *end)
-{
-    const int64_t n = end - from;
-    return n <= 0 ? 0u : n >= int64_t(kFullRange) ? kFullRange : (uint32_t(n) + 3u) & ~3u;
-}
-
-// 16 bytes a lane from base + off, zeros where that is past `range`, to LDS at `to` + 16 lanes.
-typedef __attribute__((address_space(3))) void *lds_ptr;
-__device__ __forceinline__ void i8_load16_lds(const int8_t *base, uint32_t range, uint32_t off, char *to)
-{
-    const auto rsrc = make_rsrc32(reinterpret_cast<const float *>(base), range);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 16, off, 0, 0, 0);
-}
-
-// 64 floats from base + first to LDS, at `to` + 4 lanes: zeros from `count` on.
-__device__ __forceinline__ void i8_load_floats(const float *base, int first, int count, int lane, char *to)
-{
-    const auto rsrc = make_rsrc32(base, uint32_t(max(count, 0)) * 4u);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_ptr)to, 4, (first + lane) * 4, 0, 0, 0);
-}
-
-// The tile of workgroup bid, in tile_coords' order. Divisions by numbers the host knows are a
-// product's upper half and a shift there (exact below 2^31): a division takes some 200 cycles that
-// nothing covers at a kernel's start.
-__device__ inline void i8_tile(const I8Args &p, int bid, int &tm, int &tn)
-{
-    const int t = xcd_contiguous(bid, p.tiles_m * p.tiles_n);
-    const int g = int(__umulhi(uint32_t(t), p.group_mul) >> p.group_shift);
-    const int w = t - g * kGroupM * p.tiles_n, first = g * kGroupM;
-    const int rows = min(p.tiles_m - first, kGroupM);
-    static_assert(kGroupM == 8, "whole groups are divided by shifts");
-    if (rows == kGroupM) {
-        tm = first + w % kGroupM;
-        tn = w / kGroupM;
-    } else {
-        tm = first + w % rows;
-        tn = w / rows;
-    }
 }
 
 template <typename T, bool ANY>
@@ -291,7 +157,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     uint32_t a_low = 0, b_low = 0, a_off[T::ACH], b_off[T::BCH];
     auto aim = [&](int tile) __attribute__((always_inline)) {
         int tm, tn;
-        i8_tile(p, tile, tm, tn);
+        tile_of(p, tile, tm, tn);
         m0 = tm * T::BM;
         n0 = tn * T::BN;
         At = p.A + m0 * p.lda + k0;
@@ -309,7 +175,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
         }
 #pragma unroll
         for (int i = 0; i < T::BCH; ++i) {
-            const int r = i8_b_row<T>(prow + i * (T::NT / T::CPR));
+            const int r = tile_b_row<T>(prow + i * (T::NT / T::CPR));
             b_off[i] = n0 + r < p.N ? (b_low + uint32_t(r * p.ldb) + q * 16) & ~3u : kOob;
         }
     };
@@ -338,7 +204,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
         for (int i = 0; i < T::RB; ++i) a_shift[i] = a_low + uint32_t(a_row + 32 * i) * uint32_t(p.lda);
 #pragma unroll
         for (int j = 0; j < T::CB; ++j)
-            b_shift[j] = b_low + uint32_t(i8_b_row<T>(b_row + 32 * j)) * uint32_t(p.ldb);
+            b_shift[j] = b_low + uint32_t(tile_b_row<T>(b_row + 32 * j)) * uint32_t(p.ldb);
     }
     auto read = [&](const char *st, auto tc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value;
@@ -384,17 +250,17 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     auto issue = [&](int panel, char *st) __attribute__((always_inline)) {
         const int k = panel * T::BK;
         const int8_t *const ak = At + k, *const bk = Bt + k;
-        const uint32_t an = ANY ? i8_range(ak, a_end) : kFullRange;
-        const uint32_t bn = ANY ? i8_range(bk, b_end) : kFullRange;
+        const uint32_t an = ANY ? bytes_range(ak, a_end) : kFullRange;
+        const uint32_t bn = ANY ? bytes_range(bk, b_end) : kFullRange;
         // in the range's last panel, and past it, chunks past its end read as zero (a row
         // that lies off its place by up to 3 bytes may end in the next chunk)
         const uint32_t past = k + q * 16 >= kn + (ANY ? 3 : 0) ? kOob : 0u;
 #pragma unroll
         for (int i = 0; i < T::ACH; ++i)
-            i8_load16_lds(ak, an, a_off[i] | past, st + (i * T::NT + wave * 64) * 16);
+            load16_lds(ak, an, a_off[i] | past, st + (i * T::NT + wave * 64) * 16);
 #pragma unroll
         for (int i = 0; i < T::BCH; ++i)
-            i8_load16_lds(bk, bn, b_off[i] | past, st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
+            load16_lds(bk, bn, b_off[i] | past, st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
     };
     // Operands are read LOOK steps ahead. LOOK steps before a panel's end the reads of its stage
     // are over, so the barrier comes there: the wave's loads of the next panel have landed, every
@@ -409,9 +275,9 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
         for (int i = wave; p.splits == 1 && i < (T::BM + 2 * T::SN) / 64; i += T::NT / 64) {
             char *to = at_lds + i * 256;
             const int at = i * 64;
-            if (at < T::BM) i8_load_floats(p.sa + m0, at, min(p.M - m0, T::BM), lane, to);
-            else if (at < T::BM + T::SN) i8_load_floats(p.sb + n0, at - T::BM, min(p.N - n0, T::BN), lane, to);
-            else if (p.bias) i8_load_floats(p.bias + n0, at - T::BM - T::SN, min(p.N - n0, T::BN), lane, to);
+            if (at < T::BM) load_floats_lds(p.sa + m0, at, min(p.M - m0, T::BM), lane, to);
+            else if (at < T::BM + T::SN) load_floats_lds(p.sb + n0, at - T::BM, min(p.N - n0, T::BN), lane, to);
+            else if (p.bias) load_floats_lds(p.bias + n0, at - T::BM - T::SN, min(p.N - n0, T::BN), lane, to);
         }
     };
     issue_scales(scales);
@@ -497,47 +363,11 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8(I8Args p)
     }
 }
 
-// ------------------------------------------------------------------ rows put in place ---
-// Copies rows of any length and alignment to rows of whole 16-byte chunks, zeros behind
-// their ends, for products large enough to earn it. A workgroup copies `rows` rows at a time
-// (about 2048 chunks), of A in its first blocks and of B in the others.
-struct I8Rows16 {
-    const int8_t *src;
-    int8_t *dst;
-    int64_t ld;
-    int count, rows, blocks;     // rows in all, rows to a workgroup, workgroups
-};
-
-__global__ __launch_bounds__(256) void k_gemm_i8_align(I8Rows16 a, I8Rows16 b, int K)
+// Rows put in place first, of A in the first blocks and of B in the others.
+__global__ __launch_bounds__(256) void k_gemm_i8_align(Rows16 a, Rows16 b, int K)
 {
     const bool of_a = int(blockIdx.x) < a.blocks;
-    const I8Rows16 &p = of_a ? a : b;
-    const int block = blockIdx.x - (of_a ? 0 : a.blocks);
-    const int cpr = (K + 15) / 16;
-    const int64_t row0 = int64_t(block) * p.rows;
-    const int n = min(p.rows, int(p.count - row0)) * cpr;
-    const int8_t *src = p.src + row0 * p.ld;
-    i32x4 *dst = reinterpret_cast<i32x4 *>(p.dst) + row0 * cpr;
-    constexpr int U = 4;
-    for (int e0 = threadIdx.x; e0 < n; e0 += 256 * U) {
-        Unaligned w[U];
-        uint32_t low[U];
-        int left[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int e = min(e0 + 256 * u, n - 1);
-            const int r = e / cpr, k = (e - r * cpr) * 16;
-            const int8_t *row = src + r * p.ld;
-            left[u] = K - k;
-            low[u] = uint32_t(reinterpret_cast<uintptr_t>(row + k)) & 3;
-            if (left[u] >= 16) w[u] = load_words(row + k - low[u], 0, (low[u] + 15) & ~3u);
-            else w[u] = {load_tail(row, k, K), 0};
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (e0 + 256 * u < n)
-                dst[e0 + 256 * u] = left[u] >= 16 ? join_words(w[u], low[u]) : w[u].body;
-    }
+    put_rows_in_place(of_a ? a : b, blockIdx.x - (of_a ? 0 : a.blocks), K);
 }
 
 // ------------------------------------------------------------------ the split's join ----
@@ -554,7 +384,7 @@ __global__ __launch_bounds__(256) void k_gemm_i8_join(I8Args p)
         int sum = 0;
         for (int s = 0; s < p.splits; ++s) sum += p.partial[s * total + e];
         const float x[1] = {i8_value(sum, p.sa[m], p.sb[n], p.bias ? p.bias[n] : 0.0f)};
-        i8_store_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
+        store_values_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
     }
 }
 
@@ -567,7 +397,7 @@ __global__ __launch_bounds__(256) void k_gemm_i8_empty(I8Args p)
         const int64_t m = e / p.N;
         const int n = int(e - m * p.N);
         const float x[1] = {p.bias ? p.bias[n] : 0.0f};
-        i8_store_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
+        store_values_as<1>(p.c_dtype, p.C, m * p.ldc + n, x, 1);
     }
 }
 

@@ -162,7 +162,7 @@ __global__ __launch_bounds__(T::NT) void k_gemm_i8_rows(I8Args p)
         return;
     }
     const float x[1] = {i8_value(sums[tid], esa, esb, ebias)};
-    i8_store_as<1>(p.c_dtype, p.C, em * p.ldc + en, x, 1);
+    store_values_as<1>(p.c_dtype, p.C, em * p.ldc + en, x, 1);
 }
 
 }  // namespace sgemm

@@ -6,12 +6,11 @@
 
 #include <cstdint>
 
-#include "kernel_mfma.hpp"
+#include "byte_tiles.hpp"
 #include "ops_common.hpp"
 
 namespace sgemm {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -157,49 +156,21 @@ struct Mx4Args {
     int64_t lda, ldb, ldsa, ldsb, ldc;
     int M, N, KB;              // KB: bytes to a row, K / 2
     int c_dtype, tiles_m, tiles_n;
+    uint32_t group_mul;        // division by kGroupM * tiles_n without dividing: see tile_of
+    int group_shift;
+    bool stream;               // C's rows start on lines of 64 bytes: store past the caches
     int splits, chunk;         // split s covers bytes [s * chunk, min(KB, (s + 1) * chunk))
 };
 
-template <int DT, int W, bool STREAM = false>
-__device__ inline void mx4_store(void *C, int64_t at, const float (&v)[W], int valid)
-{
-    typedef typename Elem<DT>::type T;
-    T *c = static_cast<T *>(C) + at;
-    if (valid >= W) {
-        Pack<T, W> p;
-#pragma unroll
-        for (int j = 0; j < W; ++j) p.v[j] = Elem<DT>::narrow(v[j]);
-        if constexpr (STREAM) store_pack_stream(c, p);
-        else store_pack(c, p);
-    } else {
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (j < valid) c[j] = Elem<DT>::narrow(v[j]);
-    }
-}
 __device__ inline void mx4_store_one(int dtype, void *C, int64_t at, float x)
 {
     const float v[1] = {x};
-    if (dtype == SGEMM_DTYPE_BF16) mx4_store<SGEMM_DTYPE_BF16, 1>(C, at, v, 1);
-    else if (dtype == SGEMM_DTYPE_F16) mx4_store<SGEMM_DTYPE_F16, 1>(C, at, v, 1);
-    else mx4_store<SGEMM_DTYPE_F32, 1>(C, at, v, 1);
+    store_values_as<1>(dtype, C, at, v, 1);
 }
 
-// 16 bytes of a row from byte k on; zeros from byte kn on, and no byte past it is read. A row of 16
-// bytes and more is read at its last 16, which are moved into place.
 __device__ inline i32x4 mx4_load_tail(const uint8_t *row, int k, int kn)
 {
-    unsigned __int128 v = 0;
-    if (k < kn) {
-        if (kn >= 16) {
-            const int at = min(k, kn - 16);
-            const Pack<int, 4> w = load_pack<int, 4>(reinterpret_cast<const int *>(row + at));
-            v = __builtin_bit_cast(unsigned __int128, w) >> (8 * (k - at));
-        } else {
-            for (int e = kn - 1; e >= k; --e) v = v << 8 | row[e];
-        }
-    }
-    return __builtin_bit_cast(i32x4, v);
+    return load_tail(reinterpret_cast<const int8_t *>(row), k, kn);
 }
 __device__ inline i32x4 mx4_load16(const uint8_t *p)
 {
@@ -216,6 +187,21 @@ __global__ __launch_bounds__(256) void k_mx4_join(Mx4Args p)
         float sum = 0.0f;
         for (int s = 0; s < p.splits; ++s) sum += p.partial[s * total + e];
         mx4_store_one(p.c_dtype, p.C, m * p.ldc + n, p.bias ? sum + p.bias[n] : sum);
+    }
+}
+
+// Rows put in place first: of A, B and their scales, one array after another.
+struct Mx4Copies {
+    Rows16 rows[4];
+    int bytes[4];
+};
+__global__ __launch_bounds__(256) void k_mx4_align(Mx4Copies p)
+{
+    int block = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (block >= 0 && block < p.rows[i].blocks) put_rows_in_place(p.rows[i], block, p.bytes[i]);
+        block -= p.rows[i].blocks;
     }
 }
 

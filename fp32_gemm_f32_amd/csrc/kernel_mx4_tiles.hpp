@@ -1,0 +1,330 @@
+// kernel_mx4_tiles.hpp -- the product of microscaled 4-bit operands (gemm_mx4.h) by tiles, on
+// v_mfma_scale_f32_32x32x64_f8f6f4.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "byte_tiles.hpp"
+#include "kernel_mx4.hpp"
+
+namespace sgemm {
+
+// One workgroup computes a BM x BN tile with WGM x WGN waves, panel by panel of BK = 128 bytes (256
+// elements) of K. Operand bytes move as the 8-bit product's do: straight to LDS, 16 bytes a lane, chunk
+// q of row r at chunk position q ^ a_swizzle(r), and a lane's CB column blocks are neighbours in C.
+//  * MFMA operands: lane l supplies row l % 32 and one block of 32 values with its scale. Step t of a
+//    panel takes block t + 4 (l / 32) on both sides, so that the four scales a lane needs for a panel
+//    are one word, of which step t takes byte t. Accumulator register v of lane l is row
+//    8 (v / 4) + v % 4 + 4 (l / 32) and column l % 32 of the block.
+//  * Scales come 16 bytes to a row, two panels' worth, one load of 16 bytes a lane: loaded panel by
+//    panel (8 bytes to a row) they would touch as many lines twice as often. They ride ahead of the
+//    loads of an even panel, in a ring of their own: NSTG panels in a row touch at most (NSTG + 3) / 2
+//    of them, also where a tile of odd panels is followed by another.
+//  * Chunks past the tile's rows or past K read as zero through an offset out of range; a chunk that
+//    K ends in is cut in LDS, on A's side, by the thread that loaded it. Scales past K's blocks may
+//    be anything there and are masked: one that is no number would make zeros NaN.
+//  * Rows have to start on word boundaries, of elements and of scales; others are copied first.
+template <int BM_, int BN_, int WGM_, int WGN_, int NSTG_>
+struct Mx4Tile : ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> {
+    typedef ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> Base;
+    static constexpr int SROWS = (BM_ + BN_ + Base::NT - 1) / Base::NT * Base::NT;   // rows of scales, filled up
+    static constexpr int SCH = SROWS / Base::NT;     // a thread's chunks of scales
+    static constexpr int SBYTES = SROWS * 16, SRING = (NSTG_ + 3) / 2;
+    static constexpr int LDS = NSTG_ * Base::STAGE + SRING * SBYTES;
+    static constexpr bool LOOP = LDS > 80 * 1024;    // one workgroup to a compute unit: it goes on to another tile
+    static_assert(LDS <= 160 * 1024, "LDS");
+};
+
+template <typename T>
+__device__ __forceinline__ void mx4_epilogue(const Mx4Args &p, const f32x16 (&acc)[T::RB][T::CB],
+                                             const float (&bias)[T::CB], int m0, int n0, int split, int wm, int wn)
+{
+    const int frow = threadIdx.x & 31, fhi = (threadIdx.x & 63) >> 5;
+    const int col = n0 + wn * T::WN + T::CB * frow;
+    const int valid = p.N - col;
+    const int row0 = m0 + wm * T::WM + 4 * fhi;
+    if (valid <= 0) return;
+    if (p.splits > 1) {
+        float *out = p.partial + int64_t(split) * p.M * p.N;
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
+                if (m < p.M)
+#pragma unroll
+                    for (int j = 0; j < T::CB; ++j)
+                        if (j < valid) out[int64_t(m) * p.N + col + j] = acc[i][j][v];
+            }
+        return;
+    }
+    auto store_all = [&](auto dt, auto stream) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
+                float x[T::CB];
+#pragma unroll
+                for (int j = 0; j < T::CB; ++j) x[j] = acc[i][j][v] + bias[j];
+                if (m < p.M)
+                    store_values<decltype(dt)::value, T::CB, decltype(stream)::value>(p.C, m * p.ldc + col, x, valid);
+            }
+    };
+    auto store = [&](auto dt) __attribute__((always_inline)) {
+        if (p.stream) store_all(dt, std::true_type{});
+        else store_all(dt, std::false_type{});
+    };
+    if (p.c_dtype == SGEMM_DTYPE_BF16) store(std::integral_constant<int, SGEMM_DTYPE_BF16>{});
+    else if (p.c_dtype == SGEMM_DTYPE_F16) store(std::integral_constant<int, SGEMM_DTYPE_F16>{});
+    else store(std::integral_constant<int, SGEMM_DTYPE_F32>{});
+}
+
+// a + 2^.. a b with the scales' byte `T` on both sides
+template <int T> __device__ __forceinline__ f32x16 mx4_mfma(i32x4 a, i32x4 b, f32x16 c, int sa, int sb)
+{
+    const i32x8 ax = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+    const i32x8 bx = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(ax, bx, c, 4, 4, T, sa, T, sb);
+}
+
+template <typename T>
+__global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
+{
+    constexpr int STAGE = T::STAGE;
+    __shared__ __attribute__((aligned(16))) char smem[T::LDS];
+    char *const ring = smem + T::NSTG * STAGE;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / T::WGN, wn = wave % T::WGN;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int split = p.splits == 1 ? 0 : int(blockIdx.x) / tiles;
+    const int k0 = split * p.chunk, k1 = min(p.KB, k0 + p.chunk);
+    const int kn = k1 - k0, panels = (kn + T::BK - 1) / T::BK;
+    const int blocks = (kn + 15) / 16;               // scales to a row in this split
+    const bool ragged = kn % 16 != 0;
+
+    // the tile that loads go to: this thread's chunks, LDS chunk i * NT + tid, and rows of scales. Rows
+    // past the operand's last lie past its resource's end and read as zero; of a thread's rows one
+    // offset is held, the others lie at distances that are the same for all.
+    const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
+    const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
+    const uint32_t a_off = uint32_t(prow * p.lda) + q * 16, b_off = uint32_t(tile_b_row<T>(prow) * p.ldb) + q * 16;
+    int m0, n0;
+    const int8_t *At, *Bt, *St[T::SCH];
+    uint32_t a_size, b_size, s_size[T::SCH], s_off[T::SCH];
+    auto aim = [&](int tile) __attribute__((always_inline)) {
+        int tm, tn;
+        tile_of(p, tile, tm, tn);
+        m0 = tm * T::BM;
+        n0 = tn * T::BN;
+        At = reinterpret_cast<const int8_t *>(p.A) + m0 * p.lda + k0;
+        Bt = reinterpret_cast<const int8_t *>(p.B) + n0 * p.ldb + k0;
+        a_size = bytes_range(At, reinterpret_cast<const int8_t *>(p.A) + (p.M - 1) * p.lda + p.KB);
+        b_size = bytes_range(Bt, reinterpret_cast<const int8_t *>(p.B) + (p.N - 1) * p.ldb + p.KB);
+#pragma unroll
+        for (int i = 0; i < T::SCH; ++i) {
+            // rows of A, then of B as they lie in LDS (a wave's are all of one: BM is a multiple of 64)
+            const int s0 = i * T::NT + wave * 64, s = s0 + lane;
+            const bool of_a = s0 < T::BM;
+            const int64_t ld = of_a ? p.ldsa : p.ldsb;
+            const int8_t *const from = reinterpret_cast<const int8_t *>(of_a ? p.sa : p.sb);
+            St[i] = from + (of_a ? m0 : n0) * ld + k0 / 16;
+            s_size[i] = bytes_range(St[i], from + ((of_a ? p.M : p.N) - 1) * ld + (p.KB + 15) / 16);
+            s_off[i] = s >= T::BM + T::BN ? kOob : uint32_t((of_a ? s : tile_b_row<T>(s - T::BM)) * ld);
+        }
+    };
+    static_assert(T::BM % 64 == 0, "scales of whole waves");
+    static_assert(T::NT / T::CPR % 32 == 0 || T::NT / T::CPR == 16, "a thread's rows at common distances");
+    int tile = int(blockIdx.x) - split * tiles;
+    aim(tile);
+    float bias[T::CB];
+    auto load_bias = [&](int n) __attribute__((always_inline)) {
+        const int col = n + wn * T::WN + T::CB * (lane & 31);
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j) bias[j] = p.bias && p.splits == 1 ? p.bias[min(col + j, p.N - 1)] : 0.0f;
+    };
+    f32x16 acc[T::RB][T::CB];
+#pragma unroll
+    for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j) acc[i][j] = f32x16(0.0f);
+
+    // operand reads: row l % 32 of a block; chunk t + 4 (l / 32) at step t
+    const int frow = lane & 31, fhi = lane >> 5;
+    const int fsw = a_swizzle<T::CPR>(frow);
+    const int a_row = wm * T::WM + frow, b_row = wn * T::WN + frow;
+    const int a_base = a_row * T::BK, b_base = T::A_BYTES + b_row * T::BK;
+    i32x4 fa[T::STEPS][T::RB], fb[T::STEPS][T::CB];
+    uint32_t sa[2][T::RB], sb[2][T::CB];             // of the panel multiplied, and of the next
+    auto read = [&](const char *st, auto tc) __attribute__((always_inline)) {
+        constexpr int t = decltype(tc)::value;
+        const int at = ((t + T::STEPS * fhi) ^ fsw) * 16;
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+            fa[t][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j)
+            fb[t][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
+    };
+    // the scales of a panel (of this tile), from ring entry `entry`
+    auto read_scales = [&](int panel, int entry, uint32_t (&a)[T::RB], uint32_t (&b)[T::CB]) __attribute__((always_inline)) {
+        const char *at = ring + entry * T::SBYTES + 8 * (panel & 1) + 4 * fhi;
+        const int left = blocks - 8 * panel - 4 * fhi;
+        const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+            a[i] = *reinterpret_cast<const uint32_t *>(at + (a_row + 32 * i) * 16) & keep;
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j)
+            b[j] = *reinterpret_cast<const uint32_t *>(at + (T::BM + b_row + 32 * j) * 16) & keep;
+    };
+    auto multiply = [&](auto tc, const uint32_t (&a)[T::RB], const uint32_t (&b)[T::CB]) __attribute__((always_inline)) {
+        constexpr int t = decltype(tc)::value;
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+            for (int j = 0; j < T::CB; ++j)
+                acc[i][j] = mx4_mfma<t>(fa[t][i], fb[t][j], acc[i][j], int(a[i]), int(b[j]));
+    };
+
+    // what is left of a resource k bytes on (saturated sizes lose k bytes that no tile reaches: see kMaxLd)
+    // (in signed integers: a saturating difference of unsigned ones has no scalar form)
+    const auto rest = [](uint32_t size, int k) { return uint32_t(max(int(size) - k, 0)); };
+    int load_entry = 0;                              // the ring's entry that scales go to next
+    auto issue_scales = [&](int panel) __attribute__((always_inline)) {
+        char *to = ring + load_entry * T::SBYTES;
+        load_entry = load_entry + 1 == T::SRING ? 0 : load_entry + 1;
+        const int k = 8 * panel;
+        const uint32_t past = k >= blocks ? kOob : 0u;
+#pragma unroll
+        for (int i = 0; i < T::SCH; ++i)
+            load16_lds(St[i] + k, rest(s_size[i], k), s_off[i] | past, to + (i * T::NT + wave * 64) * 16);
+    };
+    auto issue = [&](int panel, char *st) __attribute__((always_inline)) {
+        const int k = panel * T::BK;
+        // in the split's last panel, and past it, chunks past its end read as zero
+        const uint32_t past = k + q * 16 >= kn ? kOob : 0u;
+#pragma unroll
+        for (int i = 0; i < T::ACH; ++i)
+            load16_lds(At + k, rest(a_size, k), (a_off | past) + uint32_t(i * (T::NT / T::CPR) * p.lda),
+                       st + (i * T::NT + wave * 64) * 16);
+#pragma unroll
+        for (int i = 0; i < T::BCH; ++i)
+            load16_lds(Bt + k, rest(b_size, k),
+                       (b_off | past) + uint32_t(tile_b_row<T>(i * (T::NT / T::CPR)) * p.ldb),
+                       st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
+    };
+    // cuts A's chunk that the rows end in, in the last panel, once this wave's loads of it have landed
+    auto cut = [&](int panel, char *st) __attribute__((always_inline)) {
+        const int left = kn - panel * T::BK - q * 16;
+        if (left > 0 && left < 16)
+#pragma unroll
+            for (int i = 0; i < T::ACH; ++i) {
+                i32x4 *c = reinterpret_cast<i32x4 *>(st + (i * T::NT + tid) * 16);
+                *c = keep_bytes(*c, left);
+            }
+    };
+    // LOOK steps before a panel's end the reads of its stage are over, so the barrier comes there: the
+    // wave's loads of the next panel have landed, every wave's have after the barrier, and the stage
+    // just read is loaded again and the next one's first operands are read under the last steps'
+    // MFMAs. (Loads still under way then: those of NSTG - 2 panels, and of the scales ahead of half
+    // of them, rounded down.)
+    constexpr int LPP = T::ACH + T::BCH, LOOK = 1;
+    constexpr int UNDER_WAY = (T::NSTG - 2) * LPP + (T::NSTG - 2) / 2 * T::SCH;
+    if constexpr (!T::LOOP) load_bias(n0);
+#pragma unroll
+    for (int i = 0; i < T::NSTG; ++i) {
+        if (i % 2 == 0) issue_scales(i);
+        issue(i, smem + i * STAGE);
+    }
+    wait_vmcnt<(T::NSTG - 1) * LPP + (T::NSTG - 1) / 2 * T::SCH>();
+    if (ragged && panels == 1) cut(0, smem);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    int entry = 0;                                   // the ring's entry of the panel read last
+    read_scales(0, 0, sa[0], sb[0]);
+    static_for<0, LOOK>([&](auto tc) __attribute__((always_inline)) { read(smem, tc); });
+    int stage = 0;
+    int behind = 0;                                  // panels between a panel read and that of its tile
+    auto run = [&](int panel) __attribute__((always_inline)) {
+        char *st = smem + stage * STAGE;
+        stage = stage + 1 == T::NSTG ? 0 : stage + 1;
+        char *next = smem + stage * STAGE;
+        static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
+            constexpr int t = decltype(tc)::value;
+            constexpr bool turn = t == T::STEPS - LOOK;
+            if constexpr (turn) {
+                __builtin_amdgcn_sched_barrier(0);
+                wait_vmcnt<UNDER_WAY>();
+                if (ragged && panel == panels - 2) cut(panel + 1, next);
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                if ((panel + T::NSTG - behind) % 2 == 0) issue_scales(panel + T::NSTG - behind);
+            }
+            if constexpr (t + LOOK < T::STEPS) read(st, std::integral_constant<int, t + LOOK>{});
+            else read(next, std::integral_constant<int, t + LOOK - T::STEPS>{});
+            if constexpr (turn) {
+                const int coming = panel + 1 == panels ? 0 : panel + 1;      // (0: the next tile's)
+                if (coming % 2 == 0) entry = entry + 1 == T::SRING ? 0 : entry + 1;
+                read_scales(coming, entry, sa[1], sb[1]);
+                issue(panel + T::NSTG - behind, st);
+            }
+            multiply(tc, sa[0], sb[0]);
+            // operand reads behind the first MFMAs, the loads behind the others
+            constexpr int ops = T::RB + T::CB + (turn ? T::RB + T::CB : 0);
+            constexpr int loads = LPP;
+            constexpr int mf = T::RB * T::CB;
+            constexpr int rm = turn ? (mf + 1) / 2 : (ops < mf ? ops : mf);
+            constexpr int lm = mf - rm > 0 ? mf - rm : 1;
+            static_for<0, mf>([&](auto mc) __attribute__((always_inline)) {
+                constexpr int m = decltype(mc)::value;
+                constexpr int r = m < rm ? (m + 1) * ops / rm - m * ops / rm : 0;
+                constexpr int n = m - (mf - lm);
+                constexpr int l = turn && n >= 0 ? (n + 1) * loads / lm - n * loads / lm : 0;
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, r, 0);
+                if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
+            });
+        });
+#pragma unroll
+        for (int i = 0; i < T::RB; ++i) sa[0][i] = sa[1][i];
+#pragma unroll
+        for (int j = 0; j < T::CB; ++j) sb[0][j] = sb[1][j];
+    };
+    if constexpr (!T::LOOP) {
+        for (int panel = 0; panel < panels; ++panel) run(panel);
+        wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
+        mx4_epilogue<T>(p, acc, bias, m0, n0, split, wm, wn);
+    } else {
+        // The last NSTG panels of a tile load the first of the next, so that its stores and the start
+        // of the next run under each other (the grid has fewer workgroups than tiles only where K
+        // has NSTG panels).
+        for (;;) {
+            const int cm0 = m0, cn0 = n0;
+            tile += int(gridDim.x);
+            const bool more = p.splits == 1 && tile < tiles;
+            int panel = 0;
+            for (int part = 0; part < 2; ++part) {
+                const int end = part == 0 ? panels - T::NSTG : panels;
+                for (; panel < end; ++panel) run(panel);
+                if (part == 0 && more) {
+                    aim(tile);
+                    behind = panels;
+                }
+            }
+            if (!more) wait_vmcnt<0>();
+            load_bias(cn0);
+            mx4_epilogue<T>(p, acc, bias, cm0, cn0, split, wm, wn);
+            if (!more) break;
+            behind = 0;
+#pragma unroll
+            for (int i = 0; i < T::RB; ++i)
+#pragma unroll
+                for (int j = 0; j < T::CB; ++j) acc[i][j] = f32x16(0.0f);
+        }
+    }
+}
+
+}  // namespace sgemm
