@@ -75,21 +75,26 @@ constexpr Mx4Variant tile(const char *name, double c1, double c2, double ends, d
 const Mx4Variant kTiles[] = {
     tile<64, 32, 2, 1, 6>("mx4_64x32", 0.189, 0.27, 2.31, 0.0),
     tile<64, 64, 2, 2, 4>("mx4_64x64", 0.200, 0.37, 1.84, 0.0),
-    tile<64, 128, 2, 4, 3>("mx4_64x128", 0.298, 0.52, 2.17, 0.0),
+    tile<64, 128, 2, 4, 2>("mx4_64x128", 0.298, 0.52, 2.17, 0.0),
     tile<128, 128, 4, 2, 2>("mx4_128x128", 0.506, 0.95, 1.19, 0.0),
     tile<128, 128, 4, 2, 4>("mx4_128x128_s4", 0.408, 0.0, 2.04, 3.76),
     tile<128, 256, 2, 4, 2>("mx4_128x256", 0.644, 0.0, 2.83, 7.49),
     tile<192, 256, 2, 4, 2>("mx4_192x256", 0.962, 0.0, 3.46, 8.19),
     tile<256, 256, 4, 2, 2>("mx4_256x256", 1.125, 0.0, 2.20, 7.80),
+    tile<256, 256, 2, 2, 2>("mx4_256x256_w4", 9.125, 0.0, 2.20, 7.80),
 };
 // Few rows: 16 rows and columns, turns of 512 elements to a wave.
 const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0};
 
-// The operands, and which of them can be loaded as they lie: rows on word boundaries.
+// The operands, and which of them the tiles can load as they lie: rows on word boundaries, A's of
+// whole chunks.
 struct Mx4Operands {
     const uint8_t *p[4];      // A, B, and their scales
     int64_t ld[4];
-    bool ready(int i) const { return ld[i] % 4 == 0 && reinterpret_cast<uintptr_t>(p[i]) % 4 == 0; }
+    bool ready(int i, int K) const
+    {
+        return ld[i] % 4 == 0 && reinterpret_cast<uintptr_t>(p[i]) % 4 == 0 && (i > 0 || K % 32 == 0);
+    }
 };
 
 struct Mx4Plan {
@@ -151,7 +156,7 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
     bool copy[4];
     double copied = 0.0;
     for (int i = 0; i < 4; ++i) {
-        copy[i] = !x.ready(i);
+        copy[i] = !x.ready(i, K);
         if (copy[i]) copied += double(i % 2 == 0 ? M : N) * K / (i < 2 ? 2 : 32);
     }
     for (const Mx4Variant &v : kTiles) {

@@ -19,23 +19,26 @@ namespace sgemm {
 //    panel takes block t + 4 (l / 32) on both sides, so that the four scales a lane needs for a panel
 //    are one word, of which step t takes byte t. Accumulator register v of lane l is row
 //    8 (v / 4) + v % 4 + 4 (l / 32) and column l % 32 of the block.
-//  * Scales come 16 bytes to a row, two panels' worth, one load of 16 bytes a lane: loaded panel by
-//    panel (8 bytes to a row) they would touch as many lines twice as often. They ride ahead of the
-//    loads of an even panel, in a ring of their own: NSTG panels in a row touch at most (NSTG + 3) / 2
-//    of them, also where a tile of odd panels is followed by another.
-//  * Chunks past the tile's rows or past K read as zero through an offset out of range; a chunk that
-//    K ends in is cut in LDS, on A's side, by the thread that loaded it. Scales past K's blocks may
-//    be anything there and are masked: one that is no number would make zeros NaN.
+//  * Panels go in pairs, for their scales come 16 bytes to a row, one load of 16 bytes a lane, ahead of
+//    the loads of an even panel, into a ring of their own. A word of each of 32 rows 16 bytes apart
+//    would hit 8 banks; so a lane reads all 16 bytes of a row, lanes below 32 of one block of rows and
+//    the others of the next, and one exchange between the halves (v_permlane32_swap) gives both
+//    blocks a panel's words.
+//  * Chunks past the tile's rows or past K read as zero through an offset out of range. Scales behind
+//    the last block may be anything and are masked: one that is no number would make zeros NaN. K
+//    ends on whole chunks on A's side (B's bytes behind K meet zeros): other A are copied first.
+//  * The loop has no branch: with one, the compiler moves the MFMAs of all steps behind it.
 //  * Rows have to start on word boundaries, of elements and of scales; others are copied first.
 template <int BM_, int BN_, int WGM_, int WGN_, int NSTG_>
 struct Mx4Tile : ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> {
     typedef ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> Base;
     static constexpr int SROWS = (BM_ + BN_ + Base::NT - 1) / Base::NT * Base::NT;   // rows of scales, filled up
     static constexpr int SCH = SROWS / Base::NT;     // a thread's chunks of scales
-    static constexpr int SBYTES = SROWS * 16, SRING = (NSTG_ + 3) / 2;
+    static constexpr int SBYTES = SROWS * 16, SRING = NSTG_ / 2;
     static constexpr int LDS = NSTG_ * Base::STAGE + SRING * SBYTES;
     static constexpr bool LOOP = LDS > 80 * 1024;    // one workgroup to a compute unit: it goes on to another tile
     static_assert(LDS <= 160 * 1024, "LDS");
+    static_assert(NSTG_ % 2 == 0, "panels go in pairs");
 };
 
 template <typename T>
@@ -103,9 +106,10 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     const int tiles = p.tiles_m * p.tiles_n;
     const int split = p.splits == 1 ? 0 : int(blockIdx.x) / tiles;
     const int k0 = split * p.chunk, k1 = min(p.KB, k0 + p.chunk);
-    const int kn = k1 - k0, panels = (kn + T::BK - 1) / T::BK;
+    const int kn = k1 - k0;
+    // (an odd number is filled up where the next tile's panels follow)
+    const int panels = ((kn + T::BK - 1) / T::BK + (T::LOOP ? 1 : 0)) & (T::LOOP ? ~1 : ~0);
     const int blocks = (kn + 15) / 16;               // scales to a row in this split
-    const bool ragged = kn % 16 != 0;
 
     // the tile that loads go to: this thread's chunks, LDS chunk i * NT + tid, and rows of scales. Rows
     // past the operand's last lie past its resource's end and read as zero; of a thread's rows one
@@ -159,7 +163,18 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     const int a_row = wm * T::WM + frow, b_row = wn * T::WN + frow;
     const int a_base = a_row * T::BK, b_base = T::A_BYTES + b_row * T::BK;
     i32x4 fa[T::STEPS][T::RB], fb[T::STEPS][T::CB];
-    uint32_t sa[2][T::RB], sb[2][T::CB];             // of the panel multiplied, and of the next
+    // scales: blocks of rows of A, then of B, in pairs; words of the two halves of two panels
+    constexpr int BLOCKS = T::RB + T::CB, PAIRS = (BLOCKS + 1) / 2;
+    i32x4 pair[PAIRS];
+    uint32_t sc[2 * PAIRS];                          // of the panel multiplied
+    int s_at[PAIRS];
+#pragma unroll
+    for (int n = 0; n < PAIRS; ++n) {
+        const auto row_of = [&](int block) {
+            return block < T::RB ? wm * T::WM + 32 * block : T::BM + wn * T::WN + 32 * (block - T::RB);
+        };
+        s_at[n] = ((fhi ? row_of(min(2 * n + 1, BLOCKS - 1)) : row_of(2 * n)) + frow) * 16;
+    }
     auto read = [&](const char *st, auto tc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value;
         const int at = ((t + T::STEPS * fhi) ^ fsw) * 16;
@@ -170,25 +185,30 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
         for (int j = 0; j < T::CB; ++j)
             fb[t][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
     };
-    // the scales of a panel (of this tile), from ring entry `entry`
-    auto read_scales = [&](int panel, int entry, uint32_t (&a)[T::RB], uint32_t (&b)[T::CB]) __attribute__((always_inline)) {
-        const char *at = ring + entry * T::SBYTES + 8 * (panel & 1) + 4 * fhi;
-        const int left = blocks - 8 * panel - 4 * fhi;
-        const uint32_t keep = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << 8 * left) - 1;
+    auto read_scales = [&](int entry) __attribute__((always_inline)) {
+        const char *at = ring + entry * T::SBYTES;
 #pragma unroll
-        for (int i = 0; i < T::RB; ++i)
-            a[i] = *reinterpret_cast<const uint32_t *>(at + (a_row + 32 * i) * 16) & keep;
-#pragma unroll
-        for (int j = 0; j < T::CB; ++j)
-            b[j] = *reinterpret_cast<const uint32_t *>(at + (T::BM + b_row + 32 * j) * 16) & keep;
+        for (int n = 0; n < PAIRS; ++n) pair[n] = *reinterpret_cast<const i32x4 *>(at + s_at[n]);
     };
-    auto multiply = [&](auto tc, const uint32_t (&a)[T::RB], const uint32_t (&b)[T::CB]) __attribute__((always_inline)) {
+    // the words of a panel, the even or odd one of the pair read last
+    auto take_scales = [&](int panel, auto odd) __attribute__((always_inline)) {
+        constexpr int w = decltype(odd)::value ? 2 : 0;
+        const int left = blocks - 8 * panel - 4 * fhi;
+        const uint32_t keep = left <= 0 ? 0u : ~0u >> (32 - 8 * min(left, 4));
+#pragma unroll
+        for (int n = 0; n < PAIRS; ++n) {
+            const auto both = __builtin_amdgcn_permlane32_swap(uint32_t(pair[n][w]), uint32_t(pair[n][w + 1]), false, false);
+            sc[2 * n] = both[0] & keep;
+            sc[2 * n + 1] = both[1] & keep;
+        }
+    };
+    auto multiply = [&](auto tc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value;
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
 #pragma unroll
             for (int j = 0; j < T::CB; ++j)
-                acc[i][j] = mx4_mfma<t>(fa[t][i], fb[t][j], acc[i][j], int(a[i]), int(b[j]));
+                acc[i][j] = mx4_mfma<t>(fa[t][i], fb[t][j], acc[i][j], int(sc[i]), int(sc[T::RB + j]));
     };
 
     // what is left of a resource k bytes on (saturated sizes lose k bytes that no tile reaches: see kMaxLd)
@@ -218,21 +238,10 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
                        (b_off | past) + uint32_t(tile_b_row<T>(i * (T::NT / T::CPR)) * p.ldb),
                        st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
     };
-    // cuts A's chunk that the rows end in, in the last panel, once this wave's loads of it have landed
-    auto cut = [&](int panel, char *st) __attribute__((always_inline)) {
-        const int left = kn - panel * T::BK - q * 16;
-        if (left > 0 && left < 16)
-#pragma unroll
-            for (int i = 0; i < T::ACH; ++i) {
-                i32x4 *c = reinterpret_cast<i32x4 *>(st + (i * T::NT + tid) * 16);
-                *c = keep_bytes(*c, left);
-            }
-    };
     // LOOK steps before a panel's end the reads of its stage are over, so the barrier comes there: the
     // wave's loads of the next panel have landed, every wave's have after the barrier, and the stage
     // just read is loaded again and the next one's first operands are read under the last steps'
-    // MFMAs. (Loads still under way then: those of NSTG - 2 panels, and of the scales ahead of half
-    // of them, rounded down.)
+    // MFMAs. (Loads still under way then: those of NSTG - 2 panels, with the scales of half of them.)
     constexpr int LPP = T::ACH + T::BCH, LOOK = 1;
     constexpr int UNDER_WAY = (T::NSTG - 2) * LPP + (T::NSTG - 2) / 2 * T::SCH;
     if constexpr (!T::LOOP) load_bias(n0);
@@ -241,40 +250,44 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
         if (i % 2 == 0) issue_scales(i);
         issue(i, smem + i * STAGE);
     }
-    wait_vmcnt<(T::NSTG - 1) * LPP + (T::NSTG - 1) / 2 * T::SCH>();
-    if (ragged && panels == 1) cut(0, smem);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    int entry = 0;                                   // the ring's entry of the panel read last
-    read_scales(0, 0, sa[0], sb[0]);
+    wait_vmcnt<(T::NSTG - 1) * LPP + (T::NSTG / 2 - 1) * T::SCH>();
+    asm volatile("s_barrier" ::: "memory");
+    typedef std::integral_constant<bool, false> Even;
+    typedef std::integral_constant<bool, true> Odd;
+    int entry = 0;                                   // the ring's entry of the pair read last
+    read_scales(0);
+    take_scales(0, Even{});
     static_for<0, LOOK>([&](auto tc) __attribute__((always_inline)) { read(smem, tc); });
-    int stage = 0;
+    int stage = 0;                                   // of the pair
     int behind = 0;                                  // panels between a panel read and that of its tile
-    auto run = [&](int panel) __attribute__((always_inline)) {
-        char *st = smem + stage * STAGE;
-        stage = stage + 1 == T::NSTG ? 0 : stage + 1;
-        char *next = smem + stage * STAGE;
+    auto run = [&](int panel, auto odd) __attribute__((always_inline)) {
+        constexpr bool ODD = decltype(odd)::value;
+        char *st = smem + (stage + (ODD ? 1 : 0)) * STAGE;
+        if constexpr (ODD) stage = stage + 2 == T::NSTG ? 0 : stage + 2;
+        char *next = ODD ? smem + stage * STAGE : st + STAGE;
         static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
             constexpr int t = decltype(tc)::value;
             constexpr bool turn = t == T::STEPS - LOOK;
             if constexpr (turn) {
                 __builtin_amdgcn_sched_barrier(0);
                 wait_vmcnt<UNDER_WAY>();
-                if (ragged && panel == panels - 2) cut(panel + 1, next);
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                if ((panel + T::NSTG - behind) % 2 == 0) issue_scales(panel + T::NSTG - behind);
             }
             if constexpr (t + LOOK < T::STEPS) read(st, std::integral_constant<int, t + LOOK>{});
             else read(next, std::integral_constant<int, t + LOOK - T::STEPS>{});
             if constexpr (turn) {
-                const int coming = panel + 1 == panels ? 0 : panel + 1;      // (0: the next tile's)
-                if (coming % 2 == 0) entry = entry + 1 == T::SRING ? 0 : entry + 1;
-                read_scales(coming, entry, sa[1], sb[1]);
+                if constexpr (ODD) {
+                    entry = entry + 1 == T::SRING ? 0 : entry + 1;    
+                    read_scales(entry);
+                } else {
+                    issue_scales(panel + T::NSTG - behind);
+                }
                 issue(panel + T::NSTG - behind, st);
             }
-            multiply(tc, sa[0], sb[0]);
+            multiply(tc);
             // operand reads behind the first MFMAs, the loads behind the others
-            constexpr int ops = T::RB + T::CB + (turn ? T::RB + T::CB : 0);
-            constexpr int loads = LPP;
+            constexpr int ops = T::RB + T::CB + (turn && ODD ? PAIRS : 0);
+            constexpr int loads = LPP + (ODD ? 0 : T::SCH);
             constexpr int mf = T::RB * T::CB;
             constexpr int rm = turn ? (mf + 1) / 2 : (ops < mf ? ops : mf);
             constexpr int lm = mf - rm > 0 ? mf - rm : 1;
@@ -288,13 +301,17 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
                 if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
             });
         });
-#pragma unroll
-        for (int i = 0; i < T::RB; ++i) sa[0][i] = sa[1][i];
-#pragma unroll
-        for (int j = 0; j < T::CB; ++j) sb[0][j] = sb[1][j];
+        // (behind a tile's last panel comes the first of the next: its scales are whole or masked alike)
+        if constexpr (ODD) take_scales(panel + 1 == panels ? 0 : panel + 1, Even{});
+        else take_scales(panel + 1, Odd{});
     };
     if constexpr (!T::LOOP) {
-        for (int panel = 0; panel < panels; ++panel) run(panel);
+        int panel = 0;
+        for (; panel + 1 < panels; panel += 2) {
+            run(panel, Even{});
+            run(panel + 1, Odd{});
+        }
+        if (panel < panels) run(panel, Even{});
         wait_vmcnt<0>();   // no load is in flight to LDS when the workgroup ends
         mx4_epilogue<T>(p, acc, bias, m0, n0, split, wm, wn);
     } else {
@@ -308,7 +325,10 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
             int panel = 0;
             for (int part = 0; part < 2; ++part) {
                 const int end = part == 0 ? panels - T::NSTG : panels;
-                for (; panel < end; ++panel) run(panel);
+                for (; panel < end; panel += 2) {
+                    run(panel, Even{});
+                    run(panel + 1, Odd{});
+                }
                 if (part == 0 && more) {
                     aim(tile);
                     behind = panels;
