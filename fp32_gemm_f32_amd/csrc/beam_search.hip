@@ -21,13 +21,15 @@ struct BeamSplit {
 };
 
 // Long rows are split over workgroups where there are fewer rows than compute units, into parts of
-// at least kLeastPart elements. A second kernel joins the parts either way.
-constexpr int kLeastPart = 4096;
+// about kPart elements (4 rows of 131072 f32 into 8, 16 and 24 parts: 11.3, 10.6, 11.0 us with the second
+// kernel, which joins the parts either way; 32 rows of 32001 bf16 into 2, 4 and 8: 10.1, 10.0, 9.7; 185
+// rows of 50001 f16 into 2, 4 and 8: 14.1, 12.8, 13.9).
+constexpr int kPart = 8192;
 BeamSplit split_beams(int64_t rows, int V, int top, int cus)
 {
     BeamSplit r{1, V, 0};
-    if (rows < cus && V >= 2 * kLeastPart) {
-        const int want = int(std::min<int64_t>(ceil_div(2 * cus, rows), V / kLeastPart));
+    if (rows < cus && V >= 2 * kPart) {
+        const int want = int(std::min<int64_t>(ceil_div(3 * cus, rows), ceil_div(V, kPart)));
         r.part_len = int((ceil_div(V, want) + 7) / 8 * 8);
         r.splits = int(ceil_div(V, r.part_len));
     }
@@ -41,15 +43,17 @@ struct BeamLaunch {
     BeamKernel kernel;
     int threads;
 };
-// As the token log-probabilities' pass: more threads for fewer and longer rows; logits of half the
-// last-level cache and more are read past it.
+// Longer parts take more threads (1024 rows of 131072 bf16 with 512 and 1024: 60.2 and 56.2 us; 512 rows of
+// 32001 with 256, 512 and 1024: 16.6, 15.6, 17.2). Logits of half the last-level cache and more are
+// read past it (the former with 512 threads in two parts: 57.0 instead of 61.5).
 constexpr int64_t kStreamBytes = int64_t(128) << 20;
-template <int DT> BeamLaunch beam_pass(int64_t groups, int len, int cus, bool stream)
+template <int DT> BeamLaunch beam_pass(int len, bool stream)
 {
-    if (groups <= cus && len >= 32768) return {&k_beam_pass<DT, 1024, 4, false>, 1024};
-    if (groups <= 4 * cus && len >= 8192)
-        return {stream ? &k_beam_pass<DT, 512, 4, true> : &k_beam_pass<DT, 512, 4, false>, 512};
-    return {stream ? &k_beam_pass<DT, 256, 4, true> : &k_beam_pass<DT, 256, 4, false>, 256};
+    if (len >= 65536)
+        return {stream ? &k_beam_pass<DT, 1024, 2, true> : &k_beam_pass<DT, 1024, 2, false>, 1024};
+    if (len >= 2 * kPart)
+        return {stream ? &k_beam_pass<DT, 512, 2, true> : &k_beam_pass<DT, 512, 2, false>, 512};
+    return {stream ? &k_beam_pass<DT, 256, 2, true> : &k_beam_pass<DT, 256, 2, false>, 256};
 }
 
 // Whether a state's pieces overlap (or lie in each other, in an order that is not looked into).
@@ -137,12 +141,12 @@ extern "C" int beam_step(int B, int W, int V, const void *logits, int dtype, int
     p.ld = ld; p.pad_token = pad_token;
     p.part_bytes = r.part_bytes;
     p.W = W; p.V = V; p.top = top; p.splits = r.splits; p.part_len = r.part_len;
+    p.by_top = divisor(uint32_t(top)); p.by_splits = divisor(uint32_t(r.splits));
     const bool past_caches = rows * V * size >= kStreamBytes;
-    const int64_t groups = rows * r.splits;
     const BeamLaunch pass =
-        dtype == SGEMM_DTYPE_F32    ? beam_pass<SGEMM_DTYPE_F32>(groups, r.part_len, cus, past_caches)
-        : dtype == SGEMM_DTYPE_BF16 ? beam_pass<SGEMM_DTYPE_BF16>(groups, r.part_len, cus, past_caches)
-                                    : beam_pass<SGEMM_DTYPE_F16>(groups, r.part_len, cus, past_caches);
+        dtype == SGEMM_DTYPE_F32    ? beam_pass<SGEMM_DTYPE_F32>(r.part_len, past_caches)
+        : dtype == SGEMM_DTYPE_BF16 ? beam_pass<SGEMM_DTYPE_BF16>(r.part_len, past_caches)
+                                    : beam_pass<SGEMM_DTYPE_F16>(r.part_len, past_caches);
     // requests to a launch (rows that are split are fewer than the compute units: one turn)
     const int64_t most = most_groups(pass.threads) / r.splits / W;
     for (int64_t b = 0; b < B; b += most) {
@@ -252,6 +256,9 @@ extern "C" int reorder_beams(int B, int W, const void *beams, int beam_bytes, co
             a.chunks = int(ceil_div(s.run, 16));
             a.columns = int(s.count1 * s.count2 * a.chunks);
             a.blocks = int(ceil_div(a.columns, kReorderThreads));
+            a.by_blocks = divisor(uint32_t(a.blocks));
+            a.by_chunks = divisor(uint32_t(a.chunks));
+            a.by_count2 = divisor(uint32_t(a.count2));
             if (p.count == kStates || groups + n * a.blocks > most) {
                 const int st = flush();
                 if (st != SGEMM_OK) return st;

@@ -197,19 +197,6 @@ bool shape_in_limits(int M, int N, int K, int64_t lda, int64_t ldb)
     return K <= kMaxK && lda < kMaxLd && ldb < kMaxLd && tiles < (int64_t(1) << 30);
 }
 
-// t / d == mulhi(t, mul) >> shift for t < 2^31 and 2^shift < d <= 2^(shift + 1): mul = 2^(32 + shift) / d
-// rounded up is too large by less than 1, which adds less than t / 2^(32 + shift) < 1 / d to t / d.
-struct Divisor {
-    uint32_t mul;
-    int shift;
-};
-Divisor divisor(uint32_t d)
-{
-    int shift = 0;
-    while ((uint64_t(2) << shift) < d) ++shift;
-    return {uint32_t(((uint64_t(1) << (32 + shift)) + d - 1) / d), shift};
-}
-
 unsigned element_blocks(int64_t total)
 {
     return unsigned(std::min<int64_t>((total + 255) / 256, 16384));

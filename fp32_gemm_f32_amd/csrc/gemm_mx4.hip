@@ -21,15 +21,6 @@ constexpr int kWaves = 8;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// t / d == mulhi(t, mul) >> shift for t < 2^31 and 2^shift < d <= 2^(shift + 1): mul = 2^(32 + shift) / d
-// rounded up is too large by less than 1, which adds less than t / 2^(32 + shift) < 1 / d to t / d.
-Mx4Divisor divisor(uint32_t d)
-{
-    int shift = 0;
-    while ((uint64_t(2) << shift) < d) ++shift;
-    return {uint32_t(((uint64_t(1) << (32 + shift)) + d - 1) / d), shift};
-}
-
 unsigned element_blocks(int64_t total) { return unsigned(std::min<int64_t>((total + 255) / 256, 16384)); }
 
 // Rows in parts whose units one launch holds (and a division takes).
@@ -335,7 +326,7 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
             p.bias = bias ? bias + n : nullptr;
             p.C = static_cast<char *>(C) + (m * ldc + n) * csize;
             p.stream = reinterpret_cast<uintptr_t>(p.C) % 64 == 0 && ldc * csize % 64 == 0;
-            const Mx4Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
+            const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
             p.group_mul = d.mul; p.group_shift = d.shift;
             int64_t groups = int64_t(p.tiles_m) * p.tiles_n * plan.splits;
             if (loops) groups = std::min<int64_t>(groups, cus);

@@ -10,6 +10,7 @@
 
 #include "beam_search.h"
 #include "kernel_logprobs.hpp"
+#include "kernel_mfma.hpp"
 #include "ops_common.hpp"
 
 namespace sgemm {
@@ -25,29 +26,48 @@ struct BeamArgs {
     char *parts;               // part s of row i at (i * splits + s) * part_bytes
     int64_t part_bytes;
     int W, V, top, splits, part_len;
+    Divisor by_top, by_splits;
 };
 
 // ------------------------------------------------------------------ a beam's row --------
-// Running peak m and s = sum 2^((x - m) log2 e). log2 e is taken in two parts: its rounding to FP32
-// alone would move log s by up to 1e-7 for flat rows, and which of two beams' tokens comes first hangs
-// on such differences. (The sum's other errors are random in sign and average out: 2e-8.)
-constexpr float kLog2eLow = 1.925963033500011e-8f;
+// Running peak m and s = sum 2^(x L - c), L = log2 e as FP32 has it and c = m L: one multiply-add and one
+// exponential to an element. What FP32 rounds off here is either known (c is taken as it was rounded: see
+// beam_reference), random in sign from term to term (it averages out: 2e-8 of log s), or, as L is off
+// by 1.3e-8 of itself, that much of the row's entropy, nearly the same for all of a request's beams.
+// Which of two beams' tokens comes first hangs on such differences. Beyond kFar m L may overflow
+// (a mask of FP32's lowest value): there 2^((x - m) L), with a subtraction more.
+constexpr float kFar = 1e30f;
+constexpr double kNats = 1.0 / double(kLog2e);         // of a base-2 logarithm by L
 struct BeamStats {
     float m = kLowest, s = 0.0f;
 
-    __device__ static float power(float t)             // e^t, t <= 0
-    {
-        return __builtin_amdgcn_exp2f(__builtin_fmaf(t, kLog2e, t * kLog2eLow));
-    }
+    __device__ bool far() const { return !(__builtin_fabsf(m) <= kFar); }
     __device__ void raise(float to)
     {
         const float next = __builtin_fmaxf(m, to);
-        s *= power(__builtin_fmaxf(m - next, -1000.0f));
+        const float near = m * kLog2e - next * kLog2e, away = (m - next) * kLog2e;
+        const bool both = __builtin_fabsf(m) <= kFar && __builtin_fabsf(next) <= kFar;
+        s *= __builtin_amdgcn_exp2f(__builtin_fmaxf(both ? near : away, -1000.0f));
         m = next;
     }
-    // x with m already raised to it
-    __device__ void add(float x) { s += power(x - m); }
+    // n elements with m already raised to them
+    template <int N> __device__ void add(const float (&x)[N])
+    {
+        if (far()) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) s += __builtin_amdgcn_exp2f((x[j] - m) * kLog2e);
+        } else {
+            const float c = m * kLog2e;
+#pragma unroll
+            for (int j = 0; j < N; ++j) s += __builtin_amdgcn_exp2f(__builtin_fmaf(x[j], kLog2e, -c));
+        }
+    }
 };
+// What a sum's terms are taken over, in base 2: c, or where it is far m L without rounding.
+__device__ inline double beam_reference(float m)
+{
+    return __builtin_fabsf(m) <= kFar ? double(m * kLog2e) : double(m) * double(kLog2e);
+}
 
 // Every thread gets the workgroup's joined sums, in the same order each time.
 template <int NT> __device__ inline BeamStats join_beam_stats(StatsShared<NT> &sh, BeamStats st)
@@ -76,7 +96,7 @@ template <int NT> __device__ inline BeamStats join_beam_stats(StatsShared<NT> &s
 // out. A thread's elements: up to one of the head before the first 16-byte boundary, the chunks tid,
 // tid + NT, ... of 16 bytes, up to one of the tail.
 template <int DT, int NT, int U, bool STREAM>
-__global__ __launch_bounds__(NT) void k_beam_pass(BeamArgs p)
+__global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
 {
     typedef typename Elem<DT>::type T;
     constexpr int W = 16 / sizeof(T);
@@ -111,14 +131,15 @@ __global__ __launch_bounds__(NT) void k_beam_pass(BeamArgs p)
         v = Elem<DT>::widen(x[at]);
         note(v, at);
         st.raise(v);
-        st.add(v);
+        const float one[1] = {v};
+        st.add(one);
     };
     auto load = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
             b[u] = load_chunk_of<STREAM, T, W>(body + int64_t(min(c + u * NT, chunks - 1)) * W);
     };
-    auto widen = [&](float (&v)[W], int u, int c) __attribute__((always_inline)) {
+    auto widen = [&](float *v, int u, int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < W; ++j) v[j] = Elem<DT>::widen(b[u].v[j]);
         float peak = v[0];
@@ -130,15 +151,12 @@ __global__ __launch_bounds__(NT) void k_beam_pass(BeamArgs p)
     if (tid < head) take1(tid, edge[0]);
     int c = tid;
     for (; c + (U - 1) * NT < chunks; c += U * NT) {
-        float v[U][W], peak = kNegInf;
+        float v[U * W], peak = kNegInf;
         load(c);
 #pragma unroll
-        for (int u = 0; u < U; ++u) peak = __builtin_fmaxf(peak, widen(v[u], u, c));
+        for (int u = 0; u < U; ++u) peak = __builtin_fmaxf(peak, widen(v + u * W, u, c));
         st.raise(peak);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < W; ++j) st.add(v[u][j]);
+        st.add(v);
     }
     if (c < chunks) {                                     // fewer than U are left
         load(c);
@@ -147,8 +165,7 @@ __global__ __launch_bounds__(NT) void k_beam_pass(BeamArgs p)
             if (c + u * NT >= chunks) break;
             float v[W];
             st.raise(widen(v, u, c));
-#pragma unroll
-            for (int j = 0; j < W; ++j) st.add(v[j]);
+            st.add(v);
         }
     }
     if (tid < n - tail) take1(tail + tid, edge[1]);
@@ -203,12 +220,7 @@ __global__ __launch_bounds__(NT) void k_beam_pass(BeamArgs p)
 }
 
 // ------------------------------------------------------------------ among the beams -----
-// A continuation: its total, as an integer of the same order (0: it does not count), and what
-// orders equal totals, the beam and the logit's key.
-struct BeamChoice {
-    uint64_t total, key;
-    uint32_t beam;
-};
+// Totals as integers of the same order; 0 for those that do not count.
 __device__ inline uint64_t ordered64(double x)
 {
     const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);
@@ -218,98 +230,151 @@ __device__ inline float total_value(uint64_t o)
 {
     return float(__builtin_bit_cast(double, (o >> 63) ? o & ~(uint64_t(1) << 63) : ~o));
 }
-__device__ inline bool before(const BeamChoice &a, const BeamChoice &b)
-{
-    if (a.total != b.total) return a.total > b.total;
-    return a.beam != b.beam ? a.beam < b.beam : a.key > b.key;
-}
+
+// Continuations to be ranked: their totals, and what orders equal ones, the beam and the logit's key.
+template <int MOST> struct BeamList {
+    uint64_t total[MOST], key[MOST];
+    uint8_t beam[MOST];
+
+    __device__ void put(int i, uint64_t t, uint64_t k, int b) { total[i] = t; key[i] = k; beam[i] = uint8_t(b); }
+    // how many of the first n come before entry i
+    __device__ int rank(int i, int n) const
+    {
+        const uint64_t t = total[i];
+        int r = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            if (total[j] > t) ++r;
+            else if (total[j] == t)
+                r += beam[j] != beam[i] ? beam[j] < beam[i] : key[j] > key[i];
+        }
+        return r;
+    }
+};
 
 // One workgroup per request: each beam's log-sum-exp from its parts, then the `top` best of the
 // parts' W splits top keys. A bound that at least `top` of them reach comes from the threads' best
-// ones; those that reach it are ranked against each other.
-constexpr int kChoiceThreads = 256;
+// ones; those that reach it are ranked against each other. All of it is latency: the keys are
+// loaded first, what fits the registers (kKept to a thread), and meanwhile the sums are joined, the
+// parts of several beams side by side.
+constexpr int kChoiceThreads = 256, kKept = 8;
 __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
 {
-    constexpr int NT = kChoiceThreads, MOST = 1024;
+    constexpr int NT = kChoiceThreads, WAVES = NT / 64, SHARE = 64 / WAVES, MOST = 1024;
     // a total is (x - peak) + offset: taken in this order, logits far from 0 cancel first
-    __shared__ double offset[BEAM_MAX];                   // score - log sum; of a finished beam its score
-    __shared__ float peak[BEAM_MAX];
+    __shared__ double offset[BEAM_MAX];                   // score - log of the sum; of a finished beam its score
+    __shared__ float peaks[BEAM_MAX];
     __shared__ bool ended[BEAM_MAX];
-    __shared__ uint64_t best[NT], bound;
-    __shared__ BeamChoice list[MOST], kept[64];
+    __shared__ uint32_t best[NT];
+    __shared__ int ranks[NT];
+    __shared__ BeamList<MOST> list;
+    __shared__ uint64_t kept_total[BEAM_MAX], kept_key[BEAM_MAX];
+    __shared__ uint8_t kept_beam[BEAM_MAX];
     __shared__ int count;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t request = blockIdx.x, row0 = request * p.W;
     const char *parts = p.parts + row0 * p.splits * p.part_bytes;
     const auto part = [&](int i) { return reinterpret_cast<const RowPart *>(parts + i * p.part_bytes); };
-    for (int w = wave; w < p.W; w += NT / 64) {
-        const bool done = p.finished && p.finished[row0 + w];
-        double value = double(p.scores[row0 + w]);
+    const int total = p.W * p.splits * p.top;
+    const auto load_key = [&](int i, int &w) {
+        const int at = divide(i, p.by_top);
+        w = divide(at, p.by_splits);
+        return reinterpret_cast<const uint64_t *>(part(at) + 1)[i - at * p.top];
+    };
+    // lanes to a beam: as many as it has parts, a power of two
+    int lanes = 1;
+    while (lanes < p.splits && lanes < 64) lanes *= 2;
+    const int sub = tid & (lanes - 1), group = tid / lanes;
+    // (finished beams have no parts written: what is read of them is not used)
+    const auto row_part = [&](int w, int s) { return w < p.W && s < p.splits ? *part(w * p.splits + s) : RowPart{kLowest, 0.0f, 0.0f, 0.0f}; };
+    RowPart first = row_part(group, sub);
+    double value = group < p.W ? double(p.scores[row0 + group]) : 0.0;
+    bool done = group < p.W && p.finished && p.finished[row0 + group];
+    uint64_t key[kKept];
+    int beam[kKept];
+#pragma unroll
+    for (int e = 0; e < kKept; ++e) {
+        beam[e] = 0;
+        key[e] = e * NT + tid < total ? load_key(e * NT + tid, beam[e]) : 0;
+    }
+    for (int w = group; w < p.W;) {
         float m = kLowest;
         if (!done) {
-            for (int s = lane; s < p.splits; s += 64) m = __builtin_fmaxf(m, part(w * p.splits + s)->peak);
-            m = wave_reduce(m, [](float a, float b) { return __builtin_fmaxf(a, b); });
-            double sum = 0.0;
-            for (int s = lane; s < p.splits; s += 64) {
-                const RowPart *q = part(w * p.splits + s);
-                sum += double(q->sum) * exp(double(q->peak) - double(m));
-            }
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-            value -= log(sum);
+            m = first.peak;
+            for (int s = sub + lanes; s < p.splits; s += lanes) m = __builtin_fmaxf(m, row_part(w, s).peak);
+            for (int d = 1; d < lanes; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+            const double to = beam_reference(m);
+            const auto term = [&](const RowPart &q) {
+                const float down = __builtin_fmaxf(float(beam_reference(q.peak) - to), -1000.0f);
+                return double(q.sum) * double(__builtin_amdgcn_exp2f(down));
+            };
+            double sum = term(first);
+            for (int s = sub + lanes; s < p.splits; s += lanes) sum += term(row_part(w, s));
+            for (int d = 1; d < lanes; d <<= 1) sum += __shfl_xor(sum, d);
+            value -= log2(sum) * kNats + (__builtin_fabsf(m) <= kFar ? to * kNats - double(m) : 0.0);
         }
-        if (lane == 0) { offset[w] = value; peak[w] = m; ended[w] = done; }
+        if (sub == 0) { offset[w] = value; peaks[w] = m; ended[w] = done; }
+        w += NT / lanes;
+        if (w < p.W) {
+            first = row_part(w, sub);
+            value = double(p.scores[row0 + w]);
+            done = p.finished && p.finished[row0 + w];
+        }
     }
-    if (tid == 0) { count = 0; bound = 0; }
+    if (tid == 0) count = 0;
     __syncthreads();
 
-    const int total = p.W * p.splits * p.top;
-    const auto choice = [&](int i) {
-        const int at = i / p.top, w = at / p.splits;
-        BeamChoice c{0, 0, uint32_t(w)};
-        if (ended[w]) {
-            if (i == w * p.splits * p.top) c.total = ordered64(offset[w]);
-        } else {
-            c.key = reinterpret_cast<const uint64_t *>(part(at) + 1)[i - at * p.top];
-            if (c.key != 0) c.total = ordered64((double(key_value(c.key)) - double(peak[w])) + offset[w]);
-        }
-        return c;
+    // the total of key i, which is beam w's; of a finished beam the first counts alone
+    const auto total_of = [&](uint64_t k, int i, int w) -> uint64_t {
+        if (ended[w]) return i == w * p.splits * p.top ? ordered64(offset[w]) : 0;
+        return k == 0 ? 0 : ordered64((double(key_value(k)) - double(peaks[w])) + offset[w]);
     };
-    uint64_t mine = 0;
-#pragma unroll 4
-    for (int i = tid; i < total; i += NT) mine = max(mine, choice(i).total);
-    best[tid] = mine;
-    __syncthreads();
-    if (tid < 64) {
-        // the least of the joined lanes' bests that fewer than `top` others exceed
-        uint64_t k = best[tid];
+    uint64_t mine = 0, t[kKept];
 #pragma unroll
-        for (int w = 1; w < NT / 64; ++w) k = max(k, best[w * 64 + tid]);
-        int rank = 0;
-        for (int j = 0; j < 64; ++j) rank += lane_key(k, j) > k;
-        uint64_t t = rank < p.top ? k : ~uint64_t(0);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) t = min(t, uint64_t(__shfl_xor(static_cast<unsigned long long>(t), d)));
-        if (tid == 0) bound = max(t, uint64_t(1));
+    for (int e = 0; e < kKept; ++e) {
+        t[e] = e * NT + tid < total ? total_of(key[e], e * NT + tid, beam[e]) : 0;
+        mine = max(mine, t[e]);
     }
+    for (int i = kKept * NT + tid; i < total; i += NT) {
+        int w;
+        const uint64_t k = load_key(i, w);
+        mine = max(mine, total_of(k, i, w));
+    }
+    best[tid] = uint32_t(mine >> 32);
     __syncthreads();
-    const uint64_t floor = bound;
-    for (int i = tid; i < total; i += NT) {
-        const BeamChoice c = choice(i);
-        if (c.total < floor) continue;
+    // the threads joined to 64; the least of these that fewer than `top` others exceed, by the
+    // totals' upper words
+    uint32_t k = best[lane];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) k = max(k, best[w * 64 + lane]);
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < SHARE; ++j) rank += uint32_t(__builtin_amdgcn_readlane(k, wave * SHARE + j)) > k;
+    ranks[tid] = rank;
+    __syncthreads();
+    rank = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) rank += ranks[w * 64 + lane];
+    uint64_t at = 0;
+    for (int r = p.top - 1; at == 0; --r) at = __ballot(rank == r);          // (rank 0 is always there)
+    const uint32_t least = __builtin_amdgcn_readlane(k, __builtin_ctzll(at));
+    const uint64_t floor = max(uint64_t(least) << 32, uint64_t(1));
+
+    const auto put = [&](uint64_t total, uint64_t key, int w) {
+        if (total < floor) return;
         const int to = atomicAdd(&count, 1);
-        if (to < MOST) list[to] = c;
+        if (to < MOST) list.put(to, total, key, w);
+    };
+#pragma unroll
+    for (int e = 0; e < kKept; ++e) put(t[e], key[e], beam[e]);
+    for (int i = kKept * NT + tid; i < total; i += NT) {
+        int w;
+        const uint64_t k = load_key(i, w);
+        put(total_of(k, i, w), k, w);
     }
     __syncthreads();
     int n = count;
-    const auto ranked = [&](int have, auto fn) {
-        for (int i = tid; i < have; i += NT) {
-            const BeamChoice c = list[i];
-            int r = 0;
-            for (int j = 0; j < have; ++j) r += before(list[j], c);
-            if (r < p.top) fn(r, c);
-        }
-    };
     if (n > MOST) {
         // many equal totals: NT at a time, the list cut to its best whenever it might overflow
         __syncthreads();
@@ -317,27 +382,55 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
         __syncthreads();
         for (int i0 = 0; i0 < total; i0 += NT) {
             if (i0 + tid < total) {
-                const BeamChoice c = choice(i0 + tid);
-                if (c.total >= floor) list[atomicAdd(&count, 1)] = c;
+                int w;
+                const uint64_t k = load_key(i0 + tid, w);
+                put(total_of(k, i0 + tid, w), k, w);
             }
             __syncthreads();
             n = count;
             __syncthreads();                              // all have read it
             if (n <= MOST - NT) continue;
-            ranked(n, [&](int r, const BeamChoice &c) { kept[r] = c; });
+            for (int i = tid; i < n; i += NT) {
+                const int r = list.rank(i, n);
+                if (r < p.top) { kept_total[r] = list.total[i]; kept_key[r] = list.key[i]; kept_beam[r] = list.beam[i]; }
+            }
             __syncthreads();
-            if (tid < p.top) list[tid] = kept[tid];
+            if (tid < p.top) list.put(tid, kept_total[tid], kept_key[tid], kept_beam[tid]);
             if (tid == 0) count = p.top;
             n = p.top;
             __syncthreads();
         }
     }
     const int64_t out = request * p.top;
-    ranked(n, [&](int r, const BeamChoice &c) {
-        p.out_scores[out + r] = total_value(c.total);
-        p.out_beams[out + r] = int64_t(c.beam);
-        p.out_tokens[out + r] = ended[c.beam] ? p.pad_token : int64_t(key_index(c.key));
-    });
+    const auto write = [&](int r, uint64_t total, uint64_t key, int w) {
+        p.out_scores[out + r] = total_value(total);
+        p.out_beams[out + r] = w;
+        p.out_tokens[out + r] = ended[w] ? p.pad_token : int64_t(key_index(key));
+    };
+    if (n <= 64) {
+        // a lane holds an entry, and each wave compares them with its share of them
+        const uint64_t mt = lane < n ? list.total[lane] : 0, mk = lane < n ? list.key[lane] : 0;
+        const int mb = lane < n ? list.beam[lane] : 0;
+        int r = 0;
+        for (int j = wave; j < n; j += WAVES) {
+            const uint64_t jt = lane_key(mt, j), jk = lane_key(mk, j);
+            const int jb = __builtin_amdgcn_readlane(mb, j);
+            r += jt > mt || (jt == mt && (jb < mb || (jb == mb && jk > mk)));
+        }
+        ranks[tid] = r;
+        __syncthreads();
+        if (tid < n) {
+            r = 0;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) r += ranks[w * 64 + lane];
+            if (r < p.top) write(r, mt, mk, mb);
+        }
+    } else {
+        for (int i = tid; i < n; i += NT) {
+            const int r = list.rank(i, n);
+            if (r < p.top) write(r, list.total[i], list.key[i], list.beam[i]);
+        }
+    }
     if (tid < p.top && tid >= n) {
         p.out_scores[out + tid] = kNegInf;
         p.out_beams[out + tid] = -1;
@@ -350,10 +443,11 @@ struct StateArgs {
     const char *src;
     char *dst;
     int64_t src_row, dst_row, src_step1, dst_step1, src_step2, dst_step2, run;
-    int count2, chunks;        // pieces along the inner dimension, chunks of 16 bytes to a piece
-    int columns, blocks;       // chunks to a row, workgroups to a request
+    int columns, blocks;       // chunks of 16 bytes to a row, workgroups to a request
+    int chunks, count2;        // chunks to a piece, pieces along the inner dimension
+    Divisor by_blocks, by_chunks, by_count2;
 };
-constexpr int kStates = 40;    // to a launch: the arguments stay below 4 KB
+constexpr int kStates = 32;    // to a launch: the arguments stay below 4 KB
 struct ReorderArgs {
     const void *beams;
     int beam_bytes, W, count;
@@ -361,54 +455,58 @@ struct ReorderArgs {
     StateArgs states[kStates];
 };
 static_assert(sizeof(ReorderArgs) <= 4096, "kernel arguments");
+static_assert(BEAM_MAX <= 64 && kStates <= 64, "a lane for each beam, and for each state");
 
 // A thread takes 16 bytes of the same place of all of a request's rows: it loads what each row is to
 // become, then stores it, so that a state may be reordered in place. Rows that stay where they
-// are (in place) are left alone.
+// are (in place) are left alone. Bound by memory; small states by the way from the arguments to
+// the indices to the rows: the state of a workgroup is found by all lanes at once, the request's
+// indices are one load, a lane each.
 constexpr int kReorderThreads = 256;
 template <int MOST>
 __global__ __launch_bounds__(kReorderThreads) void k_reorder(ReorderArgs p)
 {
-    const int group = blockIdx.x;
-    int t = 0;
-    while (t + 1 < p.count && group >= p.first[t + 1]) ++t;
+    const int group = blockIdx.x, lane = threadIdx.x & 63;
+    const int at_state = lane < p.count ? p.first[lane] : 0x7fffffff;
+    const int t = __builtin_amdgcn_readfirstlane(__popcll(__ballot(group >= at_state)) - 1);
     const StateArgs &s = p.states[t];
-    const int request = (group - p.first[t]) / s.blocks;
-    const int column = (group - p.first[t] - request * s.blocks) * kReorderThreads + int(threadIdx.x);
-    if (column >= s.columns) return;
-    const int piece = column / s.chunks, i = piece / s.count2, j = piece - i * s.count2;
-    const int64_t at = int64_t(column - piece * s.chunks) * 16;
-    const int n = int(min(int64_t(16), s.run - at));
+    const int request = divide(group - p.first[t], s.by_blocks);
     const int64_t row0 = int64_t(request) * p.W;
+    int from = lane;
+    if (lane < p.W) {
+        const int64_t b = token_of(p.beams, p.beam_bytes, row0 + lane);
+        from = b >= 0 && b < p.W ? int(b) : lane;
+    }
+    const int column = (group - p.first[t] - request * s.blocks) * kReorderThreads + int(threadIdx.x);
+    const int piece = divide(column, s.by_chunks), i = divide(piece, s.by_count2), j = piece - i * s.count2;
+    const int64_t at = int64_t(column - piece * s.chunks) * 16;
+    const int n = column < s.columns ? int(min(int64_t(16), s.run - at)) : 0;
     const char *src = s.src + row0 * s.src_row + i * s.src_step1 + j * s.src_step2 + at;
     char *dst = s.dst + row0 * s.dst_row + i * s.dst_step1 + j * s.dst_step2 + at;
-    const bool in_place = s.src == s.dst;
-    int from[MOST];
-#pragma unroll
-    for (int w = 0; w < MOST; ++w) {
-        from[w] = w;
-        if (w < p.W) {
-            const int64_t b = token_of(p.beams, p.beam_bytes, row0 + w);
-            if (b >= 0 && b < p.W) from[w] = __builtin_amdgcn_readfirstlane(int(b));
-        }
-    }
+    const int64_t src_row = s.src_row, dst_row = s.dst_row;
+    // the rows that are written
+    const uint64_t rows = p.W == 64 ? ~uint64_t(0) : (uint64_t(1) << p.W) - 1;
+    const uint64_t moves = rows & (s.src == s.dst ? __ballot(from != lane) : ~uint64_t(0));
     const auto move = [&](auto zero, int off) __attribute__((always_inline)) {
-        typedef Pack<decltype(zero), 1> P;
-        P v[MOST];
-#pragma unroll
-        for (int w = 0; w < MOST; ++w)
-            if (w < p.W && !(in_place && from[w] == w))
-                v[w] = *reinterpret_cast<const P *>(src + from[w] * s.src_row + off);
-#pragma unroll
-        for (int w = 0; w < MOST; ++w)
-            if (w < p.W && !(in_place && from[w] == w))
-                *reinterpret_cast<P *>(dst + w * s.dst_row + off) = v[w];
+        typedef decltype(zero) T;
+        typedef T __attribute__((aligned(1))) anywhere;
+        T v[MOST];
+        static_for<0, MOST>([&](auto wc) __attribute__((always_inline)) {
+            constexpr int w = decltype(wc)::value;
+            v[w] = zero;
+            if (moves >> w & 1)
+                v[w] = *reinterpret_cast<const anywhere *>(src + __builtin_amdgcn_readlane(from, w) * src_row + off);
+        });
+        static_for<0, MOST>([&](auto wc) __attribute__((always_inline)) {
+            constexpr int w = decltype(wc)::value;
+            if (moves >> w & 1) *reinterpret_cast<anywhere *>(dst + w * dst_row + off) = v[w];
+        });
     };
-    if (n == 16) { move(Bits<16>::type{}, 0); return; }
-    if (n & 8) move(uint64_t(0), 0);
-    if (n & 4) move(uint32_t(0), n & 8);
-    if (n & 2) move(uint16_t(0), n & 12);
-    if (n & 1) move(uint8_t(0), n & 14);
+    if (n == 16) move(Bits<16>::type{}, 0);
+    else if (n == 8) move(uint64_t(0), 0);
+    else
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) move(uint8_t(0), k);
 }
 
 }  // namespace sgemm

@@ -69,13 +69,6 @@ template <typename T> __device__ inline Pack<T, 8> mx4_decode(uint32_t q, float 
     return x;
 }
 
-// t / d == mulhi(t, mul) >> shift for t < 2^31.
-struct Mx4Divisor {
-    uint32_t mul;
-    int shift;
-};
-__device__ inline int mx4_divide(int t, Mx4Divisor d) { return int(__umulhi(uint32_t(t), d.mul) >> d.shift); }
-
 struct Mx4RowArgs {
     const void *X;             // (the inverse: the values written)
     int64_t ldx;
@@ -84,7 +77,7 @@ struct Mx4RowArgs {
     uint8_t *scales;
     int64_t lds;
     int M, K, units;           // units of 8 elements to a row, whole blocks of them
-    Mx4Divisor by_units;
+    Divisor by_units;
 };
 
 // Four lanes share a block, 8 elements each. HBM-bound: 2 or 4 bytes in and 17 / 32 out of an element.
@@ -93,7 +86,7 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(Mx4RowArgs p)
 {
     typedef typename Elem<DT>::type T;
     const int e = int(blockIdx.x) * 256 + int(threadIdx.x);
-    const int row = mx4_divide(e, p.by_units), unit = e - row * p.units, k = unit * 8;
+    const int row = divide(e, p.by_units), unit = e - row * p.units, k = unit * 8;
     const bool mine = row < p.M;
     const T *x = static_cast<const T *>(p.X) + row * p.ldx + k;
     Pack<T, 8> v;
@@ -130,7 +123,7 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(Mx4RowArgs p)
 {
     typedef typename Elem<DT>::type T;
     const int e = int(blockIdx.x) * 256 + int(threadIdx.x);
-    const int row = mx4_divide(e, p.by_units), unit = e - row * p.units, k = unit * 8;
+    const int row = divide(e, p.by_units), unit = e - row * p.units, k = unit * 8;
     if (row >= p.M || k >= p.K) return;
     const uint8_t *in = p.Q + row * p.ldq + k / 2;
     const float size = mx4_unit(p.scales[row * p.lds + unit / 4]);

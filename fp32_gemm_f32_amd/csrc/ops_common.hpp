@@ -28,6 +28,25 @@ int launch(void (*kern)(KArgs...), dim3 grid, dim3 block, void *stream, Args... 
 // needs more goes out in several launches, each over its own rows or columns.
 inline int64_t most_groups(int threads) { return ((int64_t(1) << 32) - 1) / threads; }
 
+// t / d == mulhi(t, mul) >> shift for t < 2^31 and 2^shift < d <= 2^(shift + 1): mul = 2^(32 + shift) / d
+// rounded up is too large by less than 1, which adds less than t / 2^(32 + shift) < 1 / d to t / d.
+// (d = 1 takes none of them: mul = 2^32 has no room, and t is the quotient.)
+struct Divisor {
+    uint32_t mul;
+    int shift;
+};
+inline Divisor divisor(uint32_t d)
+{
+    if (d == 1) return {0, 0};
+    int shift = 0;
+    while ((uint64_t(2) << shift) < d) ++shift;
+    return {uint32_t(((uint64_t(1) << (32 + shift)) + d - 1) / d), shift};
+}
+__device__ inline int divide(int t, Divisor d)
+{
+    return d.mul == 0 ? t : int(__umulhi(uint32_t(t), d.mul) >> d.shift);
+}
+
 // Compute units of the current device, looked up once per device.
 inline int device_cus(int *out)
 {
