@@ -75,7 +75,12 @@ const Mx4Variant kTiles[] = {
     tile<256, 256, 2, 2, 2>("mx4_256x256_w4", 9.125, 0.0, 2.20, 7.80),
 };
 // Few rows: 16 rows and columns, turns of 512 elements to a wave.
-const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0};
+const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves, 1>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0};
+// For more columns than run at once and a K of a turn to a wave: two and one to a compute unit, which go on.
+const Mx4Variant kRowsOn[] = {
+    {"mx4_rows16_on8", &k_mx4_rows_on<8>, 16, 16, 512, 2, 1, 0.0, 0.0, 0.0, 0.0},
+    {"mx4_rows16_on16", &k_mx4_rows_on<16>, 16, 16, 1024, 1, 1, 0.0, 0.0, 0.0, 0.0},
+};
 
 // The operands, and which of them the tiles can load as they lie: rows on word boundaries, A's of
 // whole chunks.
@@ -98,10 +103,10 @@ struct Mx4Plan {
 constexpr double kLaunch = 2.5;          // us: a kernel's start and end
 constexpr double kStreamPerUs = 6.4e6;   // bytes of operands, from the last-level cache too
 
-// Whether workgroups go on to another tile, one to a compute unit.
+// Whether workgroups go on to another tile, as many as run at once.
 bool goes_on(const Mx4Variant &v, int64_t tiles, int splits, int64_t panels, int cus)
 {
-    return splits == 1 && v.loop > 0 && panels >= v.loop && tiles > cus;
+    return splits == 1 && v.loop > 0 && panels >= v.loop && tiles > cus * v.at_once;
 }
 // Microseconds of workgroups of `panels` panels each: whole rounds of them and what is left.
 double tile_cost(const Mx4Variant &v, int64_t groups, int splits, int64_t panels, int cus)
@@ -133,6 +138,10 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
     };
     const int most = int(std::min<int64_t>(16, std::max<int64_t>(1, kb / 512)));
     if (M <= 16) {
+        // (8 x 32001 x 2048 11.6 us with a workgroup to 16 columns, 8.7 going on; 1 x 16384 x 4096 9.0 and 9.6)
+        const int64_t groups = ceil_div(N, 16), turns = ceil_div(kb, kMx4Turn);
+        if (groups > 6 * cus && turns <= 16)
+            return {&kRowsOn[turns <= 8 ? 0 : 1], 1, int(groups), 1, kb, {}, kLaunch + bytes / 4.6e6};
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             const int64_t groups = ceil_div(N, kRows.bn) * s;
@@ -162,6 +171,14 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
         }
     }
     return best;
+}
+
+// Rows to a workgroup that copies them: about 512 chunks, two to a thread (1023 and 1025 rows of 515 bytes:
+// 6.0 us with 2048), more where there are many.
+int rows_to_copy(int rows, int64_t ld16)
+{
+    const int64_t chunks = std::clamp<int64_t>(rows * (ld16 / 16) / 2048, 512, 2048);
+    return int(std::max<int64_t>(1, chunks / (ld16 / 16)));
 }
 
 // Workspace: the splits' sums, then the copies.
@@ -288,7 +305,7 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
         if (!plan.copy[i]) continue;
         const int rows = i % 2 == 0 ? M : N, bytes = i < 2 ? kb : blocks;
         const int64_t ld16 = round16(bytes);
-        const int per = int(std::max<int64_t>(1, 2048 / (ld16 / 16)));
+        const int per = rows_to_copy(rows, ld16);
         int8_t *to = static_cast<int8_t *>(workspace) + space.at[i];
         copies.rows[i] = {reinterpret_cast<const int8_t *>(x.p[i]), to, x.ld[i], rows, per, int(ceil_div(rows, per))};
         copies.bytes[i] = bytes;
@@ -329,7 +346,7 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
             const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
             p.group_mul = d.mul; p.group_shift = d.shift;
             int64_t groups = int64_t(p.tiles_m) * p.tiles_n * plan.splits;
-            if (loops) groups = std::min<int64_t>(groups, cus);
+            if (loops) groups = std::min<int64_t>(groups, int64_t(cus) * v.at_once);
             st = launch(v.kernel, dim3(unsigned(groups)), dim3(v.threads), stream, p);
             if (st != SGEMM_OK) return st;
         }
