@@ -68,11 +68,9 @@ const Mx4Variant kTiles[] = {
     tile<64, 64, 2, 2, 4>("mx4_64x64", 0.200, 0.37, 1.84, 0.0),
     tile<64, 128, 2, 4, 2>("mx4_64x128", 0.298, 0.52, 2.17, 0.0),
     tile<128, 128, 4, 2, 2>("mx4_128x128", 0.506, 0.95, 1.19, 0.0),
-    tile<128, 128, 4, 2, 4>("mx4_128x128_s4", 0.408, 0.0, 2.04, 3.76),
     tile<128, 256, 2, 4, 2>("mx4_128x256", 0.644, 0.0, 2.83, 7.49),
     tile<192, 256, 2, 4, 2>("mx4_192x256", 0.962, 0.0, 3.46, 8.19),
     tile<256, 256, 4, 2, 2>("mx4_256x256", 1.125, 0.0, 2.20, 7.80),
-    tile<256, 256, 2, 2, 2>("mx4_256x256_w4", 9.125, 0.0, 2.20, 7.80),
 };
 // Few rows: 16 rows and columns, turns of 512 elements to a wave.
 const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves, 1>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0};
@@ -318,6 +316,7 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
         if (st != SGEMM_OK) return st;
     }
     p.lda = x.ld[0]; p.ldb = x.ld[1]; p.ldsa = x.ld[2]; p.ldsb = x.ld[3];
+    p.sa_step = p.sb_step = 16;
     p.partial = static_cast<float *>(workspace);
     p.splits = plan.splits; p.chunk = plan.splits > 1 ? plan.chunk : kb;
     const Mx4Variant &v = *plan.v;
@@ -340,6 +339,8 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
             p.B = x.p[1] + n * p.ldb;
             p.sa = x.p[2] + m * p.ldsa;
             p.sb = x.p[3] + n * p.ldsb;
+            p.sa_bytes = (p.M - 1) * p.ldsa + blocks;
+            p.sb_bytes = (p.N - 1) * p.ldsb + blocks;
             p.bias = bias ? bias + n : nullptr;
             p.C = static_cast<char *>(C) + (m * ldc + n) * csize;
             p.stream = reinterpret_cast<uintptr_t>(p.C) % 64 == 0 && ldc * csize % 64 == 0;

@@ -147,6 +147,8 @@ struct Mx4Args {
     void *C;
     float *partial;            // splits > 1: sums of split s at partial + s * M * N
     int64_t lda, ldb, ldsa, ldsb, ldc;
+    int64_t sa_bytes, sb_bytes;// tiles: all of the scales'
+    int sa_step, sb_step;      // tiles: from the 16 scales of a row for two panels to the next 16
     int M, N, KB;              // KB: bytes to a row, K / 2
     int c_dtype, tiles_m, tiles_n;
     uint32_t group_mul;        // division by kGroupM * tiles_n without dividing: see tile_of

@@ -1,5 +1,5 @@
 // kernel_mx4_tiles.hpp -- the product of microscaled 4-bit operands (gemm_mx4.h) by tiles, on
-// v_mfma_scale_f32_32x32x64_f8f6f4.
+// v_mfma_scale_f32_16x16x128_f8f6f4.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -15,15 +15,17 @@ namespace sgemm {
 // One workgroup computes a BM x BN tile with WGM x WGN waves, panel by panel of BK = 128 bytes (256
 // elements) of K. Operand bytes move as the 8-bit product's do: straight to LDS, 16 bytes a lane, chunk
 // q of row r at chunk position q ^ a_swizzle(r), and a lane's CB column blocks are neighbours in C.
-//  * MFMA operands: lane l supplies row l % 32 and one block of 32 values with its scale. Step t of a
-//    panel takes block t + 4 (l / 32) on both sides, so that the four scales a lane needs for a panel
-//    are one word, of which step t takes byte t. Accumulator register v of lane l is row
-//    8 (v / 4) + v % 4 + 4 (l / 32) and column l % 32 of the block.
+//  * MFMA operands: lane l supplies row l % 16 and one block of 32 values with its scale. Step t of a
+//    panel takes block t + 2 (l / 16) on both sides (so that the rows that one ds_read_b128 reads lie
+//    on distinct banks). Accumulator register v of lane l is row 4 (l / 16) + v and column l % 16 of the
+//    block. These 16 x 16 blocks of 128 values do 8 % more for their power than 32 x 32 of 64 (6.8
+//    against 6.3 PFLOP/s from registers, random values), and large products are bound by power.
 //  * Panels go in pairs, for their scales come 16 bytes to a row, one load of 16 bytes a lane, ahead of
-//    the loads of an even panel, into a ring of their own. A word of each of 32 rows 16 bytes apart
-//    would hit 8 banks; so a lane reads all 16 bytes of a row, lanes below 32 of one block of rows and
-//    the others of the next, and one exchange between the halves (v_permlane32_swap) gives both
-//    blocks a panel's words.
+//    the loads of an even panel, into a ring of their own. In rows they lie 16 bytes here and there,
+//    each a line of its own for the caches; large products put them pair by pair of panels first.
+//    A lane reads all 16 bytes of a row, the four groups of 16 lanes those of four blocks of rows,
+//    and exchanges between the groups give each block a panel's scales: 3 reads for 12 blocks and
+//    two panels.
 //  * Chunks past the tile's rows or past K read as zero through an offset out of range. Scales behind
 //    the last block may be anything and are masked: one that is no number would make zeros NaN. K
 //    ends on whole chunks on A's side (B's bytes behind K meet zeros): other A are copied first.
@@ -32,6 +34,7 @@ namespace sgemm {
 template <int BM_, int BN_, int WGM_, int WGN_, int NSTG_>
 struct Mx4Tile : ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> {
     typedef ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> Base;
+    static constexpr int RB = Base::WM / 16, CB = Base::WN / 16, STEPS = 2;
     static constexpr int SROWS = (BM_ + BN_ + Base::NT - 1) / Base::NT * Base::NT;   // rows of scales, filled up
     static constexpr int SCH = SROWS / Base::NT;     // a thread's chunks of scales
     static constexpr int SBYTES = SROWS * 16, SRING = NSTG_ / 2;
@@ -39,24 +42,33 @@ struct Mx4Tile : ByteTile<BM_, BN_, WGM_, WGN_, 128, NSTG_> {
     static constexpr bool LOOP = LDS > 80 * 1024;    // one workgroup to a compute unit: it goes on to another tile
     static_assert(LDS <= 160 * 1024, "LDS");
     static_assert(NSTG_ % 2 == 0, "panels go in pairs");
+    static_assert(Base::NT / Base::CPR % 16 == 0, "a thread's rows at common distances");
+    static_assert(BM_ % 64 == 0, "scales of whole waves");
 };
 
+// Global row of B (within the tile) at LDS row p.
+template <typename T> __device__ inline int mx4_b_row(int p)
+{
+    const int w = p / T::WN, r = p % T::WN;
+    return w * T::WN + T::CB * (r % 16) + r / 16;
+}
+
 template <typename T>
-__device__ __forceinline__ void mx4_epilogue(const Mx4Args &p, const f32x16 (&acc)[T::RB][T::CB],
+__device__ __forceinline__ void mx4_epilogue(const Mx4Args &p, const f32x4 (&acc)[T::RB][T::CB],
                                              const float (&bias)[T::CB], int m0, int n0, int split, int wm, int wn)
 {
-    const int frow = threadIdx.x & 31, fhi = (threadIdx.x & 63) >> 5;
-    const int col = n0 + wn * T::WN + T::CB * frow;
+    const int lane = threadIdx.x & 63;
+    const int col = n0 + wn * T::WN + T::CB * (lane & 15);
     const int valid = p.N - col;
-    const int row0 = m0 + wm * T::WM + 4 * fhi;
+    const int row0 = m0 + wm * T::WM + 4 * (lane >> 4);
     if (valid <= 0) return;
     if (p.splits > 1) {
         float *out = p.partial + int64_t(split) * p.M * p.N;
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
+            for (int v = 0; v < 4; ++v) {
+                const int m = row0 + 16 * i + v;
                 if (m < p.M)
 #pragma unroll
                     for (int j = 0; j < T::CB; ++j)
@@ -65,16 +77,20 @@ __device__ __forceinline__ void mx4_epilogue(const Mx4Args &p, const f32x16 (&ac
         return;
     }
     auto store_all = [&](auto dt, auto stream) __attribute__((always_inline)) {
+        constexpr int DT = decltype(dt)::value, W = DT == SGEMM_DTYPE_F32 && T::CB > 4 ? 4 : T::CB;   // 16 bytes to a store
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int m = row0 + 32 * i + 8 * (v / 4) + v % 4;
-                float x[T::CB];
+            for (int v = 0; v < 4; ++v) {
+                const int m = row0 + 16 * i + v;
+                if (m >= p.M) continue;
 #pragma unroll
-                for (int j = 0; j < T::CB; ++j) x[j] = acc[i][j][v] + bias[j];
-                if (m < p.M)
-                    store_values<decltype(dt)::value, T::CB, decltype(stream)::value>(p.C, m * p.ldc + col, x, valid);
+                for (int j = 0; j < T::CB; j += W) {
+                    float x[W];
+#pragma unroll
+                    for (int e = 0; e < W; ++e) x[e] = acc[i][j + e][v] + bias[j + e];
+                    store_values<DT, W, decltype(stream)::value>(p.C, m * p.ldc + col + j, x, valid - j);
+                }
             }
     };
     auto store = [&](auto dt) __attribute__((always_inline)) {
@@ -86,12 +102,12 @@ __device__ __forceinline__ void mx4_epilogue(const Mx4Args &p, const f32x16 (&ac
     else store(std::integral_constant<int, SGEMM_DTYPE_F32>{});
 }
 
-// a + 2^.. a b with the scales' byte `T` on both sides
-template <int T> __device__ __forceinline__ f32x16 mx4_mfma(i32x4 a, i32x4 b, f32x16 c, int sa, int sb)
+// c + a b with the scales' byte T on both sides
+template <int T> __device__ __forceinline__ f32x4 mx4_mfma(i32x4 a, i32x4 b, f32x4 c, int sa, int sb)
 {
     const i32x8 ax = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
     const i32x8 bx = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(ax, bx, c, 4, 4, T, sa, T, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ax, bx, c, 4, 4, T, sa, T, sb);
 }
 
 template <typename T>
@@ -116,10 +132,11 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     // offset is held, the others lie at distances that are the same for all.
     const int prow = tid / T::CPR;                   // LDS row of chunk i = 0
     const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
-    const uint32_t a_off = uint32_t(prow * p.lda) + q * 16, b_off = uint32_t(tile_b_row<T>(prow) * p.ldb) + q * 16;
+    const uint32_t a_off = uint32_t(prow * p.lda) + q * 16, b_off = uint32_t(mx4_b_row<T>(prow) * p.ldb) + q * 16;
     int m0, n0;
     const int8_t *At, *Bt, *St[T::SCH];
     uint32_t a_size, b_size, s_size[T::SCH], s_off[T::SCH];
+    int s_step[T::SCH];                              // from one pair of panels to the next
     auto aim = [&](int tile) __attribute__((always_inline)) {
         int tm, tn;
         tile_of(p, tile, tm, tn);
@@ -136,78 +153,86 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
             const bool of_a = s0 < T::BM;
             const int64_t ld = of_a ? p.ldsa : p.ldsb;
             const int8_t *const from = reinterpret_cast<const int8_t *>(of_a ? p.sa : p.sb);
-            St[i] = from + (of_a ? m0 : n0) * ld + k0 / 16;
-            s_size[i] = bytes_range(St[i], from + ((of_a ? p.M : p.N) - 1) * ld + (p.KB + 15) / 16);
-            s_off[i] = s >= T::BM + T::BN ? kOob : uint32_t((of_a ? s : tile_b_row<T>(s - T::BM)) * ld);
+            s_step[i] = of_a ? p.sa_step : p.sb_step;
+            St[i] = from + (of_a ? m0 : n0) * ld + int64_t(k0 / 256) * s_step[i];
+            s_size[i] = bytes_range(St[i], from + (of_a ? p.sa_bytes : p.sb_bytes));
+            s_off[i] = s >= T::BM + T::BN ? kOob : uint32_t((of_a ? s : mx4_b_row<T>(s - T::BM)) * ld);
         }
     };
-    static_assert(T::BM % 64 == 0, "scales of whole waves");
-    static_assert(T::NT / T::CPR % 32 == 0 || T::NT / T::CPR == 16, "a thread's rows at common distances");
     int tile = int(blockIdx.x) - split * tiles;
     aim(tile);
     float bias[T::CB];
     auto load_bias = [&](int n) __attribute__((always_inline)) {
-        const int col = n + wn * T::WN + T::CB * (lane & 31);
+        const int col = n + wn * T::WN + T::CB * (lane & 15);
 #pragma unroll
         for (int j = 0; j < T::CB; ++j) bias[j] = p.bias && p.splits == 1 ? p.bias[min(col + j, p.N - 1)] : 0.0f;
     };
-    f32x16 acc[T::RB][T::CB];
+    f32x4 acc[T::RB][T::CB];
 #pragma unroll
     for (int i = 0; i < T::RB; ++i)
 #pragma unroll
-        for (int j = 0; j < T::CB; ++j) acc[i][j] = f32x16(0.0f);
+        for (int j = 0; j < T::CB; ++j) acc[i][j] = f32x4(0.0f);
 
-    // operand reads: row l % 32 of a block; chunk t + 4 (l / 32) at step t
-    const int frow = lane & 31, fhi = lane >> 5;
+    // operand reads: row l % 16 of a block; chunk t + 2 (l / 16) at step t
+    const int frow = lane & 15, fq = lane >> 4;
     const int fsw = a_swizzle<T::CPR>(frow);
-    const int a_row = wm * T::WM + frow, b_row = wn * T::WN + frow;
-    const int a_base = a_row * T::BK, b_base = T::A_BYTES + b_row * T::BK;
+    const int a_base = (wm * T::WM + frow) * T::BK, b_base = T::A_BYTES + (wn * T::WN + frow) * T::BK;
     i32x4 fa[T::STEPS][T::RB], fb[T::STEPS][T::CB];
-    // scales: blocks of rows of A, then of B, in pairs; words of the two halves of two panels
-    constexpr int BLOCKS = T::RB + T::CB, PAIRS = (BLOCKS + 1) / 2;
-    i32x4 pair[PAIRS];
-    uint32_t sc[2 * PAIRS];                          // of the panel multiplied
-    int s_at[PAIRS];
+    // scales: blocks of rows of A, then of B, in fours; the two halves of the four words are two panels'
+    constexpr int BLOCKS = T::RB + T::CB, FOURS = (BLOCKS + 3) / 4;
+    i32x4 four[FOURS];
+    uint32_t sc[4 * FOURS];                          // of the panel multiplied
+    int s_at[FOURS];
 #pragma unroll
-    for (int n = 0; n < PAIRS; ++n) {
-        const auto row_of = [&](int block) {
-            return block < T::RB ? wm * T::WM + 32 * block : T::BM + wn * T::WN + 32 * (block - T::RB);
-        };
-        s_at[n] = ((fhi ? row_of(min(2 * n + 1, BLOCKS - 1)) : row_of(2 * n)) + frow) * 16;
+    for (int n = 0; n < FOURS; ++n) {
+        const int block = min(4 * n + fq, BLOCKS - 1);
+        s_at[n] = ((block < T::RB ? wm * T::WM + 16 * block : T::BM + wn * T::WN + 16 * (block - T::RB)) + frow) * 16;
     }
-    auto read = [&](const char *st, auto tc) __attribute__((always_inline)) {
+    // A's operands of a step, and half of B's
+    auto read_a = [&](const char *st, auto tc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value;
-        const int at = ((t + T::STEPS * fhi) ^ fsw) * 16;
+        const int at = ((t + T::STEPS * fq) ^ fsw) * 16;
 #pragma unroll
         for (int i = 0; i < T::RB; ++i)
-            fa[t][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 32 * T::BK);
+            fa[t][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 16 * T::BK);
+    };
+    auto read_b = [&](const char *st, auto tc, auto hc) __attribute__((always_inline)) {
+        constexpr int t = decltype(tc)::value, first = decltype(hc)::value * T::CB / 2;
+        const int at = ((t + T::STEPS * fq) ^ fsw) * 16;
 #pragma unroll
-        for (int j = 0; j < T::CB; ++j)
-            fb[t][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 32 * T::BK);
+        for (int j = first; j < first + T::CB / 2; ++j)
+            fb[t][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 16 * T::BK);
     };
     auto read_scales = [&](int entry) __attribute__((always_inline)) {
         const char *at = ring + entry * T::SBYTES;
 #pragma unroll
-        for (int n = 0; n < PAIRS; ++n) pair[n] = *reinterpret_cast<const i32x4 *>(at + s_at[n]);
+        for (int n = 0; n < FOURS; ++n) four[n] = *reinterpret_cast<const i32x4 *>(at + s_at[n]);
     };
-    // the words of a panel, the even or odd one of the pair read last
+    // The scales of a panel, the even or odd one of the pair read last, byte t for step t. Group g of 16
+    // lanes holds block g's 8 and needs two of them of each block: 2 g and 2 g + 1. Exchanging the halves
+    // of the wave leaves blocks 0 and 1 in one word, 2 and 3 in another, each with the right word of
+    // a block in every other group; exchanging neighbouring groups spreads it to both.
     auto take_scales = [&](int panel, auto odd) __attribute__((always_inline)) {
         constexpr int w = decltype(odd)::value ? 2 : 0;
-        const int left = blocks - 8 * panel - 4 * fhi;
-        const uint32_t keep = left <= 0 ? 0u : ~0u >> (32 - 8 * min(left, 4));
+        const int left = blocks - 8 * panel - 2 * fq, shift = 16 * (fq & 1);
+        const uint32_t keep = left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
 #pragma unroll
-        for (int n = 0; n < PAIRS; ++n) {
-            const auto both = __builtin_amdgcn_permlane32_swap(uint32_t(pair[n][w]), uint32_t(pair[n][w + 1]), false, false);
-            sc[2 * n] = both[0] & keep;
-            sc[2 * n + 1] = both[1] & keep;
+        for (int n = 0; n < FOURS; ++n) {
+            const auto halves = __builtin_amdgcn_permlane32_swap(uint32_t(four[n][w]), uint32_t(four[n][w + 1]), false, false);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const auto both = __builtin_amdgcn_permlane16_swap(halves[h], halves[h], false, false);
+                sc[4 * n + 2 * h] = both[0] >> shift & keep;
+                sc[4 * n + 2 * h + 1] = both[1] >> shift & keep;
+            }
         }
     };
-    auto multiply = [&](auto tc) __attribute__((always_inline)) {
-        constexpr int t = decltype(tc)::value;
+    auto multiply = [&](auto tc, auto hc) __attribute__((always_inline)) {
+        constexpr int t = decltype(tc)::value, first = decltype(hc)::value * T::CB / 2;
 #pragma unroll
-        for (int i = 0; i < T::RB; ++i)
+        for (int j = first; j < first + T::CB / 2; ++j)
 #pragma unroll
-            for (int j = 0; j < T::CB; ++j)
+            for (int i = 0; i < T::RB; ++i)
                 acc[i][j] = mx4_mfma<t>(fa[t][i], fb[t][j], acc[i][j], int(sc[i]), int(sc[T::RB + j]));
     };
 
@@ -218,11 +243,12 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     auto issue_scales = [&](int panel) __attribute__((always_inline)) {
         char *to = ring + load_entry * T::SBYTES;
         load_entry = load_entry + 1 == T::SRING ? 0 : load_entry + 1;
-        const int k = 8 * panel;
-        const uint32_t past = k >= blocks ? kOob : 0u;
+        const uint32_t past = 8 * panel >= blocks ? kOob : 0u;
 #pragma unroll
-        for (int i = 0; i < T::SCH; ++i)
+        for (int i = 0; i < T::SCH; ++i) {
+            const int k = (panel >> 1) * s_step[i];
             load16_lds(St[i] + k, rest(s_size[i], k), s_off[i] | past, to + (i * T::NT + wave * 64) * 16);
+        }
     };
     auto issue = [&](int panel, char *st) __attribute__((always_inline)) {
         const int k = panel * T::BK;
@@ -235,15 +261,19 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
 #pragma unroll
         for (int i = 0; i < T::BCH; ++i)
             load16_lds(Bt + k, rest(b_size, k),
-                       (b_off | past) + uint32_t(tile_b_row<T>(i * (T::NT / T::CPR)) * p.ldb),
+                       (b_off | past) + uint32_t(mx4_b_row<T>(i * (T::NT / T::CPR)) * p.ldb),
                        st + T::A_BYTES + (i * T::NT + wave * 64) * 16);
     };
-    // LOOK steps before a panel's end the reads of its stage are over, so the barrier comes there: the
+    // A step goes in halves of B's columns. In the first the second's columns are read, in the second the
+    // next step's A and first columns: no more than one step's operands and a half are held. In the
+    // middle of a panel's last step the reads of its stage are over, so the barrier comes there: the
     // wave's loads of the next panel have landed, every wave's have after the barrier, and the stage
-    // just read is loaded again and the next one's first operands are read under the last steps'
-    // MFMAs. (Loads still under way then: those of NSTG - 2 panels, with the scales of half of them.)
-    constexpr int LPP = T::ACH + T::BCH, LOOK = 1;
+    // just read is loaded again. (Loads still under way then: those of NSTG - 2 panels, with the scales
+    // of half of them.)
+    constexpr int LPP = T::ACH + T::BCH;
     constexpr int UNDER_WAY = (T::NSTG - 2) * LPP + (T::NSTG - 2) / 2 * T::SCH;
+    typedef std::integral_constant<int, 0> Zero;
+    typedef std::integral_constant<int, 1> One;
     if constexpr (!T::LOOP) load_bias(n0);
 #pragma unroll
     for (int i = 0; i < T::NSTG; ++i) {
@@ -257,7 +287,8 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     int entry = 0;                                   // the ring's entry of the pair read last
     read_scales(0);
     take_scales(0, Even{});
-    static_for<0, LOOK>([&](auto tc) __attribute__((always_inline)) { read(smem, tc); });
+    read_a(smem, Zero{});
+    read_b(smem, Zero{}, Zero{});
     int stage = 0;                                   // of the pair
     int behind = 0;                                  // panels between a panel read and that of its tile
     auto run = [&](int panel, auto odd) __attribute__((always_inline)) {
@@ -265,42 +296,46 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
         char *st = smem + (stage + (ODD ? 1 : 0)) * STAGE;
         if constexpr (ODD) stage = stage + 2 == T::NSTG ? 0 : stage + 2;
         char *next = ODD ? smem + stage * STAGE : st + STAGE;
-        static_for<0, T::STEPS>([&](auto tc) __attribute__((always_inline)) {
-            constexpr int t = decltype(tc)::value;
-            constexpr bool turn = t == T::STEPS - LOOK;
-            if constexpr (turn) {
-                __builtin_amdgcn_sched_barrier(0);
-                wait_vmcnt<UNDER_WAY>();
-                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            }
-            if constexpr (t + LOOK < T::STEPS) read(st, std::integral_constant<int, t + LOOK>{});
-            else read(next, std::integral_constant<int, t + LOOK - T::STEPS>{});
-            if constexpr (turn) {
-                if constexpr (ODD) {
-                    entry = entry + 1 == T::SRING ? 0 : entry + 1;    
-                    read_scales(entry);
-                } else {
-                    issue_scales(panel + T::NSTG - behind);
-                }
-                issue(panel + T::NSTG - behind, st);
-            }
-            multiply(tc);
-            // operand reads behind the first MFMAs, the loads behind the others
-            constexpr int ops = T::RB + T::CB + (turn && ODD ? PAIRS : 0);
-            constexpr int loads = LPP + (ODD ? 0 : T::SCH);
-            constexpr int mf = T::RB * T::CB;
-            constexpr int rm = turn ? (mf + 1) / 2 : (ops < mf ? ops : mf);
-            constexpr int lm = mf - rm > 0 ? mf - rm : 1;
-            static_for<0, mf>([&](auto mc) __attribute__((always_inline)) {
-                constexpr int m = decltype(mc)::value;
-                constexpr int r = m < rm ? (m + 1) * ops / rm - m * ops / rm : 0;
-                constexpr int n = m - (mf - lm);
-                constexpr int l = turn && n >= 0 ? (n + 1) * loads / lm - n * loads / lm : 0;
+        // MF MFMAs with R reads behind the first of them and L loads behind the others
+        const auto spread = [](auto rc, auto lc) __attribute__((always_inline)) {
+            constexpr int R = decltype(rc)::value, L = decltype(lc)::value, MF = T::RB * T::CB / 2;
+            constexpr int rm = L > 0 ? (MF + 1) / 2 : R < MF ? R : MF, lm = MF - rm > 0 ? MF - rm : 1;
+            static_for<0, MF>([&](auto mc) __attribute__((always_inline)) {
+                constexpr int m = decltype(mc)::value, n = m - (MF - lm);
+                constexpr int r = m < rm ? (m + 1) * R / rm - m * R / rm : 0;
+                constexpr int l = n >= 0 ? (n + 1) * L / lm - n * L / lm : 0;
                 __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
                 if constexpr (r > 0) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, r, 0);
                 if constexpr (l > 0) __builtin_amdgcn_sched_group_barrier(kSchedVmemRead, l, 0);
             });
-        });
+        };
+        constexpr int HALF = T::CB / 2;
+        static_assert(T::CB % 2 == 0 && T::STEPS == 2, "halves of two steps");
+        read_b(st, Zero{}, One{});
+        multiply(Zero{}, Zero{});
+        spread(std::integral_constant<int, HALF>{}, Zero{});
+        read_a(st, One{});
+        read_b(st, One{}, Zero{});
+        multiply(Zero{}, One{});
+        spread(std::integral_constant<int, T::RB + HALF>{}, Zero{});
+        read_b(st, One{}, One{});
+        multiply(One{}, Zero{});
+        spread(std::integral_constant<int, HALF>{}, Zero{});
+        __builtin_amdgcn_sched_barrier(0);
+        wait_vmcnt<UNDER_WAY>();
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        read_a(next, Zero{});
+        read_b(next, Zero{}, Zero{});
+        if constexpr (ODD) {
+            entry = entry + 1 == T::SRING ? 0 : entry + 1;
+            read_scales(entry);
+        } else {
+            issue_scales(panel + T::NSTG - behind);
+        }
+        issue(panel + T::NSTG - behind, st);
+        multiply(One{}, One{});
+        spread(std::integral_constant<int, T::RB + HALF + (ODD ? FOURS : 0)>{},
+               std::integral_constant<int, LPP + (ODD ? 0 : T::SCH)>{});
         // (behind a tile's last panel comes the first of the next: its scales are whole or masked alike)
         if constexpr (ODD) take_scales(panel + 1 == panels ? 0 : panel + 1, Even{});
         else take_scales(panel + 1, Odd{});
@@ -342,7 +377,7 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
 #pragma unroll
             for (int i = 0; i < T::RB; ++i)
 #pragma unroll
-                for (int j = 0; j < T::CB; ++j) acc[i][j] = f32x16(0.0f);
+                for (int j = 0; j < T::CB; ++j) acc[i][j] = f32x4(0.0f);
         }
     }
 }
