@@ -1028,7 +1028,7 @@ def reorder_beams(states, beams, out=None):
     and value caches, also views of their first positions; tokens so far), beams (B, W) int64 or
     int32; an index outside 0 to W - 1 stands for w itself. All are moved in one launch.
 
-    Results are new tensors, or written to out: tensors of the same shapes and types, for which
+    Results are new tensors (small ones, 64 MiB in all, may share an allocation), or written to out: tensors of the same shapes and types, for which
     out=states reorders in place and leaves rows that stay alone. An out must not overlap itself or
     another state. No gradient flows through it."""
     done = (_calls or _load_calls()).reorder_beams(states, beams, out)

@@ -17,28 +17,30 @@ namespace sgemm {
 namespace {
 
 constexpr int64_t kMaxLd = 8388608;         // 256 rows stay below 2^31 bytes
+constexpr int kMaxRows = 1 << 27;           // 16 bytes of each stay below 2^31
 constexpr int kWaves = 8;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 unsigned element_blocks(int64_t total) { return unsigned(std::min<int64_t>((total + 255) / 256, 16384)); }
 
-// Rows in parts whose units one launch holds (and a division takes).
-template <typename Kernel, typename Elements>
-int by_rows(Kernel kern, int M, int K, Elements *X, int size, int64_t ldx, const uint8_t *Q, int64_t ldq,
-            const uint8_t *scales, int64_t lds, void *stream)
+// Rows in parts whose units one launch holds (and a division takes); `each` units to a thread.
+typedef void (*Mx4RowKernel)(Mx4RowArgs);
+int by_rows(Mx4RowKernel kern, int each, int M, int K, const void *X, int size, int64_t ldx, const uint8_t *Q,
+            int64_t ldq, const uint8_t *scales, int64_t lds, void *stream)
 {
     Mx4RowArgs p{};
     p.ldx = ldx; p.ldq = ldq; p.lds = lds; p.K = K;
     p.units = int(4 * ceil_div(K, 32));
     p.by_units = divisor(uint32_t(p.units));
-    const int64_t most = std::max<int64_t>(1, ((int64_t(1) << 31) - 256) / p.units);
+    const int64_t most = std::max<int64_t>(1, ((int64_t(1) << 31) - 256 * each) / p.units);
     for (int64_t r = 0; r < M; r += most) {
         p.M = int(std::min<int64_t>(most, M - r));
-        p.X = static_cast<const char *>(static_cast<const void *>(X)) + r * ldx * size;
+        p.X = static_cast<const char *>(X) + r * ldx * size;
         p.Q = const_cast<uint8_t *>(Q) + r * ldq;
         p.scales = const_cast<uint8_t *>(scales) + r * lds;
-        const int st = launch(kern, dim3(unsigned(ceil_div(int64_t(p.M) * p.units, 256))), dim3(256), stream, p);
+        const int64_t groups = ceil_div(int64_t(p.M) * p.units, 256 * each);
+        const int st = launch(kern, dim3(unsigned(groups)), dim3(256), stream, p);
         if (st != SGEMM_OK) return st;
     }
     return SGEMM_OK;
@@ -48,36 +50,38 @@ typedef void (*Mx4Kernel)(Mx4Args);
 
 // The tiles, smallest first. In microseconds: `c1` and `c2` are a panel of 256 elements with one and two
 // workgroups on every compute unit, `ends` a workgroup's start and stores, `next` what each further
-// tile of a workgroup that goes on adds to its panels.
+// tile of a workgroup that goes on adds to its panels, `less` what a panel takes less with arranged
+// scales. They and the constants of make_plan were fitted to the times of every tile and split
+// of 870 products drawn over M of 17 to 12000 and N, K of 64 to 16384 (and N of 32001 and 50001): the plan's
+// choice costs 1.1 % more than the best of each on average (1.1 % on those left out of the fit). Tiles of
+// 128 x 256 and 192 x 256 and a ring of four panels of 128 x 128 would save less than 0.2 % and are not here.
 struct Mx4Variant {
     const char *name;
     Mx4Kernel kernel;
     int bm, bn, threads;
     int at_once;     // workgroups on a compute unit
     int loop;        // panels from which a workgroup goes on to another tile, or 0
-    double c1, c2, ends, next;
+    double c1, c2, ends, next, less;
 };
 template <int BM, int BN, int WGM, int WGN, int NSTG>
-constexpr Mx4Variant tile(const char *name, double c1, double c2, double ends, double next)
+constexpr Mx4Variant tile(const char *name, double c1, double c2, double ends, double next, double less)
 {
     typedef Mx4Tile<BM, BN, WGM, WGN, NSTG> T;
-    return {name, &k_mx4_tiles<T>, BM, BN, T::NT, T::LOOP ? 1 : 2, T::LOOP ? NSTG : 0, c1, c2, ends, next};
+    return {name, &k_mx4_tiles<T>, BM, BN, T::NT, T::LOOP ? 1 : 2, T::LOOP ? NSTG : 0, c1, c2, ends, next, less};
 }
 const Mx4Variant kTiles[] = {
-    tile<64, 32, 2, 1, 6>("mx4_64x32", 0.189, 0.27, 2.31, 0.0),
-    tile<64, 64, 2, 2, 4>("mx4_64x64", 0.200, 0.37, 1.84, 0.0),
-    tile<64, 128, 2, 4, 2>("mx4_64x128", 0.298, 0.52, 2.17, 0.0),
-    tile<128, 128, 4, 2, 2>("mx4_128x128", 0.506, 0.95, 1.19, 0.0),
-    tile<128, 256, 2, 4, 2>("mx4_128x256", 0.644, 0.0, 2.83, 7.49),
-    tile<192, 256, 2, 4, 2>("mx4_192x256", 0.962, 0.0, 3.46, 8.19),
-    tile<256, 256, 4, 2, 2>("mx4_256x256", 1.125, 0.0, 2.20, 7.80),
+    tile<64, 32, 2, 1, 6>("mx4_64x32", 0.258, 0.34, 1.12, 0.0, 0.0),
+    tile<64, 64, 2, 2, 4>("mx4_64x64", 0.263, 0.43, 1.65, 0.0, 0.0),
+    tile<64, 128, 2, 4, 2>("mx4_64x128", 0.501, 0.73, 0.16, 0.0, 0.0),
+    tile<128, 128, 4, 2, 2>("mx4_128x128", 0.645, 0.90, 0.0, 0.0, 0.05),
+    tile<256, 256, 4, 2, 2>("mx4_256x256", 1.626, 0.0, 3.14, 3.75, 0.08),
 };
 // Few rows: 16 rows and columns, turns of 512 elements to a wave.
-const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves, 1>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0};
+const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves, 1>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0, 0.0};
 // For more columns than run at once and a K of a turn to a wave: two and one to a compute unit, which go on.
 const Mx4Variant kRowsOn[] = {
-    {"mx4_rows16_on8", &k_mx4_rows_on<8>, 16, 16, 512, 2, 1, 0.0, 0.0, 0.0, 0.0},
-    {"mx4_rows16_on16", &k_mx4_rows_on<16>, 16, 16, 1024, 1, 1, 0.0, 0.0, 0.0, 0.0},
+    {"mx4_rows16_on8", &k_mx4_rows_on<8>, 16, 16, 512, 2, 1, 0.0, 0.0, 0.0, 0.0, 0.0},
+    {"mx4_rows16_on16", &k_mx4_rows_on<16>, 16, 16, 1024, 1, 1, 0.0, 0.0, 0.0, 0.0, 0.0},
 };
 
 // The operands, and which of them the tiles can load as they lie: rows on word boundaries, A's of
@@ -94,12 +98,12 @@ struct Mx4Operands {
 struct Mx4Plan {
     const Mx4Variant *v;
     int tiles_m, tiles_n, splits, chunk;
-    bool copy[4];
+    bool copy[4];             // A, B: into whole chunks; scales: arranged
     double cost;
 };
 
 constexpr double kLaunch = 2.5;          // us: a kernel's start and end
-constexpr double kStreamPerUs = 6.4e6;   // bytes of operands, from the last-level cache too
+constexpr double kFill = 6.7;            // panels that a workgroup's first one takes
 
 // Whether workgroups go on to another tile, as many as run at once.
 bool goes_on(const Mx4Variant &v, int64_t tiles, int splits, int64_t panels, int cus)
@@ -107,15 +111,16 @@ bool goes_on(const Mx4Variant &v, int64_t tiles, int splits, int64_t panels, int
     return splits == 1 && v.loop > 0 && panels >= v.loop && tiles > cus * v.at_once;
 }
 // Microseconds of workgroups of `panels` panels each: whole rounds of them and what is left.
-double tile_cost(const Mx4Variant &v, int64_t groups, int splits, int64_t panels, int cus)
+double tile_cost(const Mx4Variant &v, int64_t groups, int splits, int64_t panels, int cus, bool arranged)
 {
     const int64_t full = groups / (cus * v.at_once), rest = groups % (cus * v.at_once);
     const int64_t rounds = full + (rest > 0);
+    const double less = arranged ? v.less : 0.0, c1 = v.c1 - less;
     if (goes_on(v, groups, splits, panels, cus))
-        return v.c1 * (double(rounds * panels) + 2.7) + v.ends + double(rounds - 1) * v.next;
-    const double whole = v.at_once == 2 ? v.c2 : v.c1;
-    const double tail = rest == 0 ? 0.0 : rest <= cus ? v.c1 : v.c2;
-    return (double(full) * whole + tail) * (double(panels) + 2.7) + double(rounds) * v.ends;
+        return c1 * (double(rounds * panels) + kFill) + v.ends + double(rounds - 1) * v.next;
+    const double whole = v.at_once == 2 ? v.c2 - less : c1;
+    const double tail = rest == 0 ? 0.0 : rest <= cus ? c1 : v.c2 - less;
+    return (double(full) * whole + tail) * (double(panels) + kFill) + double(rounds) * v.ends;
 }
 
 // The cheapest of every tile, K whole or split. (The cost orders choices and is no time.)
@@ -132,7 +137,7 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
         return std::pair<int, int>(int(ceil_div(kb, chunk)), int(std::min<int64_t>(chunk, kb)));
     };
     const auto join_cost = [&](int splits) {
-        return splits == 1 ? 0.0 : 2.3 + double(splits + 1) * M * N * 4 / 1.9e6;
+        return splits == 1 ? 0.0 : 2.0 + double(splits + 1) * M * N * 4 / 1.9e6;
     };
     const int most = int(std::min<int64_t>(16, std::max<int64_t>(1, kb / 512)));
     if (M <= 16) {
@@ -151,21 +156,22 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
         }
         return best;
     }
-    bool copy[4];
-    double copied = 0.0;
-    for (int i = 0; i < 4; ++i) {
-        copy[i] = !x.ready(i, K);
-        if (copy[i]) copied += double(i % 2 == 0 ? M : N) * K / (i < 2 ? 2 : 32);
-    }
+    // operands off a word's boundary are copied, scales off it arranged; others are where it pays
+    const auto traffic = [&](int i) { return 2.0 * double(i % 2 == 0 ? M : N) * K / (i < 2 ? 2 : 32) / 5.0e6; };
+    const bool copy_a = !x.ready(0, K), copy_b = !x.ready(1, K), odd_sa = !x.ready(2, K), odd_sb = !x.ready(3, K);
+    const double copies = (copy_a || copy_b ? 3.5 : 0.0) + (copy_a ? traffic(0) : 0.0) + (copy_b ? traffic(1) : 0.0);
     for (const Mx4Variant &v : kTiles) {
         const int64_t tm = ceil_div(M, v.bm), tn = ceil_div(N, v.bn);
         for (int want = 1; want <= most; ++want) {
             const auto [s, chunk] = splits_of(want);
             if (s > 1 && tm * tn * s > 2 * int64_t(cus)) break;
-            const double work = tile_cost(v, tm * tn * s, s, ceil_div(chunk, 128), cus), reads = bytes / kStreamPerUs;
-            const double body = std::max(work, reads) + 0.02 * std::min(work, reads);   // reads alone tie
-            offer({&v, int(tm), int(tn), s, chunk, {copy[0], copy[1], copy[2], copy[3]},
-                   kLaunch + body + join_cost(s) + (copied > 0.0 ? 4.6 + 2.0 * copied / 6.8e6 : 0.0)});
+            for (const bool arrange : {false, true}) {
+                if (arrange && v.less == 0.0 && !odd_sa && !odd_sb) continue;
+                const bool sa = odd_sa || arrange, sb = odd_sb || arrange;
+                const double moves = (sa || sb ? 3.0 : 0.0) + (sa ? traffic(2) : 0.0) + (sb ? traffic(3) : 0.0);
+                offer({&v, int(tm), int(tn), s, chunk, {copy_a, copy_b, sa, sb},
+                       kLaunch + tile_cost(v, tm * tn * s, s, ceil_div(chunk, 128), cus, sa && sb) + join_cost(s) + copies + moves});
+            }
         }
     }
     return best;
@@ -190,7 +196,7 @@ Mx4Space space_of(const Mx4Plan &p, int M, int N, int K)
     s.bytes = p.splits > 1 ? round16(int64_t(p.splits) * M * N * 4) : 0;
     for (int i = 0; i < 4; ++i) {
         s.at[i] = s.bytes;
-        if (p.copy[i]) s.bytes += int64_t(i % 2 == 0 ? M : N) * round16(ceil_div(K, i < 2 ? 2 : 32));
+        if (p.copy[i]) s.bytes += int64_t(i % 2 == 0 ? M : N) * round16(ceil_div(K, i < 2 ? 2 : 32));   // (whole groups of scales, too)
     }
     return s;
 }
@@ -198,7 +204,7 @@ Mx4Space space_of(const Mx4Plan &p, int M, int N, int K)
 bool shape_in_limits(int M, int N, int64_t lda, int64_t lda_scales, int64_t ldb, int64_t ldb_scales)
 {
     return lda < kMaxLd && ldb < kMaxLd && lda_scales < kMaxLd && ldb_scales < kMaxLd &&
-           ceil_div(M, 16) * ceil_div(N, 16) < (int64_t(1) << 30);
+           M < kMaxRows && N < kMaxRows && ceil_div(M, 16) * ceil_div(N, 16) < (int64_t(1) << 30);
 }
 
 // Validation of the quantiser and its inverse; `writes` the packed rows and scales, or the values.
@@ -228,10 +234,13 @@ extern "C" int gemm_mx4_quantize(int M, int K, const void *X, int x_dtype, int64
     if (st != SGEMM_OK) return st;
     if (M == 0 || K == 0) return SGEMM_OK;
     const int size = dtype_bytes(x_dtype);
-    auto kern = x_dtype == SGEMM_DTYPE_F32    ? &k_mx4_quantize<SGEMM_DTYPE_F32>
-                : x_dtype == SGEMM_DTYPE_BF16 ? &k_mx4_quantize<SGEMM_DTYPE_BF16>
-                                              : &k_mx4_quantize<SGEMM_DTYPE_F16>;
-    return by_rows(kern, M, K, X, size, ldx, Q, ldq, scales, lds, stream);
+    // several units to a thread where there are plenty (8192 x 8192 bf16)
+    const bool many = int64_t(M) * ceil_div(K, 32) >= (1 << 18);
+    const Mx4RowKernel kern =
+        x_dtype == SGEMM_DTYPE_F32    ? (many ? &k_mx4_quantize<SGEMM_DTYPE_F32, 4> : &k_mx4_quantize<SGEMM_DTYPE_F32, 1>)
+        : x_dtype == SGEMM_DTYPE_BF16 ? (many ? &k_mx4_quantize<SGEMM_DTYPE_BF16, 4> : &k_mx4_quantize<SGEMM_DTYPE_BF16, 1>)
+                                      : (many ? &k_mx4_quantize<SGEMM_DTYPE_F16, 4> : &k_mx4_quantize<SGEMM_DTYPE_F16, 1>);
+    return by_rows(kern, many ? 4 : 1, M, K, X, size, ldx, Q, ldq, scales, lds, stream);
 }
 
 extern "C" int gemm_mx4_dequantize(int M, int K, const uint8_t *Q, int64_t ldq, const uint8_t *scales, int64_t lds,
@@ -241,10 +250,10 @@ extern "C" int gemm_mx4_dequantize(int M, int K, const uint8_t *Q, int64_t ldq, 
     if (st != SGEMM_OK) return st;
     if (M == 0 || K == 0) return SGEMM_OK;
     const int size = dtype_bytes(y_dtype);
-    auto kern = y_dtype == SGEMM_DTYPE_F32    ? &k_mx4_dequantize<SGEMM_DTYPE_F32>
-                : y_dtype == SGEMM_DTYPE_BF16 ? &k_mx4_dequantize<SGEMM_DTYPE_BF16>
-                                              : &k_mx4_dequantize<SGEMM_DTYPE_F16>;
-    return by_rows(kern, M, K, Y, size, ldy, Q, ldq, scales, lds, stream);
+    const Mx4RowKernel kern = y_dtype == SGEMM_DTYPE_F32    ? &k_mx4_dequantize<SGEMM_DTYPE_F32>
+                              : y_dtype == SGEMM_DTYPE_BF16 ? &k_mx4_dequantize<SGEMM_DTYPE_BF16>
+                                                            : &k_mx4_dequantize<SGEMM_DTYPE_F16>;
+    return by_rows(kern, 1, M, K, Y, size, ldy, Q, ldq, scales, lds, stream);
 }
 
 extern "C" size_t gemm_mx4_workspace_size(int M, int N, int K, const uint8_t *A, int64_t lda, const uint8_t *a_scales,
@@ -297,26 +306,39 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
     const Mx4Plan plan = make_plan(M, N, K, x, cus);
     const Mx4Space space = space_of(plan, M, N, K);
     if (workspace_bytes < size_t(space.bytes)) return SGEMM_EINVAL_ARG;
-    Mx4Copies copies{};
-    int copy_blocks = 0;
-    for (int i = 0; i < 4; ++i) {
-        if (!plan.copy[i]) continue;
-        const int rows = i % 2 == 0 ? M : N, bytes = i < 2 ? kb : blocks;
-        const int64_t ld16 = round16(bytes);
-        const int per = rows_to_copy(rows, ld16);
-        int8_t *to = static_cast<int8_t *>(workspace) + space.at[i];
-        copies.rows[i] = {reinterpret_cast<const int8_t *>(x.p[i]), to, x.ld[i], rows, per, int(ceil_div(rows, per))};
-        copies.bytes[i] = bytes;
-        copy_blocks += copies.rows[i].blocks;
-        x.p[i] = reinterpret_cast<const uint8_t *>(to);
-        x.ld[i] = ld16;
+    const auto place = [&](int i) { return static_cast<uint8_t *>(workspace) + space.at[i]; };
+    int64_t step[2] = {16, 16};                  // scales: of a row's groups, and of all of them
+    int64_t size[2] = {(M - 1) * lda_scales + blocks, (N - 1) * ldb_scales + blocks};
+    if (plan.copy[0] || plan.copy[1]) {
+        Rows16 rows[2] = {};
+        for (int i = 0; i < 2; ++i) {
+            if (!plan.copy[i]) continue;
+            const int count = i == 0 ? M : N, per = rows_to_copy(count, round16(kb));
+            rows[i] = {reinterpret_cast<const int8_t *>(x.p[i]), reinterpret_cast<int8_t *>(place(i)), x.ld[i], count, per,
+                       int(ceil_div(count, per))};
+            x.p[i] = place(i);
+            x.ld[i] = round16(kb);
+        }
+        st = launch(&k_mx4_align, dim3(unsigned(rows[0].blocks + rows[1].blocks)), dim3(256), stream, rows[0], rows[1], kb);
+        if (st != SGEMM_OK) return st;
     }
-    if (copy_blocks > 0) {
-        st = launch(&k_mx4_align, dim3(unsigned(copy_blocks)), dim3(256), stream, copies);
+    if (plan.copy[2] || plan.copy[3]) {
+        Mx4Scales s[2] = {};
+        const int across = int(ceil_div(blocks, 64));
+        for (int i = 0; i < 2; ++i) {
+            if (!plan.copy[i + 2]) continue;
+            const int count = i == 0 ? M : N;
+            s[i] = {x.p[i + 2], place(i + 2), x.ld[i + 2], count, int(ceil_div(count, 64)) * across, across};
+            x.p[i + 2] = place(i + 2);
+            x.ld[i + 2] = 16;
+            step[i] = int64_t(count) * 16;
+            size[i] = step[i] * ceil_div(blocks, 16);
+        }
+        st = launch(&k_mx4_arrange, dim3(unsigned(s[0].blocks + s[1].blocks)), dim3(256), stream, s[0], s[1], blocks);
         if (st != SGEMM_OK) return st;
     }
     p.lda = x.ld[0]; p.ldb = x.ld[1]; p.ldsa = x.ld[2]; p.ldsb = x.ld[3];
-    p.sa_step = p.sb_step = 16;
+    p.sa_step = int(step[0]); p.sb_step = int(step[1]);
     p.partial = static_cast<float *>(workspace);
     p.splits = plan.splits; p.chunk = plan.splits > 1 ? plan.chunk : kb;
     const Mx4Variant &v = *plan.v;
@@ -339,8 +361,8 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
             p.B = x.p[1] + n * p.ldb;
             p.sa = x.p[2] + m * p.ldsa;
             p.sb = x.p[3] + n * p.ldsb;
-            p.sa_bytes = (p.M - 1) * p.ldsa + blocks;
-            p.sb_bytes = (p.N - 1) * p.ldsb + blocks;
+            p.sa_bytes = size[0] - m * p.ldsa;       // to the end of all, so that no row of a part is cut
+            p.sb_bytes = size[1] - n * p.ldsb;
             p.bias = bias ? bias + n : nullptr;
             p.C = static_cast<char *>(C) + (m * ldc + n) * csize;
             p.stream = reinterpret_cast<uintptr_t>(p.C) % 64 == 0 && ldc * csize % 64 == 0;

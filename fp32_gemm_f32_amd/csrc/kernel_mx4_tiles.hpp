@@ -102,12 +102,12 @@ __device__ __forceinline__ void mx4_epilogue(const Mx4Args &p, const f32x4 (&acc
     else store(std::integral_constant<int, SGEMM_DTYPE_F32>{});
 }
 
-// c + a b with the scales' byte T on both sides
-template <int T> __device__ __forceinline__ f32x4 mx4_mfma(i32x4 a, i32x4 b, f32x4 c, int sa, int sb)
+// c + a b with the scales' bytes SA and SB
+template <int SA, int SB> __device__ __forceinline__ f32x4 mx4_mfma(i32x4 a, i32x4 b, f32x4 c, int sa, int sb)
 {
     const i32x8 ax = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
     const i32x8 bx = __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ax, bx, c, 4, 4, T, sa, T, sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ax, bx, c, 4, 4, SA, sa, SB, sb);
 }
 
 template <typename T>
@@ -134,8 +134,8 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     const int q = (tid % T::CPR) ^ a_swizzle<T::CPR>(prow);
     const uint32_t a_off = uint32_t(prow * p.lda) + q * 16, b_off = uint32_t(mx4_b_row<T>(prow) * p.ldb) + q * 16;
     int m0, n0;
-    const int8_t *At, *Bt, *St[T::SCH];
-    uint32_t a_size, b_size, s_size[T::SCH], s_off[T::SCH];
+    const int8_t *At, *Bt, *St[T::SCH], *s_end[T::SCH];
+    uint32_t a_size, b_size, s_off[T::SCH];
     int s_step[T::SCH];                              // from one pair of panels to the next
     auto aim = [&](int tile) __attribute__((always_inline)) {
         int tm, tn;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
             const int8_t *const from = reinterpret_cast<const int8_t *>(of_a ? p.sa : p.sb);
             s_step[i] = of_a ? p.sa_step : p.sb_step;
             St[i] = from + (of_a ? m0 : n0) * ld + int64_t(k0 / 256) * s_step[i];
-            s_size[i] = bytes_range(St[i], from + (of_a ? p.sa_bytes : p.sb_bytes));
+            s_end[i] = from + (of_a ? p.sa_bytes : p.sb_bytes);
             s_off[i] = s >= T::BM + T::BN ? kOob : uint32_t((of_a ? s : mx4_b_row<T>(s - T::BM)) * ld);
         }
     };
@@ -176,12 +176,14 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     // operand reads: row l % 16 of a block; chunk t + 2 (l / 16) at step t
     const int frow = lane & 15, fq = lane >> 4;
     const int fsw = a_swizzle<T::CPR>(frow);
-    const int a_base = (wm * T::WM + frow) * T::BK, b_base = T::A_BYTES + (wn * T::WN + frow) * T::BK;
+    // (what is the wave's is kept apart from what is the lane's: it needs no vector registers)
+    const int a_base = wm * T::WM * T::BK, b_base = T::A_BYTES + wn * T::WN * T::BK;
+    const int lane_at[T::STEPS] = {frow * T::BK + ((T::STEPS * fq) ^ fsw) * 16, frow * T::BK + ((1 + T::STEPS * fq) ^ fsw) * 16};
     i32x4 fa[T::STEPS][T::RB], fb[T::STEPS][T::CB];
     // scales: blocks of rows of A, then of B, in fours; the two halves of the four words are two panels'
     constexpr int BLOCKS = T::RB + T::CB, FOURS = (BLOCKS + 3) / 4;
     i32x4 four[FOURS];
-    uint32_t sc[4 * FOURS];                          // of the panel multiplied
+    uint32_t sc[2 * FOURS];                          // of the panel multiplied, two blocks to a word
     int s_at[FOURS];
 #pragma unroll
     for (int n = 0; n < FOURS; ++n) {
@@ -189,51 +191,49 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
         s_at[n] = ((block < T::RB ? wm * T::WM + 16 * block : T::BM + wn * T::WN + 16 * (block - T::RB)) + frow) * 16;
     }
     // A's operands of a step, and half of B's
-    auto read_a = [&](const char *st, auto tc) __attribute__((always_inline)) {
+    auto read_a = [&](int st, auto tc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value;
-        const int at = ((t + T::STEPS * fq) ^ fsw) * 16;
+        const char *const at = smem + ((st + a_base) + lane_at[t]);
 #pragma unroll
-        for (int i = 0; i < T::RB; ++i)
-            fa[t][i] = *reinterpret_cast<const i32x4 *>(st + a_base + at + i * 16 * T::BK);
+        for (int i = 0; i < T::RB; ++i) fa[t][i] = *reinterpret_cast<const i32x4 *>(at + i * 16 * T::BK);
     };
-    auto read_b = [&](const char *st, auto tc, auto hc) __attribute__((always_inline)) {
+    auto read_b = [&](int st, auto tc, auto hc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value, first = decltype(hc)::value * T::CB / 2;
-        const int at = ((t + T::STEPS * fq) ^ fsw) * 16;
+        const char *const at = smem + ((st + b_base) + lane_at[t]);
 #pragma unroll
-        for (int j = first; j < first + T::CB / 2; ++j)
-            fb[t][j] = *reinterpret_cast<const i32x4 *>(st + b_base + at + j * 16 * T::BK);
+        for (int j = first; j < first + T::CB / 2; ++j) fb[t][j] = *reinterpret_cast<const i32x4 *>(at + j * 16 * T::BK);
     };
     auto read_scales = [&](int entry) __attribute__((always_inline)) {
         const char *at = ring + entry * T::SBYTES;
 #pragma unroll
         for (int n = 0; n < FOURS; ++n) four[n] = *reinterpret_cast<const i32x4 *>(at + s_at[n]);
     };
-    // The scales of a panel, the even or odd one of the pair read last, byte t for step t. Group g of 16
-    // lanes holds block g's 8 and needs two of them of each block: 2 g and 2 g + 1. Exchanging the halves
-    // of the wave leaves blocks 0 and 1 in one word, 2 and 3 in another, each with the right word of
-    // a block in every other group; exchanging neighbouring groups spreads it to both.
+    // The scales of a panel, the even or odd one of the pair read last. Group g of 16 lanes holds block g's
+    // 8 and needs two of them of each block: 2 g and 2 g + 1. Exchanging the halves of the wave leaves
+    // blocks 0 and 1 in one word, 2 and 3 in another, each with the right word of a block in every
+    // other group; exchanging neighbouring groups spreads it to both, and of two blocks' words the
+    // right halves make one: bytes 0 and 1 for the first one's steps, 2 and 3 for the other's.
+    const uint32_t halves = fq & 1 ? 0x07060302u : 0x05040100u;
     auto take_scales = [&](int panel, auto odd) __attribute__((always_inline)) {
         constexpr int w = decltype(odd)::value ? 2 : 0;
-        const int left = blocks - 8 * panel - 2 * fq, shift = 16 * (fq & 1);
-        const uint32_t keep = left >= 2 ? 0xffffu : left == 1 ? 0xffu : 0u;
+        const int left = blocks - 8 * panel - 2 * fq;
+        const uint32_t keep = left >= 2 ? ~0u : left == 1 ? 0x00ff00ffu : 0u;
 #pragma unroll
         for (int n = 0; n < FOURS; ++n) {
-            const auto halves = __builtin_amdgcn_permlane32_swap(uint32_t(four[n][w]), uint32_t(four[n][w + 1]), false, false);
+            const auto two = __builtin_amdgcn_permlane32_swap(uint32_t(four[n][w]), uint32_t(four[n][w + 1]), false, false);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const auto both = __builtin_amdgcn_permlane16_swap(halves[h], halves[h], false, false);
-                sc[4 * n + 2 * h] = both[0] >> shift & keep;
-                sc[4 * n + 2 * h + 1] = both[1] >> shift & keep;
+                const auto both = __builtin_amdgcn_permlane16_swap(two[h], two[h], false, false);
+                sc[2 * n + h] = __builtin_amdgcn_perm(both[1], both[0], halves) & keep;
             }
         }
     };
     auto multiply = [&](auto tc, auto hc) __attribute__((always_inline)) {
         constexpr int t = decltype(tc)::value, first = decltype(hc)::value * T::CB / 2;
-#pragma unroll
-        for (int j = first; j < first + T::CB / 2; ++j)
-#pragma unroll
-            for (int i = 0; i < T::RB; ++i)
-                acc[i][j] = mx4_mfma<t>(fa[t][i], fb[t][j], acc[i][j], int(sc[i]), int(sc[T::RB + j]));
+        static_for<0, T::CB / 2 * T::RB>([&](auto mc) __attribute__((always_inline)) {
+            constexpr int i = decltype(mc)::value % T::RB, j = first + decltype(mc)::value / T::RB, b = T::RB + j;
+            acc[i][j] = mx4_mfma<t + 2 * (i % 2), t + 2 * (b % 2)>(fa[t][i], fb[t][j], acc[i][j], int(sc[i / 2]), int(sc[b / 2]));
+        });
     };
 
     // what is left of a resource k bytes on (saturated sizes lose k bytes that no tile reaches: see kMaxLd)
@@ -246,8 +246,8 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
         const uint32_t past = 8 * panel >= blocks ? kOob : 0u;
 #pragma unroll
         for (int i = 0; i < T::SCH; ++i) {
-            const int k = (panel >> 1) * s_step[i];
-            load16_lds(St[i] + k, rest(s_size[i], k), s_off[i] | past, to + (i * T::NT + wave * 64) * 16);
+            const int8_t *const at = St[i] + int64_t(panel >> 1) * s_step[i];
+            load16_lds(at, bytes_range(at, s_end[i]), s_off[i] | past, to + (i * T::NT + wave * 64) * 16);
         }
     };
     auto issue = [&](int panel, char *st) __attribute__((always_inline)) {
@@ -287,15 +287,15 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
     int entry = 0;                                   // the ring's entry of the pair read last
     read_scales(0);
     take_scales(0, Even{});
-    read_a(smem, Zero{});
-    read_b(smem, Zero{}, Zero{});
+    read_a(0, Zero{});
+    read_b(0, Zero{}, Zero{});
     int stage = 0;                                   // of the pair
     int behind = 0;                                  // panels between a panel read and that of its tile
     auto run = [&](int panel, auto odd) __attribute__((always_inline)) {
         constexpr bool ODD = decltype(odd)::value;
-        char *st = smem + (stage + (ODD ? 1 : 0)) * STAGE;
+        const int st = (stage + (ODD ? 1 : 0)) * STAGE;
         if constexpr (ODD) stage = stage + 2 == T::NSTG ? 0 : stage + 2;
-        char *next = ODD ? smem + stage * STAGE : st + STAGE;
+        const int next = ODD ? stage * STAGE : st + STAGE;
         // MF MFMAs with R reads behind the first of them and L loads behind the others
         const auto spread = [](auto rc, auto lc) __attribute__((always_inline)) {
             constexpr int R = decltype(rc)::value, L = decltype(lc)::value, MF = T::RB * T::CB / 2;
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(T::NT) void k_mx4_tiles(Mx4Args p)
         } else {
             issue_scales(panel + T::NSTG - behind);
         }
-        issue(panel + T::NSTG - behind, st);
+        issue(panel + T::NSTG - behind, smem + st);
         multiply(One{}, One{});
         spread(std::integral_constant<int, T::RB + HALF + (ODD ? FOURS : 0)>{},
                std::integral_constant<int, LPP + (ODD ? 0 : T::SCH)>{});

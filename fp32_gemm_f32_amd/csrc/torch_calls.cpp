@@ -492,6 +492,41 @@ bool state_of(const at::Tensor &src, const at::Tensor &dst, beam_state &s)
     return true;
 }
 
+// New tensors like the given ones. Small ones share an allocation (each of its own takes the host 0.5 us:
+// 18 of 4 rows 16 us in all, the GPU 7), large ones have their own.
+constexpr int64_t kShared = int64_t(64) << 20, kApart = 512;
+std::vector<at::Tensor> empty_like_all(const std::vector<at::Tensor> &like, const at::Device &device)
+{
+    const auto room = [](const at::Tensor &t) {
+        return (t.numel() * int64_t(t.element_size()) + kApart - 1) / kApart * kApart;
+    };
+    int64_t all = 0;
+    for (const at::Tensor &t : like) all += room(t);
+    std::vector<at::Tensor> out;
+    out.reserve(like.size());
+    if (all > kShared || like.size() < 2) {
+        for (const at::Tensor &t : like) out.push_back(empty(t.sizes(), t.scalar_type(), device));
+        return out;
+    }
+    const at::Tensor space = empty({all}, at::kByte, device);
+    int64_t at_byte = 0;
+    c10::SmallVector<int64_t, 8> strides;
+    for (const at::Tensor &t : like) {
+        strides.resize(size_t(t.dim()));
+        int64_t step = 1;
+        for (int64_t d = t.dim() - 1; d >= 0; --d) {
+            strides[size_t(d)] = step;
+            step *= std::max<int64_t>(t.size(d), 1);
+        }
+        at::Tensor o = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(space.storage()), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                                t.dtype());
+        o.unsafeGetTensorImpl()->set_sizes_and_strides(t.sizes(), strides, at_byte / int64_t(t.element_size()));
+        out.push_back(std::move(o));
+        at_byte += room(t);
+    }
+    return out;
+}
+
 // reorder_beams(states, beams, out or None) -> out, or None: sequences of tensors only
 PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -532,8 +567,8 @@ PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
     {
         pybind11::gil_scoped_release release;
         const Place place(device);
+        if (!given) dst = empty_like_all(src, device);
         for (Py_ssize_t i = 0; i < count; ++i) {
-            if (!given) dst.push_back(empty(src[i].sizes(), src[i].scalar_type(), device));
             beam_state s;
             if (src[i].numel() == 0) continue;
             if (!state_of(src[i], dst[i], s)) { fits = false; break; }

@@ -61,11 +61,12 @@ int gemm_mx4_dequantize(int M, int K,
  * N floats. Repeated calls with the same arguments give the same bits; another plan (other shapes
  * or alignments) may sum in another order.
  *
- * Limits: leading dimensions of A, B and their scales below 8388608, fewer than 2^30 blocks of 16 x
- * 16 in C, else SGEMM_ETOO_LARGE.
+ * Limits: M and N below 2^27, leading dimensions of A, B and their scales below 8388608, fewer than
+ * 2^30 blocks of 16 x 16 in C, else SGEMM_ETOO_LARGE.
  *
  * workspace: products with few tiles split K over workgroups and join the partial sums there with a
- * second kernel; operands off a word's boundary are copied there first. Caller-owned device memory
+ * second kernel; operands off a word's boundary are copied there first, and so are a large product's
+ * scales, in another order. Caller-owned device memory
  * of gemm_mx4_workspace_size bytes, 16-byte aligned, SGEMM_EINVAL_ARG if smaller (where that is 0,
  * NULL with 0 bytes). It must not overlap the operands or C. No initialisation needed, contents
  * unspecified on return; calls that share one must not overlap in time.

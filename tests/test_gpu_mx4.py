@@ -327,3 +327,18 @@ def test_repeated_calls_give_the_same_bits(torch, M, N, K):
     want = g.matmul_mx4(a, sa, b, sb)
     for _ in range(3):
         assert torch.equal(g.matmul_mx4(a, sa, b, sb), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(4096, 4096, 8192), (4000, 3900, 12320)])
+def test_large_products_with_scales_in_another_order(torch, M, N, K):
+    """Shapes whose scales the plan puts in another order first, whole pairs of panels and in part."""
+    d = g.gemm_mx4_plan_describe(M, N, K)
+    assert d["workspace_bytes"] >= (M + N) * (K // 32), d
+    torch.manual_seed(M)
+    (a, sa), (b, sb) = ((torch.randint(0, 256, (r, K // 2), dtype=torch.uint8, device="cuda"),
+                         torch.randint(126, 129, (r, K // 32), dtype=torch.uint8, device="cuda")) for r in (M, N))
+    C = g.matmul_mx4(a, sa, b, sb)
+    va, vb = (g.dequantize_mx4(q, s).double() for q, s in ((a, sa), (b, sb)))
+    want = va @ vb.t().contiguous()
+    bound = (K / 32) * 2.0 ** -23 * (va.abs() @ vb.abs().t().contiguous())       # a rounding to a block
+    assert ((C.double() - want).abs() <= bound).all()
