@@ -159,7 +159,7 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
     // operands off a word's boundary are copied, scales off it arranged; others are where it pays
     const auto traffic = [&](int i) { return 2.0 * double(i % 2 == 0 ? M : N) * K / (i < 2 ? 2 : 32) / 5.0e6; };
     const bool copy_a = !x.ready(0, K), copy_b = !x.ready(1, K), odd_sa = !x.ready(2, K), odd_sb = !x.ready(3, K);
-    const double copies = (copy_a || copy_b ? 3.5 : 0.0) + (copy_a ? traffic(0) : 0.0) + (copy_b ? traffic(1) : 0.0);
+    const double copies = (copy_a ? traffic(0) : 0.0) + (copy_b ? traffic(1) : 0.0);
     for (const Mx4Variant &v : kTiles) {
         const int64_t tm = ceil_div(M, v.bm), tn = ceil_div(N, v.bn);
         for (int want = 1; want <= most; ++want) {
@@ -168,7 +168,7 @@ Mx4Plan make_plan(int M, int N, int K, const Mx4Operands &x, int cus)
             for (const bool arrange : {false, true}) {
                 if (arrange && v.less == 0.0 && !odd_sa && !odd_sb) continue;
                 const bool sa = odd_sa || arrange, sb = odd_sb || arrange;
-                const double moves = (sa || sb ? 3.0 : 0.0) + (sa ? traffic(2) : 0.0) + (sb ? traffic(3) : 0.0);
+                const double moves = (sa || sb || copies > 0.0 ? 3.0 : 0.0) + (sa ? traffic(2) : 0.0) + (sb ? traffic(3) : 0.0);
                 offer({&v, int(tm), int(tn), s, chunk, {copy_a, copy_b, sa, sb},
                        kLaunch + tile_cost(v, tm * tn * s, s, ceil_div(chunk, 128), cus, sa && sb) + join_cost(s) + copies + moves});
             }
@@ -309,32 +309,32 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
     const auto place = [&](int i) { return static_cast<uint8_t *>(workspace) + space.at[i]; };
     int64_t step[2] = {16, 16};                  // scales: of a row's groups, and of all of them
     int64_t size[2] = {(M - 1) * lda_scales + blocks, (N - 1) * ldb_scales + blocks};
-    if (plan.copy[0] || plan.copy[1]) {
-        Rows16 rows[2] = {};
-        for (int i = 0; i < 2; ++i) {
-            if (!plan.copy[i]) continue;
-            const int count = i == 0 ? M : N, per = rows_to_copy(count, round16(kb));
-            rows[i] = {reinterpret_cast<const int8_t *>(x.p[i]), reinterpret_cast<int8_t *>(place(i)), x.ld[i], count, per,
-                       int(ceil_div(count, per))};
+    Mx4Place placed{};
+    placed.bytes = kb;
+    placed.count = blocks;
+    int64_t places = 0;
+    for (int i = 0; i < 2; ++i) {
+        const int count = i == 0 ? M : N;
+        if (plan.copy[i]) {
+            const int per = rows_to_copy(count, round16(kb));
+            placed.rows[i] = {reinterpret_cast<const int8_t *>(x.p[i]), reinterpret_cast<int8_t *>(place(i)), x.ld[i], count,
+                              per, int(ceil_div(count, per))};
+            places += placed.rows[i].blocks;
             x.p[i] = place(i);
             x.ld[i] = round16(kb);
         }
-        st = launch(&k_mx4_align, dim3(unsigned(rows[0].blocks + rows[1].blocks)), dim3(256), stream, rows[0], rows[1], kb);
-        if (st != SGEMM_OK) return st;
-    }
-    if (plan.copy[2] || plan.copy[3]) {
-        Mx4Scales s[2] = {};
-        const int across = int(ceil_div(blocks, 64));
-        for (int i = 0; i < 2; ++i) {
-            if (!plan.copy[i + 2]) continue;
-            const int count = i == 0 ? M : N;
-            s[i] = {x.p[i + 2], place(i + 2), x.ld[i + 2], count, int(ceil_div(count, 64)) * across, across};
+        if (plan.copy[i + 2]) {
+            const int across = int(ceil_div(blocks, 64));
+            placed.scales[i] = {x.p[i + 2], place(i + 2), x.ld[i + 2], count, int(ceil_div(count, 64)) * across, across};
+            places += placed.scales[i].blocks;
             x.p[i + 2] = place(i + 2);
             x.ld[i + 2] = 16;
             step[i] = int64_t(count) * 16;
             size[i] = step[i] * ceil_div(blocks, 16);
         }
-        st = launch(&k_mx4_arrange, dim3(unsigned(s[0].blocks + s[1].blocks)), dim3(256), stream, s[0], s[1], blocks);
+    }
+    if (places > 0) {
+        st = launch(&k_mx4_place, dim3(unsigned(places)), dim3(256), stream, placed);
         if (st != SGEMM_OK) return st;
     }
     p.lda = x.ld[0]; p.ldb = x.ld[1]; p.ldsa = x.ld[2]; p.ldsb = x.ld[3];

@@ -210,15 +210,10 @@ __global__ __launch_bounds__(256) void k_mx4_join(Mx4Args p)
     }
 }
 
-// Rows put in place first, of A in the first blocks and of B in the others.
-__global__ __launch_bounds__(256) void k_mx4_align(Rows16 a, Rows16 b, int K)
-{
-    const bool of_a = int(blockIdx.x) < a.blocks;
-    put_rows_in_place(of_a ? a : b, blockIdx.x - (of_a ? 0 : a.blocks), K);
-}
-
-// Scales in another order: 16 of a row (a group, two panels' worth) at (group rows + row) 16, zeros behind
-// the last. A wave takes 16 rows and four groups: it reads 64 bytes of each row and writes four times 256.
+// What is put in place first, in one launch, for a launch of its own costs 2.5 us: rows of A and of B in
+// whole chunks, and scales in another order, 16 of a row (a group, two panels' worth) at (group rows + row)
+// 16 with zeros behind the last. Of those a wave takes 16 rows and four groups: it reads 64 bytes of
+// each row and writes four times 256.
 struct Mx4Scales {
     const uint8_t *src;
     uint8_t *dst;
@@ -226,17 +221,34 @@ struct Mx4Scales {
     int rows, blocks;          // workgroups, 64 rows and four groups each
     int across;                // of them to 64 rows
 };
-__global__ __launch_bounds__(256) void k_mx4_arrange(Mx4Scales a, Mx4Scales b, int scales)
+struct Mx4Place {
+    Rows16 rows[2];
+    Mx4Scales scales[2];
+    int bytes, count;          // of a row's elements; scales to a row
+};
+__device__ inline void mx4_arrange(const Mx4Scales &p, int block, int scales)
 {
-    const bool of_a = int(blockIdx.x) < a.blocks;
-    const Mx4Scales &p = of_a ? a : b;
-    const int block = blockIdx.x - (of_a ? 0 : a.blocks), down = block / p.across;
+    const int down = block / p.across;
     const int row = down * 64 + int(threadIdx.x >> 6) * 16 + int(threadIdx.x & 15);
     const int group = (block - down * p.across) * 4 + int(threadIdx.x >> 4 & 3);
     if (row >= p.rows || group * 16 >= scales) return;
     const uint8_t *from = p.src + row * p.ld;
     const i32x4 v = group * 16 + 16 <= scales ? mx4_load16(from + group * 16) : mx4_load_tail(from, group * 16, scales);
     *reinterpret_cast<i32x4 *>(p.dst + (int64_t(group) * p.rows + row) * 16) = v;
+}
+__global__ __launch_bounds__(256) void k_mx4_place(Mx4Place p)
+{
+    int block = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (block >= 0 && block < p.rows[i].blocks) put_rows_in_place(p.rows[i], block, p.bytes);
+        block -= p.rows[i].blocks;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (block >= 0 && block < p.scales[i].blocks) mx4_arrange(p.scales[i], block, p.count);
+        block -= p.scales[i].blocks;
+    }
 }
 
 // K == 0: the empty sum plus the bias.

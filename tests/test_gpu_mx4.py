@@ -329,7 +329,7 @@ def test_repeated_calls_give_the_same_bits(torch, M, N, K):
         assert torch.equal(g.matmul_mx4(a, sa, b, sb), want)
 
 
-@pytest.mark.parametrize("M,N,K", [(4096, 4096, 8192), (4000, 3900, 12320)])
+@pytest.mark.parametrize("M,N,K", [(4096, 8192, 16384), (4000, 7900, 14368)])
 def test_large_products_with_scales_in_another_order(torch, M, N, K):
     """Shapes whose scales the plan puts in another order first, whole pairs of panels and in part."""
     d = g.gemm_mx4_plan_describe(M, N, K)
