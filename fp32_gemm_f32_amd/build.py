@@ -15,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -62,23 +63,24 @@ def flags(vgpr_form: bool = True) -> list[str]:
 def build(asm: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     report = os.path.join(BUILD_DIR, "resource_usage.txt")
-    objs, log = [], []
-    for src, vgpr_form in SOURCES:
-        obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-        cmd = [hipcc(), *flags(vgpr_form), "-c", src, "-o", obj,
-               "-Rpass-analysis=kernel-resource-usage"]
+    objs = [os.path.join(BUILD_DIR, os.path.basename(src) + ".o") for src, _ in SOURCES]
+
+    def compile_unit(unit):
+        (src, vgpr_form), obj = unit
+        cmd = [hipcc(), *flags(vgpr_form), "-c", src, "-o", obj, "-Rpass-analysis=kernel-resource-usage"]
         if verbose:
             print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        log.append(r.stderr)
+        return subprocess.run(cmd, capture_output=True, text=True)
+
+    # the units side by side: the largest takes most of the time
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+        done = list(pool.map(compile_unit, zip(SOURCES, objs)))
+    with open(report, "w") as f:
+        f.write("".join(r.stderr for r in done))
+    for (src, _), r in zip(SOURCES, done):
         if r.returncode != 0:
-            with open(report, "w") as f:
-                f.write("".join(log))
             sys.stderr.write(r.stderr[-8000:])
             raise RuntimeError(f"hipcc failed ({r.returncode}) on {src}; see {report}")
-        objs.append(obj)
-    with open(report, "w") as f:
-        f.write("".join(log))
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-fPIC", "-shared", *objs, "-o", OUT + ".tmp"]
     if verbose:
         print(" ".join(cmd), flush=True)

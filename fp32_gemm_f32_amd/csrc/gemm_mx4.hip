@@ -185,6 +185,13 @@ int rows_to_copy(int rows, int64_t ld16)
     return int(std::max<int64_t>(1, chunks / (ld16 / 16)));
 }
 
+// Workgroups of the plan's launch.
+int64_t groups_of(const Mx4Plan &p, int kb, int cus)
+{
+    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n;
+    return goes_on(*p.v, tiles, p.splits, ceil_div(kb, 128), cus) ? int64_t(cus) * p.v->at_once : tiles * p.splits;
+}
+
 // Workspace: the splits' sums, then the copies.
 struct Mx4Space {
     int64_t at[4], bytes;     // offsets of the copies, the whole
@@ -304,6 +311,7 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
     if (st != SGEMM_OK) return st;
     Mx4Operands x = {{A, B, a_scales, b_scales}, {lda, ldb, lda_scales, ldb_scales}};
     const Mx4Plan plan = make_plan(M, N, K, x, cus);
+    if (groups_of(plan, kb, cus) > most_groups(plan.v->threads)) return SGEMM_ETOO_LARGE;
     const Mx4Space space = space_of(plan, M, N, K);
     if (workspace_bytes < size_t(space.bytes)) return SGEMM_EINVAL_ARG;
     const auto place = [&](int i) { return static_cast<uint8_t *>(workspace) + space.at[i]; };
@@ -342,37 +350,15 @@ extern "C" int gemm_mx4(int M, int N, int K, const uint8_t *A, int64_t lda, cons
     p.partial = static_cast<float *>(workspace);
     p.splits = plan.splits; p.chunk = plan.splits > 1 ? plan.chunk : kb;
     const Mx4Variant &v = *plan.v;
-    const bool loops = goes_on(v, int64_t(plan.tiles_m) * plan.tiles_n, plan.splits, ceil_div(kb, 128), cus);
-    // C in parts that one launch each may take, almost always one: no more workgroups than
-    // most_groups, rows and columns that a tile past the last of 2^31 - 1 would carry out of an int
-    // (split products are one part: make_plan gives them few tiles)
-    const int64_t most = loops ? INT64_MAX : most_groups(v.threads), most_rows = int64_t(1) << 30;
-    const int64_t part_m = std::min({int64_t(plan.tiles_m), most, most_rows / v.bm});
-    const int64_t part_n = std::min({int64_t(plan.tiles_n), most / part_m, most_rows / v.bn});
-    const int csize = dtype_bytes(c_dtype);
-    for (int64_t tm = 0; tm < plan.tiles_m; tm += part_m)
-        for (int64_t tn = 0; tn < plan.tiles_n; tn += part_n) {
-            const int64_t m = tm * v.bm, n = tn * v.bn;
-            p.tiles_m = int(std::min(part_m, plan.tiles_m - tm));
-            p.tiles_n = int(std::min(part_n, plan.tiles_n - tn));
-            p.M = int(std::min<int64_t>(M - m, part_m * v.bm));
-            p.N = int(std::min<int64_t>(N - n, part_n * v.bn));
-            p.A = x.p[0] + m * p.lda;
-            p.B = x.p[1] + n * p.ldb;
-            p.sa = x.p[2] + m * p.ldsa;
-            p.sb = x.p[3] + n * p.ldsb;
-            p.sa_bytes = size[0] - m * p.ldsa;       // to the end of all, so that no row of a part is cut
-            p.sb_bytes = size[1] - n * p.ldsb;
-            p.bias = bias ? bias + n : nullptr;
-            p.C = static_cast<char *>(C) + (m * ldc + n) * csize;
-            p.stream = reinterpret_cast<uintptr_t>(p.C) % 64 == 0 && ldc * csize % 64 == 0;
-            const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
-            p.group_mul = d.mul; p.group_shift = d.shift;
-            int64_t groups = int64_t(p.tiles_m) * p.tiles_n * plan.splits;
-            if (loops) groups = std::min<int64_t>(groups, int64_t(cus) * v.at_once);
-            st = launch(v.kernel, dim3(unsigned(groups)), dim3(v.threads), stream, p);
-            if (st != SGEMM_OK) return st;
-        }
+    p.tiles_m = plan.tiles_m; p.tiles_n = plan.tiles_n;
+    p.sa_bytes = size[0]; p.sb_bytes = size[1];
+    p.A = x.p[0]; p.B = x.p[1]; p.sa = x.p[2]; p.sb = x.p[3];
+    // (as the 8-bit product stores C)
+    p.stream = reinterpret_cast<uintptr_t>(C) % 64 == 0 && ldc * dtype_bytes(c_dtype) % 64 == 0;
+    const Divisor d = divisor(uint32_t(kGroupM) * uint32_t(p.tiles_n));
+    p.group_mul = d.mul; p.group_shift = d.shift;
+    st = launch(v.kernel, dim3(unsigned(groups_of(plan, kb, cus))), dim3(v.threads), stream, p);
+    if (st != SGEMM_OK) return st;
     if (plan.splits == 1) return SGEMM_OK;
     return launch(&k_mx4_join, dim3(element_blocks(int64_t(M) * N)), dim3(256), stream, p);
 }

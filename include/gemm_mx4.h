@@ -62,7 +62,8 @@ int gemm_mx4_dequantize(int M, int K,
  * or alignments) may sum in another order.
  *
  * Limits: M and N below 2^27, leading dimensions of A, B and their scales below 8388608, fewer than
- * 2^30 blocks of 16 x 16 in C, else SGEMM_ETOO_LARGE.
+ * 2^30 blocks of 16 x 16 in C, and a C that one launch's workgroups cover (any of up to 2^35
+ * elements), else SGEMM_ETOO_LARGE.
  *
  * workspace: products with few tiles split K over workgroups and join the partial sums there with a
  * second kernel; operands off a word's boundary are copied there first, and so are a large product's
