@@ -823,6 +823,14 @@ def _padded(rows: int, cols: int, device):
     return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
 
 
+def _int_sizes(*sizes):
+    """Sizes that the C ABI takes, which counts rows and columns in 32 bits."""
+    for n in sizes:
+        if n > 0x7fffffff:
+            raise ValueError(f"at most 2147483647 rows and columns, not {n}")
+    return sizes
+
+
 def quantize_mx4(X, out=None, scales=None):
     """(Q, scales): X (M, K) in microscaled 4-bit floating point (E2M1 elements, a power of two for each
     32 of a row). Q is (M, ceil(K / 2)) uint8, element 2 i of a row in the low half of byte i; scales
@@ -838,7 +846,7 @@ def quantize_mx4(X, out=None, scales=None):
 
     code = _dtype_code(X.dtype)
     X = _rows(X.detach(), "X")
-    M, K = X.shape
+    M, K = _int_sizes(*X.shape)
     row, blocks = (K + 1) // 2, (K + 31) // 32
     out = _padded(M, row, X.device) if out is None else _out(out, (M, row), torch.uint8, X.device, "out")
     scales = (_padded(M, blocks, X.device) if scales is None
@@ -871,7 +879,7 @@ def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
 
     if out is None:
         done = (_calls or _load_calls()).dequantize_mx4(Q, scales, 0 if dtype is None else _dtype_code(dtype),
-                                                        -1 if columns is None else columns)
+                                                        columns)
         if done is not None:
             return done
     Q, scales = _packed_rows(Q, scales, "Q")
@@ -880,6 +888,7 @@ def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
         columns = 2 * R
     if (columns + 1) // 2 != R or columns < 0:
         raise ValueError(f"rows of {R} bytes hold {2 * R} or {2 * R - 1} columns, not {columns}")
+    _int_sizes(M, columns)
     if dtype is None:
         dtype = torch.float32 if out is None else out.dtype
     code = _dtype_code(dtype)
@@ -911,6 +920,7 @@ def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
     N, R2 = B.shape
     if R != R2:
         raise ValueError(f"rows of A and B differ in length: {R} vs {R2} bytes")
+    _int_sizes(M, N, 2 * R)
     if out_dtype is None:
         out_dtype = torch.float32 if out is None else out.dtype
     code = _dtype_code(out_dtype)
@@ -962,7 +972,7 @@ def beam_step(logits, scores, top=None, finished=None, pad_token: int = 0) -> Be
     and pad_token. Continuations of probability 0 (logits or scores of -infinity) and of rows that
     hold a NaN or +infinity do not count. Of equal totals the lower beam comes first, of a beam's equal
     logits the lower token. No gradient flows through it."""
-    done = (_calls or _load_calls()).beam_step(logits, scores, -1 if top is None else top, finished, pad_token)
+    done = (_calls or _load_calls()).beam_step(logits, scores, top, finished, pad_token)
     if done is not None:
         return BeamStep(*done)
     import torch
@@ -976,6 +986,7 @@ def beam_step(logits, scores, top=None, finished=None, pad_token: int = 0) -> Be
     if logits.shape[0] != B * W:
         raise ValueError(f"logits must have {B * W} rows, one for each beam, got {logits.shape[0]}")
     V = logits.shape[1]
+    _int_sizes(B, V)
     top = W if top is None else top
     if scores.dtype != torch.float32:
         raise TypeError(f"scores must be float32, got {scores.dtype}")
@@ -1028,9 +1039,9 @@ def reorder_beams(states, beams, out=None):
     and value caches, also views of their first positions; tokens so far), beams (B, W) int64 or
     int32; an index outside 0 to W - 1 stands for w itself. All are moved in one launch.
 
-    Results are new tensors (small ones, 64 MiB in all, may share an allocation), or written to out: tensors of the same shapes and types, for which
-    out=states reorders in place and leaves rows that stay alone. An out must not overlap itself or
-    another state. No gradient flows through it."""
+    Results are new tensors (small ones, 64 MiB in all, may share an allocation), or written to out:
+    tensors of the same shapes and types, for which out=states reorders in place and leaves rows that
+    stay alone. An out must not overlap itself or another state. No gradient flows through it."""
     done = (_calls or _load_calls()).reorder_beams(states, beams, out)
     if done is not None:
         return done
@@ -1048,6 +1059,7 @@ def reorder_beams(states, beams, out=None):
     B, W = beams.shape
     if W > 64:
         raise ValueError(f"a request has at most 64 beams, got {W}")
+    _int_sizes(B)
     dev = beams.device
     _on_gpu(dev, *sources)
     beams = beams.resolve_neg().contiguous()

@@ -77,7 +77,7 @@ const Mx4Variant kTiles[] = {
     tile<256, 256, 4, 2, 2>("mx4_256x256", 1.626, 0.0, 3.14, 3.75, 0.08),
 };
 // Few rows: 16 rows and columns, turns of 512 elements to a wave.
-const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves, 1>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0, 0.0};
+const Mx4Variant kRows = {"mx4_rows16", &k_mx4_rows<kWaves>, 16, 16, 64 * kWaves, 2, 0, 0.0, 0.0, 0.0, 0.0, 0.0};
 // For more columns than run at once and a K of a turn to a wave: two and one to a compute unit, which go on.
 const Mx4Variant kRowsOn[] = {
     {"mx4_rows16_on8", &k_mx4_rows_on<8>, 16, 16, 512, 2, 1, 0.0, 0.0, 0.0, 0.0, 0.0},

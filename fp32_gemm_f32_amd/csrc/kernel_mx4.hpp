@@ -110,11 +110,12 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(Mx4RowArgs p)
         const int k = unit[u] * 8;
         const T *x = static_cast<const T *>(p.X) + row[u] * p.ldx + k;
         const bool mine = row[u] < p.M;
-        if (mine && k + 8 <= p.K) {
+        const int left = p.K - k;                         // (k + 8 may pass 31 bits)
+        if (mine && left >= 8) {
             v[u] = mx4_load_unit<U != 1>(x);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[u].v[j] = mine && k + j < p.K ? x[j] : T(0.0f);
+            for (int j = 0; j < 8; ++j) v[u].v[j] = mine && j < left ? x[j] : T(0.0f);
         }
     }
 #pragma unroll
@@ -133,7 +134,7 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(Mx4RowArgs p)
         if (row[u] >= p.M) continue;
         const int k = unit[u] * 8;
         uint8_t *out = p.Q + row[u] * p.ldq + k / 2;
-        const int bytes = (p.K + 1) / 2 - k / 2;
+        const int bytes = (p.K - k) / 2 + (p.K & 1);      // (k is even)
         if (bytes >= 4) {
             *reinterpret_cast<Pack<uint32_t, 1> *>(out) = Pack<uint32_t, 1>{{q}};
         } else {
@@ -153,15 +154,16 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(Mx4RowArgs p)
     const uint8_t *in = p.Q + row * p.ldq + k / 2;
     const float size = mx4_unit(p.scales[row * p.lds + unit / 4]);
     T *y = static_cast<T *>(const_cast<void *>(p.X)) + row * p.ldx + k;
-    if (k + 8 <= p.K) {
+    const int left = p.K - k;                             // (k + 8 may pass 31 bits)
+    if (left >= 8) {
         store_pack(y, mx4_decode<T>(load_pack<uint32_t, 1>(reinterpret_cast<const uint32_t *>(in)).v[0], size));
     } else {
         uint32_t q = 0;
-        for (int j = 0; j < (p.K - k + 1) / 2; ++j) q |= uint32_t(in[j]) << 8 * j;
+        for (int j = 0; j < (left + 1) / 2; ++j) q |= uint32_t(in[j]) << 8 * j;
         const Pack<T, 8> v = mx4_decode<T>(q, size);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (k + j < p.K) y[j] = v.v[j];
+            if (j < left) y[j] = v.v[j];
     }
 }
 

@@ -10,7 +10,7 @@
 
 namespace sgemm {
 
-// A workgroup of WAVES waves computes 16 x 16 CB of C on v_mfma_scale_f32_16x16x128_f8f6f4; the waves
+// A workgroup of WAVES waves computes 16 x 16 of C on v_mfma_scale_f32_16x16x128_f8f6f4; the waves
 // take turns of 256 bytes of K (512 elements, 16 scales to a row) and their sums are added in LDS, in
 // the waves' order.
 //  * MFMA operands: lane l supplies row l % 16 and a block of 32 values with its scale, block l / 16
@@ -23,60 +23,46 @@ namespace sgemm {
 //  * Rows past M and columns past N repeat the last one; their sums are not stored.
 //  * The next turn is loaded before this one is multiplied.
 constexpr int kMx4Turn = 256;
-template <int WAVES, int CB>
+template <int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(Mx4Args p)
 {
-    constexpr int NT = 64 * WAVES, BN = 16 * CB;
-    static_assert(16 * BN <= NT, "an element of C to a thread");
-    __shared__ float sums[WAVES][16 * BN];
+    static_assert(256 <= 64 * WAVES, "an element of C to a thread");
+    __shared__ float sums[WAVES][256];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tiles = p.tiles_m * p.tiles_n;
     const int split = blockIdx.x / tiles, tile = blockIdx.x - split * tiles;
     const int tn = tile / p.tiles_m, tm = tile - tn * p.tiles_m;
-    const int m0 = tm * 16, n0 = tn * BN;
+    const int m0 = tm * 16, n0 = tn * 16;
     const int k0 = split * p.chunk, k1 = min(p.KB, k0 + p.chunk);
     const int r = lane & 15, q = lane >> 4;
-    const int64_t ar = min(m0 + r, p.M - 1);
-    const uint8_t *A = p.A + ar * p.lda, *SA = p.sa + ar * p.ldsa, *B[CB], *SB[CB];
-#pragma unroll
-    for (int j = 0; j < CB; ++j) {
-        const int64_t br = min(n0 + 16 * j + r, p.N - 1);
-        B[j] = p.B + br * p.ldb;
-        SB[j] = p.sb + br * p.ldsb;
-    }
+    const int64_t ar = min(m0 + r, p.M - 1), br = min(n0 + r, p.N - 1);
+    const uint8_t *A = p.A + ar * p.lda, *SA = p.sa + ar * p.ldsa;
+    const uint8_t *B = p.B + br * p.ldb, *SB = p.sb + br * p.ldsb;
     const int blocks = (p.KB + 15) / 16;
-    const int em = m0 + tid / BN, en = n0 + tid % BN;
-    const bool stores = tid < 16 * BN && em < p.M && en < p.N;
+    const int em = m0 + tid / 16, en = n0 + tid % 16;
+    const bool stores = tid < 256 && em < p.M && en < p.N;
     const float bias = stores && p.bias ? p.bias[en] : 0.0f;
 
     struct Turn {
-        i32x4 a[4], b[CB][4], sa, sb[CB];
+        i32x4 a[4], b[4], sa, sb;
     };
     auto load = [&](Turn &x, int k) __attribute__((always_inline)) {
 #pragma unroll
-        for (int j = 0; j < CB; ++j) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) x.b[j][t] = mx4_load16(B[j] + k + 64 * t + 16 * q);
-            x.sb[j] = mx4_load16(SB[j] + k / 16);
-        }
+        for (int t = 0; t < 4; ++t) x.b[t] = mx4_load16(B + k + 64 * t + 16 * q);
+        x.sb = mx4_load16(SB + k / 16);
 #pragma unroll
         for (int t = 0; t < 4; ++t) x.a[t] = mx4_load16(A + k + 64 * t + 16 * q);
         x.sa = mx4_load16(SA + k / 16);
     };
-    f32x4 acc[CB];
-#pragma unroll
-    for (int j = 0; j < CB; ++j) acc[j] = f32x4(0.0f);
+    f32x4 acc = f32x4(0.0f);
     auto multiply = [&](const Turn &x) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const i32x8 a = __builtin_shufflevector(x.a[t], x.a[t], 0, 1, 2, 3, -1, -1, -1, -1);
-#pragma unroll
-            for (int j = 0; j < CB; ++j) {
-                const i32x8 b = __builtin_shufflevector(x.b[j][t], x.b[j][t], 0, 1, 2, 3, -1, -1, -1, -1);
-                acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[j], 4, 4, 0, int(uint32_t(x.sa[t]) >> 8 * q), 0,
-                                                                          int(uint32_t(x.sb[j][t]) >> 8 * q));
-            }
+            const i32x8 b = __builtin_shufflevector(x.b[t], x.b[t], 0, 1, 2, 3, -1, -1, -1, -1);
+            acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 4, 0, int(uint32_t(x.sa[t]) >> 8 * q), 0,
+                                                                   int(uint32_t(x.sb[t]) >> 8 * q));
         }
     };
     constexpr int STRIDE = WAVES * kMx4Turn;
@@ -100,18 +86,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_mx4_rows(Mx4Args p)
         for (int t = 0; t < 4; ++t) {
             const int k = whole + 64 * t + 16 * q;
             x.a[t] = mx4_load_tail(A, k, k1);
-#pragma unroll
-            for (int j = 0; j < CB; ++j) x.b[j][t] = mx4_load_tail(B[j], k, k1);
+            x.b[t] = mx4_load_tail(B, k, k1);
         }
         x.sa = mx4_load_tail(SA, whole / 16, blocks);
-#pragma unroll
-        for (int j = 0; j < CB; ++j) x.sb[j] = mx4_load_tail(SB[j], whole / 16, blocks);
+        x.sb = mx4_load_tail(SB, whole / 16, blocks);
         multiply(x);
     }
 #pragma unroll
-    for (int j = 0; j < CB; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sums[wave][(4 * q + v) * BN + 16 * j + r] = acc[j][v];
+    for (int v = 0; v < 4; ++v) sums[wave][(4 * q + v) * 16 + r] = acc[v];
     __syncthreads();
     if (!stores) return;
     float sum = 0.0f;

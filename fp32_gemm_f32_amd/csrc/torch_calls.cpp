@@ -309,19 +309,18 @@ PyObject *quantize_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// dequantize_mx4(Q, scales, type, columns or -1) -> values or None
+// dequantize_mx4(Q, scales, type, columns or None) -> values or None
 PyObject *dequantize_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 4 || !PyLong_CheckExact(args[2]) || !PyLong_CheckExact(args[3])) return none();
+    if (n != 4 || !PyLong_CheckExact(args[2]) || (args[3] != Py_None && !PyLong_CheckExact(args[3]))) return none();
     const at::Tensor *q = plain(args[0]), *scales = plain(args[1]);
     if (!q || !scales) return none();
     const Packed p(*q, *scales);
     const int code = int(PyLong_AsLong(args[2]));
-    long columns = PyLong_AsLong(args[3]);
+    const long columns = args[3] == Py_None ? 2L * p.q.cols : PyLong_AsLong(args[3]);
     if (PyErr_Occurred()) PyErr_Clear();
     if (!p.ok || code < 0 || code > 2) return none();
-    if (columns == -1) columns = 2L * p.q.cols;
     if (columns < 0 || packed_columns(columns) != p.q.cols) return none();
     at::Tensor y;
     int status;
@@ -410,11 +409,11 @@ PyObject *linear_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
 
 // ---- beam search
 
-// beam_step(logits, scores, top or -1, finished or None, pad_token) -> (scores, beams, tokens) or None
+// beam_step(logits, scores, top or None, finished or None, pad_token) -> (scores, beams, tokens) or None
 PyObject *beam_step_(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    if (n != 5 || !PyLong_CheckExact(args[2]) || !PyLong_CheckExact(args[4])) return none();
+    if (n != 5 || (args[2] != Py_None && !PyLong_CheckExact(args[2])) || !PyLong_CheckExact(args[4])) return none();
     const at::Tensor *x = plain(args[0]), *scores = plain(args[1]);
     const at::Tensor *finished = args[3] == Py_None ? nullptr : plain(args[3]);
     if (!x || !scores || (args[3] != Py_None && !finished)) return none();
@@ -425,7 +424,7 @@ PyObject *beam_step_(PyObject *, PyObject *const *args, Py_ssize_t n)
         return t.scalar_type() == type && t.dim() == 2 && t.is_contiguous() && t.device() == device && !t.is_neg() &&
                t.size(0) <= INT_MAX && t.size(1) <= BEAM_MAX;
     };
-    long top = PyLong_AsLong(args[2]);
+    long top = args[2] == Py_None ? 0 : PyLong_AsLong(args[2]);
     const long long pad_token = PyLong_AsLongLong(args[4]);
     if (PyErr_Occurred()) {
         PyErr_Clear();
@@ -435,7 +434,7 @@ PyObject *beam_step_(PyObject *, PyObject *const *args, Py_ssize_t n)
     const int64_t B = scores->size(0), W = scores->size(1);
     if (finished && (!per_beam(*finished, at::kBool) || finished->size(0) != B || finished->size(1) != W))
         return none();
-    if (top == -1) top = W;
+    if (args[2] == Py_None) top = W;
     if (m.rows != B * W || W < 1 || top < 1 || top > BEAM_MAX) return none();
     at::Tensor out[3], space;
     int status;

@@ -171,6 +171,8 @@ def test_step_refusals(torch):
     with pytest.raises(ValueError):
         g.beam_step(x, s, top=0)
     with pytest.raises(ValueError):
+        g.beam_step(x, s, top=-1)
+    with pytest.raises(ValueError):
         g.beam_step(x, s, top=65)
     with pytest.raises(ValueError):
         g.beam_step(torch.zeros(65, 10, device="cuda"), torch.zeros(1, 65, device="cuda"))
@@ -263,6 +265,29 @@ def test_reorder_single_and_many_states(torch):
     assert torch.equal(g.reorder_beams([odd], beams)[0], odd[beams[0]])
     with pytest.raises(ValueError):
         g.reorder_beams([odd], beams, out=[odd])
+
+
+def test_reordered_tensors_are_ordinary_ones(torch):
+    """Results that share an allocation: of every type, apart, and good for a graph of gradients."""
+    beams = torch.tensor([[1, 1, 0], [2, 0, 1]], device="cuda", dtype=torch.int32)
+    rows = torch.tensor([1, 1, 0, 5, 3, 4], device="cuda")
+    kinds = [torch.float32, torch.bool, torch.int64, torch.complex64, torch.float8_e4m3fn, torch.float64, torch.int8]
+    states = [torch.randint(0, 2, (6, 3, 5), device="cuda").to(kind) for kind in kinds]
+    moved = g.reorder_beams(states, beams)
+    for kind, s, m in zip(kinds, states, moved):
+        assert m.dtype == kind and m.is_contiguous()
+        assert torch.equal(m.view(6, -1).view(torch.uint8), s[rows].view(6, -1).view(torch.uint8))
+    moved[0].zero_()
+    assert torch.equal(moved[2], states[2][rows])
+    x = moved[5].requires_grad_()
+    (x * x).sum().backward()
+    assert torch.equal(x.grad, 2 * states[5][rows])
+    with torch.inference_mode():
+        assert all(t.is_inference() for t in g.reorder_beams(states, beams))
+    # the first columns of more continuations than beams
+    r = g.beam_step(torch.randn(6, 50, device="cuda"), torch.zeros(2, 3, device="cuda"), top=7)
+    got = g.reorder_beams(states[:1], r.beams[:, :3])[0]
+    assert torch.equal(got, states[0][(r.beams[:, :3] + 3 * torch.arange(2, device="cuda")[:, None]).view(-1)])
 
 
 def test_reorder_into_other_tensors(torch):

@@ -65,3 +65,31 @@ def test_reorder(torch):
     for w in windows(border, B):
         want = torch.arange(B, dtype=torch.int32, device="cuda")[w][:, None] + 7 * beams[w]
         assert torch.equal(out[w], want)
+
+
+def test_the_longest_row(torch):
+    """2^31 - 1 elements: a unit of eight starts at 2^31 - 8 and ends past what 31 bits count."""
+    K = 2 ** 31 - 1
+    x = torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    end = torch.randn(1, 33, device="cuda").bfloat16()
+    x[:, -31:] = end[:, :31]                       # the last block, 31 of 32
+    x[:, :32] = end[:, :32]
+    print(f"[many rows] mx4 quantize 1x{K}", flush=True)
+    q = torch.full((1, 2 ** 30 + 16), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((1, 2 ** 26 + 16), 0x55, dtype=torch.uint8, device="cuda")
+    g.quantize_mx4(x, out=q[:, :2 ** 30], scales=s[:, :2 ** 26])
+    for part, at in [(end[:, :31], 2 ** 31 - 32), (end[:, :32], 0)]:
+        a, b = g.quantize_mx4(part.contiguous())
+        assert torch.equal(q[:, at // 2:at // 2 + 16], a) and torch.equal(s[:, at // 32:at // 32 + 1], b)
+    assert not q[:, 16:2 ** 30 - 16].any() and not s[:, 1:2 ** 26 - 1].any()
+    assert (q[:, 2 ** 30:] == 0x55).all() and (s[:, 2 ** 26:] == 0x55).all()
+    y = torch.full((1, 2 ** 31 + 31), 9.0, dtype=torch.bfloat16, device="cuda")
+    g.dequantize_mx4(q[:, :2 ** 30], s[:, :2 ** 26], columns=K, out=y[:, :K])
+    a, b = g.quantize_mx4(end[:, :31].contiguous())
+    assert torch.equal(y[:, K - 31:K], g.dequantize_mx4(a, b, dtype=torch.bfloat16, columns=31))
+    assert not y[:, 32:K - 31].any() and (y[:, K:] == 9.0).all()
+    del x, y
+    with pytest.raises(ValueError):                # 2^31 elements
+        g.dequantize_mx4(q[:, :2 ** 30], s[:, :2 ** 26])
+    with pytest.raises(ValueError):
+        g.matmul_mx4(q[:, :2 ** 30], s[:, :2 ** 26], q[:, :2 ** 30], s[:, :2 ** 26])

@@ -288,6 +288,8 @@ def test_other_layouts_and_refusals(torch):
     with pytest.raises(ValueError):
         g.dequantize_mx4(A, SA, columns=94)
     with pytest.raises(ValueError):
+        g.dequantize_mx4(A, SA, columns=-1)
+    with pytest.raises(ValueError):
         g.linear_mx4(torch.zeros(2, 94, device="cuda"), B, SB)
     with pytest.raises(TypeError):
         g.quantize_mx4(torch.zeros(2, 64, dtype=torch.float64, device="cuda"))
