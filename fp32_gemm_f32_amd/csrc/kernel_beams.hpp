@@ -102,6 +102,8 @@ __global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
 {
     typedef typename Elem<DT>::type T;
     constexpr int W = 16 / sizeof(T);
+    // (in shorter parts it costs more than it saves: 4 rows of 131072 f32 10.9 and 11.3 us)
+    constexpr bool APART = NT == 1024;
     __shared__ StatsShared<NT> stats;
     __shared__ TopShared<NT> tops;
     const int tid = threadIdx.x;
@@ -119,13 +121,14 @@ __global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
 
     BeamStats st;
     Pack<T, W> b[U];
-    // the best group: its value in key order, and its first element
-    uint32_t best = 0;
+    // the best group: its value in key order, and its first element; the second best's value
+    uint32_t best = 0, second = 0;
     int best_at = tid < head ? tid : tid < chunks ? head + tid * W : tail + tid;
     const bool empty = best_at >= n;
     auto note = [&](float peak, int at) __attribute__((always_inline)) {
         const uint32_t o = ordered(peak);
         best_at = o > best ? at : best_at;
+        if constexpr (APART) second = max(second, min(o, best));
         best = max(best, o);
     };
     float edge[2] = {0.0f, 0.0f};                         // the thread's head and tail elements
@@ -183,26 +186,42 @@ __global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
     uint64_t floor = top_bound(tops, mine, top);
     // the bound's group reaches W - 1 elements behind its first
     floor = max(floor - min(uint32_t(floor), uint32_t(W - 1)), uint64_t(1));
-    if (chunks <= U * NT) {                               // b holds all of this thread's chunks
-        static_assert(U * W <= 32, "a bit for each element");
-        if (mine >= floor) {
+    // Where b holds all of a thread's chunks they are looked at there. Else the thread is listed, and all
+    // threads look at the listed ones' chunks; APART: but where only its best group reaches the bound
+    // it loads that alone (16 bytes here and there are a line of 128 each: of 1024 rows of 131072 bf16
+    // and 16 of each, 12 % more is read without, 56.7 and 54.3 us).
+    if (mine >= floor) {
+        if (chunks <= U * NT) {
+            static_assert(U * W <= 32, "a bit for each element");
             const int mine_n = tid < chunks ? (chunks - tid + NT - 1) / NT * W : 0;
             add_candidates<DT>(tops, b, mine_n == 32 ? 0xffffffffu : (1u << mine_n) - 1, floor,
                                [&](int i) { return head + (tid + i / W * NT) * W + i % W; });
             if (tid < head) add_candidate(tops, key_of(edge[0], uint32_t(tid)), floor);
             if (tid < n - tail) add_candidate(tops, key_of(edge[1], uint32_t(tail + tid)), floor);
+        } else if (!APART || second >= uint32_t(floor >> 32)) {
+            tops.threads[atomicAdd(&tops.n_threads, 1)] = tid;
+        } else if (best_at < head || best_at >= tail) {
+            add_candidate(tops, key_of(edge[best_at < head ? 0 : 1], uint32_t(best_at)), floor);
+        } else {
+            const Pack<T, W> one[1] = {load_pack<T, W>(x + best_at)};
+            add_candidates<DT>(tops, one, (1u << W) - 1, floor, [&](int j) { return best_at + j; });
         }
-        __syncthreads();
-        const int found = tops.n_cand;
-        if (found <= kCandidates) {
-            rank_top(tops, found, top, emit);
-            return;
-        }
-        __syncthreads();                                  // all have read it
-        if (tid == 0) tops.n_cand = 0;
     }
-    if (mine >= floor) tops.threads[atomicAdd(&tops.n_threads, 1)] = tid;
     __syncthreads();
+    int found = tops.n_cand;
+    const int listed = tops.n_threads;
+    if (found <= kCandidates && listed == 0) {
+        rank_top(tops, found, top, emit);
+        return;
+    }
+    if (found > kCandidates) {                            // list them all
+        __syncthreads();                                  // all have read it
+        if (tid == 0) { tops.n_cand = 0; tops.n_threads = 0; }
+        __syncthreads();
+        if (mine >= floor) tops.threads[atomicAdd(&tops.n_threads, 1)] = tid;
+        __syncthreads();
+        found = 0;
+    }
     // the threads' chunks, and one more slot for their head and tail
     const int per = (chunks + NT - 1) / NT + 1;
     auto look = [&](int slot, uint64_t from) {
@@ -218,7 +237,7 @@ __global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
         const Pack<T, W> one[1] = {load_pack<T, W>(body + int64_t(chunk) * W)};
         add_candidates<DT>(tops, one, (1u << W) - 1, from, [&](int j) { return head + chunk * W + j; });
     };
-    select_top(tops, floor, tops.n_threads * per, top, look, emit);
+    select_top(tops, floor, tops.n_threads * per, top, look, emit, found);
 }
 
 // ------------------------------------------------------------------ among the beams -----
@@ -258,8 +277,9 @@ template <int MOST> struct BeamList {
 // parts' W splits top keys. A bound that at least `top` of them reach comes from the threads' best
 // ones; those that reach it are ranked against each other. All of it is latency: the keys are
 // loaded first, what fits the registers (kKept to a thread), and meanwhile the sums are joined, the
-// parts of several beams side by side. 128 requests of 8 beams, 16 of each: 4 us, of which the way to the
-// first loads is a fifth, the sums' logarithms a fifth, bound, list and ranks a fifth each.
+// parts of several beams side by side. 128 requests of 8 beams, 16 of each: 5 us, of which the way to the
+// first loads is a fifth, the sums' logarithms a fifth, bound, list and ranks a fifth each; 2 of 64
+// beams in six parts, 64 of each: 68 us, most of it the keys' loads and the totals, taken twice.
 constexpr int kChoiceThreads = 256, kKept = 8;
 __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
 {
@@ -280,10 +300,13 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
     const char *parts = p.parts + row0 * p.splits * p.part_bytes;
     const auto part = [&](int i) { return reinterpret_cast<const RowPart *>(parts + i * p.part_bytes); };
     const int total = p.W * p.splits * p.top;
+    // Key i: part i / top's, which are in descending order. Each part starts with another one, or the
+    // threads' best ones would be firsts in one thread and lasts in another, and the bound the best of
+    // the lasts (with top = 64: 24576 keys of 64 beams took 3.8 ms).
     const auto load_key = [&](int i, int &w) {
-        const int at = divide(i, p.by_top);
+        const int at = divide(i, p.by_top), r = i - at * p.top + at - divide(at, p.by_top) * p.top;
         w = divide(at, p.by_splits);
-        return reinterpret_cast<const uint64_t *>(part(at) + 1)[i - at * p.top];
+        return reinterpret_cast<const uint64_t *>(part(at) + 1)[r < p.top ? r : r - p.top];
     };
     // lanes to a beam: as many as it has parts, a power of two
     int lanes = 1;
@@ -339,11 +362,19 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
         t[e] = e * NT + tid < total ? total_of(key[e], e * NT + tid, beam[e]) : 0;
         mine = max(mine, t[e]);
     }
-    for (int i = kKept * NT + tid; i < total; i += NT) {
-        int w;
-        const uint64_t k = load_key(i, w);
-        mine = max(mine, total_of(k, i, w));
-    }
+    // those that are not kept, kKept loads at a time
+    const auto each_further = [&](auto take) __attribute__((always_inline)) {
+        for (int i0 = kKept * NT + tid; i0 < total; i0 += kKept * NT) {
+            uint64_t k[kKept];
+            int w[kKept];
+#pragma unroll
+            for (int e = 0; e < kKept; ++e) k[e] = load_key(min(i0 + e * NT, total - 1), w[e]);
+#pragma unroll
+            for (int e = 0; e < kKept; ++e)
+                if (i0 + e * NT < total) take(total_of(k[e], i0 + e * NT, w[e]), k[e], w[e]);
+        }
+    };
+    each_further([&](uint64_t t, uint64_t, int) { mine = max(mine, t); });
     best[tid] = uint32_t(mine >> 32);
     __syncthreads();
     // the threads joined to 64; the least of these that fewer than `top` others exceed, by the
@@ -371,23 +402,23 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
     };
 #pragma unroll
     for (int e = 0; e < kKept; ++e) put(t[e], key[e], beam[e]);
-    for (int i = kKept * NT + tid; i < total; i += NT) {
-        int w;
-        const uint64_t k = load_key(i, w);
-        put(total_of(k, i, w), k, w);
-    }
+    each_further(put);
     __syncthreads();
     int n = count;
     if (n > MOST) {
-        // many equal totals: NT at a time, the list cut to its best whenever it might overflow
+        // many equal totals: NT at a time, the list cut to its best whenever it might overflow; from then on
+        // only what comes before the last of these is added
         __syncthreads();
         if (tid == 0) count = 0;
         __syncthreads();
+        bool cut = false;
+        const int last = p.top - 1;
         for (int i0 = 0; i0 < total; i0 += NT) {
             if (i0 + tid < total) {
                 int w;
-                const uint64_t k = load_key(i0 + tid, w);
-                put(total_of(k, i0 + tid, w), k, w);
+                const uint64_t k = load_key(i0 + tid, w), t = total_of(k, i0 + tid, w);
+                const bool before = t > kept_total[last] || (t == kept_total[last] && (w < kept_beam[last] || (w == kept_beam[last] && k > kept_key[last])));
+                if (!cut || before) put(t, k, w);
             }
             __syncthreads();
             n = count;
@@ -401,8 +432,42 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
             if (tid < p.top) list.put(tid, kept_total[tid], kept_key[tid], kept_beam[tid]);
             if (tid == 0) count = p.top;
             n = p.top;
+            cut = true;
             __syncthreads();
         }
+    }
+    if (n > 64) {
+        // Ranking takes n^2: the list is cut to what reaches the total of rank `top`, by the upper words. Every
+        // wave finds it by halving, the words in its registers (1024 keys of one beam, 64 of them, with the
+        // pass: 322 and 41 us).
+        uint32_t upper[MOST / 64], least = 0;
+#pragma unroll
+        for (int e = 0; e < MOST / 64; ++e) upper[e] = e * 64 + lane < n ? uint32_t(list.total[e * 64 + lane] >> 32) : 0;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t to = least | 1u << bit;
+            int reach = 0;
+#pragma unroll
+            for (int e = 0; e < MOST / 64; ++e) reach += __popcll(__ballot(upper[e] >= to));
+            if (reach >= p.top) least = to;
+        }
+        uint64_t own_total[MOST / NT], own_key[MOST / NT];
+        int own_beam[MOST / NT];
+#pragma unroll
+        for (int e = 0; e < MOST / NT; ++e) {
+            const int i = e * NT + tid;
+            own_total[e] = i < n ? list.total[i] : 0;
+            own_key[e] = i < n ? list.key[i] : 0;
+            own_beam[e] = i < n ? list.beam[i] : 0;
+        }
+        __syncthreads();
+        if (tid == 0) count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < MOST / NT; ++e)
+            if (own_total[e] != 0 && uint32_t(own_total[e] >> 32) >= least)
+                list.put(atomicAdd(&count, 1), own_total[e], own_key[e], own_beam[e]);
+        __syncthreads();
+        n = count;
     }
     const int64_t out = request * p.top;
     const auto write = [&](int r, uint64_t total, uint64_t key, int w) {

@@ -245,10 +245,10 @@ __device__ inline void rank_top(TopShared<NT> &sh, int n, int top, Emit emit)
 // kNarrow at a time from a list cut to the top. Then emit(rank, key) for the top.
 template <int NT, typename Look, typename Emit>
 __device__ inline void select_top(TopShared<NT> &sh, uint64_t floor, int slots, int top, Look look,
-                                  Emit emit)
+                                  Emit emit, int have = 0)
 {
     static_assert(kCandidates >= 2 * kNarrow * 8, "the list holds a narrow step");
-    int width = NT, have = 0;
+    int width = NT;
     for (int at = 0; at < slots;) {
         const int slot = at + int(threadIdx.x);
         if (int(threadIdx.x) < width && slot < slots) look(slot, floor);

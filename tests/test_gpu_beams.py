@@ -139,6 +139,37 @@ def test_ties(torch):
             check(torch, r, reference(x, scores, top), x.shape[1], ties=True)
 
 
+@pytest.mark.parametrize("B,W,V,top", [(2, 64, 20001, 64), (1, 64, 33000, 32), (5, 48, 4000, 48), (1, 40, 66000, 63),
+                                       (260, 1, 70001, 64), (130, 2, 65536, 33)])
+@pytest.mark.parametrize("kind", ["spread", "alike", "steps"])
+def test_many_beams(torch, kind, B, W, V, top):
+    """More keys than the list of the choice holds: beams that differ, beams that are alike, and few
+    distinct logits, whose best ones fill the list many times."""
+    rng = np.random.default_rng(B + W + top)
+    if kind == "steps":
+        x = np.repeat(rng.integers(-2, 3, size=(B, V)), W, axis=0).astype(np.float32)
+        scores = np.full((B, W), -2.0, np.float32)
+    else:
+        x = rng.standard_normal((B * W, V)).astype(np.float32)
+        scores = (-rng.random((B, W)) * (2.0 if kind == "spread" else 0.0)).astype(np.float32)
+    r = g.beam_step(torch.from_numpy(x).cuda(), torch.from_numpy(scores).cuda(), top=top)
+    want = reference(x, scores, top)
+    if kind != "steps":
+        check(torch, r, want, V)
+        return
+    # The beams of a request are the same, but rows of odd lengths lie differently in 16-byte chunks: their
+    # sums of V terms go in other orders, each off by up to n 2^-24 (check's n), and so are the totals. Any
+    # beam may come first, then; each beam's own continuations are the first ones of its order.
+    n = V / 256 + 64
+    assert np.abs(r.scores.cpu().numpy() - want[0]).max() <= n * 2.0 ** -24 + 2.0 ** -24 * np.abs(want[0]).max()
+    beams, tokens = r.beams.cpu().numpy(), r.tokens.cpu().numpy()
+    for b in range(B):
+        order = np.lexsort((np.arange(V), -x[b * W]))[:top]
+        for w in range(W):
+            mine = tokens[b][beams[b] == w]
+            assert np.array_equal(mine, order[:len(mine)])
+
+
 def test_rows_without_a_continuation(torch):
     x = np.random.default_rng(1).standard_normal((12, 600)).astype(np.float32)
     x[0], x[1, 5], x[2, 7], x[3, 1:] = -INF, np.nan, INF, -INF
