@@ -417,7 +417,9 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
             if (i0 + tid < total) {
                 int w;
                 const uint64_t k = load_key(i0 + tid, w), t = total_of(k, i0 + tid, w);
-                const bool before = t > kept_total[last] || (t == kept_total[last] && (w < kept_beam[last] || (w == kept_beam[last] && k > kept_key[last])));
+                const bool before = t > kept_total[last] ||
+                                    (t == kept_total[last] &&
+                                     (w < kept_beam[last] || (w == kept_beam[last] && k > kept_key[last])));
                 if (!cut || before) put(t, k, w);
             }
             __syncthreads();

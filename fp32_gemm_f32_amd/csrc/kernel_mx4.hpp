@@ -157,6 +157,7 @@ __global__ __launch_bounds__(256) void k_mx4_dequantize(Mx4RowArgs p)
     const int left = p.K - k;                             // (k + 8 may pass 31 bits)
     if (left >= 8) {
         store_pack(y, mx4_decode<T>(load_pack<uint32_t, 1>(reinterpret_cast<const uint32_t *>(in)).v[0], size));
+        store_data_guard<true>();                         // the other branch begins with writes of its registers
     } else {
         uint32_t q = 0;
         for (int j = 0; j < (left + 1) / 2; ++j) q |= uint32_t(in[j]) << 8 * j;
