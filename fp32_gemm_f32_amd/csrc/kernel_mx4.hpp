@@ -80,6 +80,12 @@ struct Mx4RowArgs {
     Divisor by_units;
 };
 
+// Bytes that what is left of a row takes. A row is filled up to whole blocks of four units, so a unit may
+// start behind its end: `left` is below 0 then, and -1 / 2 is 0.
+constexpr int mx4_bytes_of(int left) { return left <= 0 ? 0 : left / 2 + left % 2; }
+static_assert(mx4_bytes_of(-1) == 0 && mx4_bytes_of(-25) == 0 && mx4_bytes_of(0) == 0 && mx4_bytes_of(1) == 1 &&
+              mx4_bytes_of(7) == 4 && mx4_bytes_of(8) == 4 && mx4_bytes_of(0x7fffffff) == 0x40000000, "a row's end");
+
 // 8 elements; STREAM: read past the caches.
 template <bool STREAM, typename T> __device__ inline Pack<T, 8> mx4_load_unit(const T *x)
 {
@@ -134,7 +140,7 @@ __global__ __launch_bounds__(256) void k_mx4_quantize(Mx4RowArgs p)
         if (row[u] >= p.M) continue;
         const int k = unit[u] * 8;
         uint8_t *out = p.Q + row[u] * p.ldq + k / 2;
-        const int bytes = (p.K - k) / 2 + (p.K & 1);      // (k is even)
+        const int bytes = mx4_bytes_of(p.K - k);
         if (bytes >= 4) {
             *reinterpret_cast<Pack<uint32_t, 1> *>(out) = Pack<uint32_t, 1>{{q}};
         } else {
