@@ -214,8 +214,8 @@ __global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
         rank_top(tops, found, top, emit);
         return;
     }
+    __syncthreads();                                      // all have read both before either changes
     if (found > kCandidates) {                            // list them all
-        __syncthreads();                                  // all have read it
         if (tid == 0) { tops.n_cand = 0; tops.n_threads = 0; }
         __syncthreads();
         if (mine >= floor) tops.threads[atomicAdd(&tops.n_threads, 1)] = tid;
