@@ -32,9 +32,11 @@ struct BeamArgs {
 // ------------------------------------------------------------------ a beam's row --------
 // Running peak m and s = sum 2^(x L - c), L = log2 e as FP32 has it and c = m L: one multiply-add and one
 // exponential to an element. What FP32 rounds off here is either known (c is taken as it was rounded: see
-// beam_reference), random in sign from term to term (it averages out: 2e-8 of log s), or, as L is off
-// by 1.3e-8 of itself, that much of the row's entropy, nearly the same for all of a request's beams.
-// Which of two beams' tokens comes first hangs on such differences. Beyond kFar m L may overflow
+// beam_reference), random in sign from term to term, or, as L is off by 1.3e-8 of itself, that much of
+// the row's entropy, nearly the same for all of a request's beams. Which of two beams' tokens comes
+// first hangs on such differences. raise() rounds both its products, so that a sum goes from one c as it
+// was rounded to another: a multiply-add in place of one of them would rescale by 2^(half a step of c)
+// each time, even where the peak stays. Beyond kFar m L may overflow
 // (a mask of FP32's lowest value): there 2^((x - m) L), with a subtraction more.
 constexpr float kFar = 1e30f;
 constexpr double kNats = 1.0 / double(kLog2e);         // of a base-2 logarithm by L
@@ -44,6 +46,7 @@ struct BeamStats {
     __device__ bool far() const { return !(__builtin_fabsf(m) <= kFar); }
     __device__ void raise(float to)
     {
+#pragma clang fp contract(off)
         const float next = __builtin_fmaxf(m, to);
         const float near = m * kLog2e - next * kLog2e, away = (m - next) * kLog2e;
         const bool both = __builtin_fabsf(m) <= kFar && __builtin_fabsf(next) <= kFar;
