@@ -31,32 +31,38 @@ struct BeamArgs {
 
 // ------------------------------------------------------------------ a beam's row --------
 // Running peak m and s = sum 2^(x L - c), L = log2 e as FP32 has it and c = m L: one multiply-add and one
-// exponential to an element. What FP32 rounds off here is either known (c is taken as it was rounded: see
-// beam_reference), random in sign from term to term, or, as L is off by 1.3e-8 of itself, that much of
-// the row's entropy, nearly the same for all of a request's beams. Which of two beams' tokens comes
-// first hangs on such differences. raise() rounds both its products, so that a sum goes from one c as it
-// was rounded to another: a multiply-add in place of one of them would rescale by 2^(half a step of c)
-// each time, even where the peak stays. Beyond kFar m L may overflow
-// (a mask of FP32's lowest value): there 2^((x - m) L), with a subtraction more.
-constexpr float kFar = 1e30f;
+// exponential to an element. What FP32 rounds off here is either known (c is taken as it was rounded),
+// random in sign from term to term, or, as L is off by 1.3e-8 of itself, that much of the row's entropy,
+// nearly the same for all of a request's beams. Which of two beams' tokens comes first hangs on such
+// differences. beam_rescale rounds both its products, so that a sum goes from one c as it was rounded to
+// another: a multiply-add in place of one of them would rescale by 2^(half a step of c) each time, even
+// where the peak stays.
+// Up to kFar a step of c is 128 at most, so that sums of 2^31 terms stay in range. Beyond, logits that
+// differ do so by 128 and more, also from those up to it: a term, there 2^((x - m) L), is 1 or 0, and so
+// is the factor between two peaks one of which lies beyond.
+constexpr float kFar = 1073741824.0f;                  // 2^30
 constexpr double kNats = 1.0 / double(kLog2e);         // of a base-2 logarithm by L
+__device__ inline bool beam_near(float m) { return __builtin_fabsf(m) <= kFar; }
+// What a sum over peak `from` is multiplied by to be one over `to`, a larger one or the same.
+__device__ inline float beam_rescale(float from, float to)
+{
+#pragma clang fp contract(off)
+    const float near = __builtin_amdgcn_exp2f(from * kLog2e - to * kLog2e);
+    return beam_near(from) && beam_near(to) ? near : from == to ? 1.0f : 0.0f;
+}
 struct BeamStats {
     float m = kLowest, s = 0.0f;
 
-    __device__ bool far() const { return !(__builtin_fabsf(m) <= kFar); }
     __device__ void raise(float to)
     {
-#pragma clang fp contract(off)
         const float next = __builtin_fmaxf(m, to);
-        const float near = m * kLog2e - next * kLog2e, away = (m - next) * kLog2e;
-        const bool both = __builtin_fabsf(m) <= kFar && __builtin_fabsf(next) <= kFar;
-        s *= __builtin_amdgcn_exp2f(__builtin_fmaxf(both ? near : away, -1000.0f));
+        s *= beam_rescale(m, next);
         m = next;
     }
     // n elements with m already raised to them
     template <int N> __device__ void add(const float (&x)[N])
     {
-        if (far()) {
+        if (!beam_near(m)) {
 #pragma unroll
             for (int j = 0; j < N; ++j) s += __builtin_amdgcn_exp2f((x[j] - m) * kLog2e);
         } else {
@@ -66,11 +72,6 @@ struct BeamStats {
         }
     }
 };
-// What a sum's terms are taken over, in base 2: c, or where it is far m L without rounding.
-__device__ inline double beam_reference(float m)
-{
-    return __builtin_fabsf(m) <= kFar ? double(m * kLog2e) : double(m) * double(kLog2e);
-}
 
 // Every thread gets the workgroup's joined sums, in the same order each time.
 template <int NT> __device__ inline BeamStats join_beam_stats(StatsShared<NT> &sh, BeamStats st)
@@ -333,15 +334,11 @@ __global__ __launch_bounds__(kChoiceThreads) void k_beam_choice(BeamArgs p)
             m = first.peak;
             for (int s = sub + lanes; s < p.splits; s += lanes) m = __builtin_fmaxf(m, row_part(w, s).peak);
             for (int d = 1; d < lanes; d <<= 1) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-            const double to = beam_reference(m);
-            const auto term = [&](const RowPart &q) {
-                const float down = __builtin_fmaxf(float(beam_reference(q.peak) - to), -1000.0f);
-                return double(q.sum) * double(__builtin_amdgcn_exp2f(down));
-            };
+            const auto term = [&](const RowPart &q) { return double(q.sum) * double(beam_rescale(q.peak, m)); };
             double sum = term(first);
             for (int s = sub + lanes; s < p.splits; s += lanes) sum += term(row_part(w, s));
             for (int d = 1; d < lanes; d <<= 1) sum += __shfl_xor(sum, d);
-            value -= log2(sum) * kNats + (__builtin_fabsf(m) <= kFar ? to * kNats - double(m) : 0.0);
+            value -= log2(sum) * kNats + (beam_near(m) ? double(m * kLog2e) * kNats - double(m) : 0.0);
         }
         if (sub == 0) { offset[w] = value; peaks[w] = m; ended[w] = done; }
         w += NT / lanes;
