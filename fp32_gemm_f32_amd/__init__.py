@@ -823,6 +823,25 @@ def _padded(rows: int, cols: int, device):
     return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
 
 
+def _check_outputs(*outs) -> None:
+    """A caller's outputs take no part in a graph of gradients: what it holds for them would be the
+    gradient of what was there before."""
+    import torch
+
+    for t in outs:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise RuntimeError("an out that requires grad cannot be written: no gradient flows through this "
+                               "operator")
+
+
+def _written(*outs) -> None:
+    """Tells autograd that a caller's outputs hold other values now, so that a backward pass that saved one
+    of them refuses to use it."""
+    from torch.autograd.graph import increment_version
+
+    increment_version([t for t in outs if t is not None])
+
+
 def _int_sizes(*sizes):
     """Sizes that the C ABI takes, which counts rows and columns in 32 bits."""
     for n in sizes:
@@ -844,16 +863,19 @@ def quantize_mx4(X, out=None, scales=None):
             return done
     import torch
 
+    _check_outputs(out, scales)
     code = _dtype_code(X.dtype)
     X = _rows(X.detach(), "X")
     M, K = _int_sizes(*X.shape)
     row, blocks = (K + 1) // 2, (K + 31) // 32
+    given = out, scales
     out = _padded(M, row, X.device) if out is None else _out(out, (M, row), torch.uint8, X.device, "out")
     scales = (_padded(M, blocks, X.device) if scales is None
               else _out(scales, (M, blocks), torch.uint8, X.device, "scales"))
     with _Device(X.device) as stream:
         gemm_mx4_quantize(M, K, X.data_ptr(), code, _ld_of(X), out.data_ptr(), _ld_of(out),
                           scales.data_ptr(), _ld_of(scales), stream)
+    _written(*given)
     return out, scales
 
 
@@ -882,6 +904,8 @@ def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
                                                         columns)
         if done is not None:
             return done
+    given = out
+    _check_outputs(given)
     Q, scales = _packed_rows(Q, scales, "Q")
     M, R = Q.shape
     if columns is None:
@@ -897,6 +921,7 @@ def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
     with _Device(Q.device) as stream:
         gemm_mx4_dequantize(M, columns, Q.data_ptr(), _ld_of(Q), scales.data_ptr(), _ld_of(scales),
                             out.data_ptr(), code, _ld_of(out), stream)
+    _written(given)
     return out
 
 
@@ -914,6 +939,8 @@ def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
                                                     0 if out_dtype is None else _dtype_code(out_dtype))
         if done is not None:
             return done
+    given = out
+    _check_outputs(given)
     A, a_scales = _packed_rows(A, a_scales, "A")
     B, b_scales = _packed_rows(B, b_scales, "B")
     M, R = A.shape
@@ -936,6 +963,7 @@ def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
         ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
         gemm_mx4(M, N, 2 * R, *operands, 0 if bias is None else bias.data_ptr(), out.data_ptr(), code,
                  _ld_of(out), 0 if ws is None else ws.data_ptr(), ws_bytes, stream)
+    _written(given)
     return out
 
 
@@ -1041,7 +1069,9 @@ def reorder_beams(states, beams, out=None):
 
     Results are new tensors (small ones, 64 MiB in all, may share an allocation), or written to out:
     tensors of the same shapes and types, for which out=states reorders in place and leaves rows that
-    stay alone. An out must not overlap itself or another state. No gradient flows through it."""
+    stay alone. An out must not overlap itself or another state, nor require grad (but under
+    torch.no_grad); a backward pass that saved its values notices the change. No gradient flows through
+    it."""
     done = (_calls or _load_calls()).reorder_beams(states, beams, out)
     if done is not None:
         return done
@@ -1050,6 +1080,7 @@ def reorder_beams(states, beams, out=None):
     single = isinstance(states, torch.Tensor)
     sources = [states] if single else list(states)
     targets = None if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
+    _check_outputs(*(targets or ()))
     if beams.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"beams must be int64 or int32, got {beams.dtype}")
     if beams.dim() != 2:
@@ -1091,4 +1122,6 @@ def reorder_beams(states, beams, out=None):
             table.append(fields)
     with _Device(dev) as stream:
         reorder_beams_raw(B, W, beams.data_ptr(), beams.element_size(), table, stream)
+    if out is not None:
+        _written(*targets)
     return targets[0] if single else targets

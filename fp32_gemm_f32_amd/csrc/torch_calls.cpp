@@ -12,6 +12,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -557,7 +558,8 @@ PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
         if (!given) continue;
         const at::Tensor *o = plain(PySequence_Fast_GET_ITEM(args[2], i));
         if (!o || o->device() != device || o->layout() != at::kStrided || o->scalar_type() != t->scalar_type() ||
-            o->sizes() != t->sizes() || o->is_neg() || o->is_conj())
+            o->sizes() != t->sizes() || o->is_neg() || o->is_conj() ||
+            (o->requires_grad() && c10::GradMode::is_enabled()))
             return none();
         dst.push_back(*o);
     }
@@ -577,6 +579,10 @@ PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
                                states.data(), int(states.size()), place.stream);
     }
     if (status != SGEMM_OK) return none();
+    // (autograd refuses to use a saved tensor of another version)
+    if (given)
+        for (const at::Tensor &t : dst)
+            if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
     PyObject *r = PyList_New(count);
     if (!r) return nullptr;
     for (Py_ssize_t i = 0; i < count; ++i)
