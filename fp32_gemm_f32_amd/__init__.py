@@ -823,6 +823,16 @@ def _padded(rows: int, cols: int, device):
     return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device)[:, :cols]
 
 
+def _no_tangent(what: str, *tensors) -> None:
+    """Refuses tensors that carry a forward-mode tangent, which would be lost."""
+    import torch
+
+    for t in tensors:
+        if t is not None and torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError(f"{what} has no forward-mode derivative: its tensors must not carry a "
+                                      "tangent")
+
+
 def _check_outputs(*outs) -> None:
     """A caller's outputs take no part in a graph of gradients: what it holds for them would be the
     gradient of what was there before."""
@@ -856,13 +866,14 @@ def quantize_mx4(X, out=None, scales=None):
     (M, ceil(K / 32)) uint8, s for 2^(s - 127). X is float32, bfloat16 or float16; a row is a token of
     activations or an output channel of weights. The codes are defined to the bit (gemm_mx4.h).
     Where 4 does not divide a row's bytes the result is a view of padded rows, which the product reads
-    in place. No gradient flows through it."""
+    in place. No gradient flows through it; a forward-mode tangent is refused."""
     if out is None and scales is None:
         done = (_calls or _load_calls()).quantize_mx4(X)
         if done is not None:
             return done
     import torch
 
+    _no_tangent("quantize_mx4", X)
     _check_outputs(out, scales)
     code = _dtype_code(X.dtype)
     X = _rows(X.detach(), "X")
@@ -895,8 +906,8 @@ def _packed_rows(q, scales, name: str):
 
 def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
     """The values that Q (M, R) uint8 with its scales stands for: (M, columns) of dtype (float32 by
-    default, bfloat16 or float16), columns 2 R unless it is given as 2 R - 1. No gradient flows through
-    it."""
+    default, bfloat16 or float16), columns 2 R unless it is given as 2 R - 1. No gradient flows
+    through it; a forward-mode tangent is refused."""
     import torch
 
     if out is None:
@@ -905,6 +916,7 @@ def dequantize_mx4(Q, scales, dtype=None, columns=None, out=None):
         if done is not None:
             return done
     given = out
+    _no_tangent("dequantize_mx4", out)
     _check_outputs(given)
     Q, scales = _packed_rows(Q, scales, "Q")
     M, R = Q.shape
@@ -931,7 +943,7 @@ def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
     row of B is an output channel), their scales (M or N, ceil(R / 16)) uint8, bias (N,) float32. C is
     out_dtype (float32 by default, bfloat16 or float16). The workspace (for a split K, or for
     operands off a word's boundary) is a torch allocation made here. No gradient flows through
-    it."""
+    it; a forward-mode tangent is refused."""
     import torch
 
     if out is None:
@@ -940,6 +952,7 @@ def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
         if done is not None:
             return done
     given = out
+    _no_tangent("matmul_mx4", bias, out)
     _check_outputs(given)
     A, a_scales = _packed_rows(A, a_scales, "A")
     B, b_scales = _packed_rows(B, b_scales, "B")
@@ -969,8 +982,8 @@ def matmul_mx4(A, a_scales, B, b_scales, bias=None, out_dtype=None, out=None):
 
 def linear_mx4(X, B, b_scales, bias=None, out_dtype=None):
     """quantize_mx4(X), then its product with the 4-bit weights B (N, ceil(K / 2)) of scales b_scales: a
-    projection of activations X (..., K). The result has X's type unless out_dtype says otherwise. No
-    gradient flows through it."""
+    projection of activations X (..., K). The result has X's type unless out_dtype says
+    otherwise. No gradient flows through it; a forward-mode tangent is refused."""
     if X.dim() == 2:
         done = (_calls or _load_calls()).linear_mx4(X, B, b_scales, bias,
                                                     -1 if out_dtype is None else _dtype_code(out_dtype))
@@ -999,12 +1012,13 @@ def beam_step(logits, scores, top=None, finished=None, pad_token: int = 0) -> Be
     finished (B, W) bool marks beams that have ended: such a beam offers itself alone, with its score
     and pad_token. Continuations of probability 0 (logits or scores of -infinity) and of rows that
     hold a NaN or +infinity do not count. Of equal totals the lower beam comes first, of a beam's equal
-    logits the lower token. No gradient flows through it."""
+    logits the lower token. No gradient flows through it; a forward-mode tangent is refused."""
     done = (_calls or _load_calls()).beam_step(logits, scores, top, finished, pad_token)
     if done is not None:
         return BeamStep(*done)
     import torch
 
+    _no_tangent("beam_step", logits, scores)
     code = _dtype_code(logits.dtype)
     if scores.dim() != 2:
         raise ValueError(f"scores must be 2-D, got {scores.dim()}-D")
@@ -1070,8 +1084,8 @@ def reorder_beams(states, beams, out=None):
     Results are new tensors (small ones, 64 MiB in all, may share an allocation), or written to out:
     tensors of the same shapes and types, for which out=states reorders in place and leaves rows that
     stay alone. An out must not overlap itself or another state, nor require grad (but under
-    torch.no_grad); a backward pass that saved its values notices the change. No gradient flows through
-    it."""
+    torch.no_grad); a backward pass that saved its values notices the change. No gradient flows
+    through it; a forward-mode tangent is refused."""
     done = (_calls or _load_calls()).reorder_beams(states, beams, out)
     if done is not None:
         return done
@@ -1080,6 +1094,7 @@ def reorder_beams(states, beams, out=None):
     single = isinstance(states, torch.Tensor)
     sources = [states] if single else list(states)
     targets = None if out is None else [out] if isinstance(out, torch.Tensor) else list(out)
+    _no_tangent("reorder_beams", *sources, *(targets or ()))
     _check_outputs(*(targets or ()))
     if beams.dtype not in (torch.int64, torch.int32):
         raise TypeError(f"beams must be int64 or int32, got {beams.dtype}")

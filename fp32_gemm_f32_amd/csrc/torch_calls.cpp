@@ -87,6 +87,9 @@ at::Tensor empty(at::IntArrayRef size, at::ScalarType type, const at::Device &de
     return at::detail::empty_cuda(size, type, device, std::nullopt);
 }
 
+// (a forward-mode tangent would be lost: the Python layer refuses it)
+bool dual(const at::Tensor *t) { return t && t->_fw_grad(0).defined(); }
+
 // The launch's device and stream, for the time of a call.
 struct Place {
     c10::hip::HIPGuard guard;
@@ -179,8 +182,7 @@ PyObject *token_logprobs_(PyObject *, PyObject *const *args, Py_ssize_t n)
     const int code = dtype_code(x->scalar_type());
     const at::Device device = x->device();
     const long top = PyLong_AsLong(args[2]);
-    // (a forward-mode tangent would be lost: the Python layer refuses it)
-    if (!m.ok || code < 0 || top < 0 || top > TOKEN_LOGPROBS_MAX_TOP || x->_fw_grad(0).defined()) {
+    if (!m.ok || code < 0 || top < 0 || top > TOKEN_LOGPROBS_MAX_TOP || dual(x)) {
         PyErr_Clear();
         return none();
     }
@@ -294,7 +296,7 @@ PyObject *quantize_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (!x) return none();
     const Matrix m(*x);
     const int code = dtype_code(x->scalar_type());
-    if (!m.ok || code < 0) return none();
+    if (!m.ok || code < 0 || dual(x)) return none();
     at::Tensor q, scales;
     int status;
     {
@@ -360,7 +362,7 @@ PyObject *matmul_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
     const int code = int(PyLong_AsLong(args[5]));
     if (!pa.ok || !pb.ok || pa.q.cols != pb.q.cols || b->device() != device || code < 0 || code > 2) return none();
     const MaybeVector bias(args[4], pb.q.rows, device);
-    if (!bias.ok) return none();
+    if (!bias.ok || dual(bias.t)) return none();
     at::Tensor c;
     int status;
     {
@@ -390,7 +392,7 @@ PyObject *linear_mx4(PyObject *, PyObject *const *args, Py_ssize_t n)
         pb.q.cols != packed_columns(m.cols))
         return none();
     const MaybeVector bias(args[3], pb.q.rows, device);
-    if (!bias.ok) return none();
+    if (!bias.ok || dual(bias.t) || dual(x)) return none();
     at::Tensor q, scales, c;
     int status;
     {
@@ -431,7 +433,7 @@ PyObject *beam_step_(PyObject *, PyObject *const *args, Py_ssize_t n)
         PyErr_Clear();
         return none();
     }
-    if (!m.ok || code < 0 || !per_beam(*scores, at::kFloat)) return none();
+    if (!m.ok || code < 0 || !per_beam(*scores, at::kFloat) || dual(x) || dual(scores)) return none();
     const int64_t B = scores->size(0), W = scores->size(1);
     if (finished && (!per_beam(*finished, at::kBool) || finished->size(0) != B || finished->size(1) != W))
         return none();
@@ -552,14 +554,14 @@ PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
     for (Py_ssize_t i = 0; i < count; ++i) {
         const at::Tensor *t = plain(PySequence_Fast_GET_ITEM(args[0], i));
         if (!t || t->device() != device || t->layout() != at::kStrided || t->dim() < 1 || t->size(0) != rows ||
-            t->is_neg() || t->is_conj())
+            t->is_neg() || t->is_conj() || dual(t))
             return none();
         src.push_back(*t);
         if (!given) continue;
         const at::Tensor *o = plain(PySequence_Fast_GET_ITEM(args[2], i));
         if (!o || o->device() != device || o->layout() != at::kStrided || o->scalar_type() != t->scalar_type() ||
             o->sizes() != t->sizes() || o->is_neg() || o->is_conj() ||
-            (o->requires_grad() && c10::GradMode::is_enabled()))
+            dual(o) || (o->requires_grad() && c10::GradMode::is_enabled()))
             return none();
         dst.push_back(*o);
     }

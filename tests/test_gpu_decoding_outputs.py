@@ -74,3 +74,24 @@ def test_outputs_that_require_grad(torch):
     g.reorder_beams([t], beams, out=[t])
     g.reorder_beams(t, beams, out=t)
     assert t.tolist() == [1, 1, 1]
+
+
+def test_tangents_are_refused(torch):
+    """Also on the shorter way in, which takes ordinary tensors on a GPU; others are served in a dual level as
+    outside of it."""
+    fa = torch.autograd.forward_ad
+    x, bias, scores = torch.randn(4, 64, device="cuda"), torch.randn(8, device="cuda"), torch.zeros(2, 2, device="cuda")
+    w, ws = g.quantize_mx4(torch.randn(8, 64, device="cuda"))
+    beams = torch.tensor([[1, 0], [0, 0]], device="cuda")
+    q, s = g.quantize_mx4(x)
+
+    with fa.dual_level():
+        dx, dbias, dscores = (fa.make_dual(t, torch.ones_like(t)) for t in (x, bias, scores))
+        for call in (lambda: g.quantize_mx4(dx), lambda: g.linear_mx4(dx, w, ws), lambda: g.linear_mx4(x, w, ws, bias=dbias),
+                     lambda: g.matmul_mx4(q, s, w, ws, bias=dbias), lambda: g.beam_step(dx, scores),
+                     lambda: g.beam_step(x, dscores), lambda: g.reorder_beams([beams.view(-1), dx], beams),
+                     lambda: g.reorder_beams([torch.zeros_like(x)], beams, out=[dx])):
+            with pytest.raises(NotImplementedError):
+                call()
+        inside = g.linear_mx4(x, w, ws, bias=bias)
+    assert torch.equal(inside, g.linear_mx4(x, w, ws, bias=bias))
