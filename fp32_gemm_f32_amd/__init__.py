@@ -1019,6 +1019,8 @@ def beam_step(logits, scores, top=None, finished=None, pad_token: int = 0) -> Be
     import torch
 
     _no_tangent("beam_step", logits, scores)
+    if not -2 ** 63 <= pad_token < 2 ** 63:
+        raise ValueError(f"pad_token must fit 64 bits, got {pad_token}")
     code = _dtype_code(logits.dtype)
     if scores.dim() != 2:
         raise ValueError(f"scores must be 2-D, got {scores.dim()}-D")
