@@ -587,8 +587,9 @@ PyObject *reorder_beams_(PyObject *, PyObject *const *args, Py_ssize_t n)
             if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
     PyObject *r = PyList_New(count);
     if (!r) return nullptr;
-    for (Py_ssize_t i = 0; i < count; ++i)
-        PyList_SET_ITEM(r, i, given ? Py_NewRef(PySequence_Fast_GET_ITEM(args[2], i)) : THPVariable_Wrap(dst[i]));
+    // (of given ones the objects that they have: the caller's list may be another one by now, for other
+    // threads ran meanwhile)
+    for (Py_ssize_t i = 0; i < count; ++i) PyList_SET_ITEM(r, i, THPVariable_Wrap(dst[size_t(i)]));
     return r;
     END_HANDLE_TH_ERRORS
 }

@@ -95,3 +95,34 @@ def test_tangents_are_refused(torch):
                 call()
         inside = g.linear_mx4(x, w, ws, bias=bias)
     assert torch.equal(inside, g.linear_mx4(x, w, ws, bias=bias))
+
+
+def test_a_list_that_changes_meanwhile(torch):
+    """Another thread empties and fills the caller's list while calls run: each call takes it as it was when
+    it began, or refuses one that it found in between."""
+    import threading
+
+    beams = torch.tensor([[1, 0]], device="cuda")
+    states = [torch.zeros(2, i + 1, device="cuda") for i in range(12)]
+    outs, over = list(states), threading.Event()
+
+    def churn():
+        while not over.is_set():
+            del outs[3:]
+            outs.extend(states[3:])
+
+    t = threading.Thread(target=churn)
+    t.start()
+    try:
+        done = 0
+        for _ in range(300):
+            try:
+                r = g.reorder_beams(states, beams, out=outs)
+            except ValueError:                                   # the list was short
+                continue
+            done += 1
+            assert len(r) == 12 and all(a is b for a, b in zip(r, states))
+    finally:
+        over.set()
+        t.join()
+    assert done > 0
