@@ -77,17 +77,57 @@ uint64_t extent_of(int64_t rows, int64_t row, int64_t n1, int64_t s1, int64_t n2
     const __int128 most = static_cast<__int128>(1) << 62;
     return uint64_t(n < most ? n : most);
 }
-struct Span {
-    uint64_t from, bytes;      // all rows
-    int64_t row, in_row;       // a row's stride, bytes of one row
+// One side of a state.
+struct Side {
+    const beam_state *state;
     bool written;
+    uint64_t from, bytes;
 };
-// Whether two spans that overlap as a whole (a starts first) are disjoint slices of common rows.
-bool slices(const Span &a, const Span &b)
+// Its bytes by their strides from the largest on (counts of 1 and strides of 0 add none).
+struct Span {
+    int64_t run;
+    bool in_place;
+    int levels = 0;
+    struct { int64_t n, step; } level[3];
+
+    Span(const Side &x, int64_t rows) : run(x.state->run), in_place(x.state->src == x.state->dst)
+    {
+        const beam_state &s = *x.state;
+        const int64_t n[3] = {rows, s.count1, s.count2};
+        const int64_t step[3] = {x.written ? s.dst_row : s.src_row, x.written ? s.dst_step1 : s.src_step1,
+                                 x.written ? s.dst_step2 : s.src_step2};
+        for (int i = 0; i < 3; ++i) {
+            if (n[i] <= 1 || step[i] == 0) continue;
+            int at = levels++;
+            for (; at > 0 && level[at - 1].step < step[i]; --at) level[at] = level[at - 1];
+            level[at] = {n[i], step[i]};
+        }
+    }
+    // from the first byte to the last of the levels from k on, saturated
+    uint64_t extent(int k) const
+    {
+        const __int128 most = static_cast<__int128>(1) << 62;
+        __int128 sum = run;
+        for (; k < levels; ++k) sum = std::min(most, sum + static_cast<__int128>(level[k].n - 1) * level[k].step);
+        return uint64_t(sum);
+    }
+};
+// Whether the levels from k on of b, which starts d bytes behind a, hold none of a's bytes: those that
+// end before b starts, and slices of a common stride. Of such a stride's periods, a's parts lie at their
+// start and b's r behind it. Where b's do not reach into the next period they meet a's of the same one
+// at most, always r behind them; else, where a's end before r, those of the next one, which start s - r
+// behind b's. Anything else counts as an overlap, and so do slices of the inner strides but of
+// states that are both reordered in place.
+bool apart(const Span &a, const Span &b, uint64_t d, int k)
 {
-    if (a.row != b.row || a.row <= 0 || a.in_row > a.row || b.in_row > b.row) return false;
-    const int64_t at = int64_t((b.from - a.from) % uint64_t(a.row));
-    return at >= a.in_row && at + b.in_row <= a.row;
+    if (d >= a.extent(k)) return true;
+    if (k == a.levels || k == b.levels || a.level[k].step != b.level[k].step) return false;
+    const uint64_t s = uint64_t(a.level[k].step), r = d % s, of_a = a.extent(k + 1), of_b = b.extent(k + 1);
+    if (of_a > s || of_b > s) return false;
+    if (r >= of_a && r + of_b <= s) return true;
+    if (!a.in_place || !b.in_place) return false;
+    if (r + of_b <= s) return apart(a, b, r, k + 1);
+    return of_a <= r && apart(b, a, s - r, k + 1);
 }
 
 }  // namespace
@@ -187,9 +227,9 @@ extern "C" int reorder_beams(int B, int W, const void *beams, int beam_bytes, co
     if (rows == 0 || count == 0) return SGEMM_OK;
     const Region idx = region(beams, 1, rows, rows, beam_bytes);
     if (bad_region(idx, beam_bytes)) return SGEMM_EINVAL_PTR;
-    std::vector<Span> spans;
+    std::vector<Side> sides;
     try {
-        spans.reserve(size_t(count) * 2);
+        sides.reserve(size_t(count) * 2);
     } catch (...) {
         return SGEMM_ELAUNCH;
     }
@@ -198,25 +238,24 @@ extern "C" int reorder_beams(int B, int W, const void *beams, int beam_bytes, co
         const beam_state &s = states[i];
         if (!s.count1 || !s.count2 || !s.run) continue;
         if (s.src == nullptr || s.dst == nullptr) return SGEMM_EINVAL_PTR;
-        const uint64_t from = reinterpret_cast<uintptr_t>(s.src), to = reinterpret_cast<uintptr_t>(s.dst);
-        const Span dst = {to, extent_of(rows, s.dst_row, s.count1, s.dst_step1, s.count2, s.dst_step2, s.run), s.dst_row,
-                          int64_t(extent_of(1, 0, s.count1, s.dst_step1, s.count2, s.dst_step2, s.run)), true};
-        const Span src = {from, extent_of(rows, s.src_row, s.count1, s.src_step1, s.count2, s.src_step2, s.run), s.src_row,
-                          int64_t(extent_of(1, 0, s.count1, s.src_step1, s.count2, s.src_step2, s.run)), false};
         const bool same = s.src_row == s.dst_row && (s.count1 == 1 || s.src_step1 == s.dst_step1) &&
                           (s.count2 == 1 || s.src_step2 == s.dst_step2);
-        spans.push_back(dst);
-        if (from != to) spans.push_back(src);
+        const uint64_t bytes = extent_of(rows, s.dst_row, s.count1, s.dst_step1, s.count2, s.dst_step2, s.run);
+        sides.push_back({&s, true, reinterpret_cast<uintptr_t>(s.dst), bytes});
+        if (s.src != s.dst)
+            sides.push_back({&s, false, reinterpret_cast<uintptr_t>(s.src),
+                             extent_of(rows, s.src_row, s.count1, s.src_step1, s.count2, s.src_step2, s.run)});
         else if (!same) return SGEMM_EALIAS;
         const __int128 columns = static_cast<__int128>(s.count1) * s.count2 * ceil_div(s.run, 16);
         large = large || columns >= (int64_t(1) << 31) - kReorderThreads;
-        const Region r = {s.dst, dst.bytes};
-        if (overlaps(r, idx)) return SGEMM_EALIAS;
+        if (overlaps({s.dst, bytes}, idx)) return SGEMM_EALIAS;
     }
-    std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.from < b.from; });
-    for (size_t i = 0; i < spans.size(); ++i)
-        for (size_t j = i + 1; j < spans.size() && spans[j].from - spans[i].from < spans[i].bytes; ++j)
-            if ((spans[i].written || spans[j].written) && !slices(spans[i], spans[j])) return SGEMM_EALIAS;
+    std::sort(sides.begin(), sides.end(), [](const Side &a, const Side &b) { return a.from < b.from; });
+    for (size_t i = 0; i < sides.size(); ++i)
+        for (size_t j = i + 1; j < sides.size() && sides[j].from - sides[i].from < sides[i].bytes; ++j)
+            if ((sides[i].written || sides[j].written) &&
+                !apart({sides[i], rows}, {sides[j], rows}, sides[j].from - sides[i].from, 0))
+                return SGEMM_EALIAS;
     if (large) return SGEMM_ETOO_LARGE;
 
     auto kern = W <= 4 ? &k_reorder<4> : W <= 8 ? &k_reorder<8> : W <= 16 ? &k_reorder<16>

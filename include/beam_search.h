@@ -72,8 +72,9 @@ typedef struct {
  * (beam_step's -1) stands for w itself. W is 1 to BEAM_MAX.
  *
  * In place where a state's dst is its src, with the same strides; rows that stay are not touched then.
- * Any other overlap of what is written with anything else is SGEMM_EALIAS (states that share an
- * allocation must not interleave their rows, except as disjoint slices of common rows). Strides and
+ * Any other overlap of what is written with anything else is SGEMM_EALIAS. States that share an
+ * allocation must not interleave their rows, except as disjoint slices of common rows, or, where both
+ * are reordered in place, of common pieces (keys and values side by side in each position). Strides and
  * counts are not negative (else SGEMM_EINVAL_DIM), pieces of a dst do not overlap (SGEMM_EINVAL_LD),
  * a state has fewer than 2^35 bytes to a row (SGEMM_ETOO_LARGE). `states` is host memory, read
  * before the call returns.
