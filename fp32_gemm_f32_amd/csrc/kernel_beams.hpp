@@ -39,7 +39,7 @@ struct BeamArgs {
 // where the peak stays.
 // Up to kFar a step of c is 128 at most, so that sums of 2^31 terms stay in range. Beyond, logits that
 // differ do so by 128 and more, also from those up to it: a term, there 2^((x - m) L), is 1 or 0, and so
-// is the factor between two peaks one of which lies beyond.
+// is the factor between two peaks one of which lies beyond, for which 2^(their difference) will do.
 constexpr float kFar = 1073741824.0f;                  // 2^30
 constexpr double kNats = 1.0 / double(kLog2e);         // of a base-2 logarithm by L
 __device__ inline bool beam_near(float m) { return __builtin_fabsf(m) <= kFar; }
@@ -47,8 +47,8 @@ __device__ inline bool beam_near(float m) { return __builtin_fabsf(m) <= kFar; }
 __device__ inline float beam_rescale(float from, float to)
 {
 #pragma clang fp contract(off)
-    const float near = __builtin_amdgcn_exp2f(from * kLog2e - to * kLog2e);
-    return beam_near(from) && beam_near(to) ? near : from == to ? 1.0f : 0.0f;
+    const float near = from * kLog2e - to * kLog2e, far = from - to;
+    return __builtin_amdgcn_exp2f(__builtin_fmaxf(-from, to) <= kFar ? near : far);
 }
 struct BeamStats {
     float m = kLowest, s = 0.0f;
