@@ -99,7 +99,7 @@ template <int NT> __device__ inline BeamStats join_beam_stats(StatsShared<NT> &s
 // (key_of) in descending order, 0 for those it is too short for. Rows of finished beams are left
 // out. A thread's elements: up to one of the head before the first 16-byte boundary, the chunks tid,
 // tid + NT, ... of 16 bytes, up to one of the tail. Bound by memory and, nearly as much, by the
-// exponentials: 1024 rows of 131072 bf16 take 50 us (5.4 TB/s). Registers are kept to 64, so that a compute
+// exponentials: 1024 rows of 131072 bf16 take 53.4 us (5.0 TB/s). Registers are kept to 64, so that a compute
 // unit holds 32 waves (more loads to a thread, or the next ones ahead of these, cost waves: 60 us).
 template <int DT, int NT, int U, bool STREAM>
 __global__ __launch_bounds__(NT, 8) void k_beam_pass(BeamArgs p)
@@ -531,7 +531,7 @@ static_assert(BEAM_MAX <= 64 && kStates <= 64, "a lane for each beam, and for ea
 // become, then stores it, so that a state may be reordered in place. Rows that stay where they
 // are (in place) are left alone. Bound by memory: 256 rows of 4 caches of 8 x 1000 x 128 bf16 in place take
 // 232 us (6.2 TB/s of what moves; with stores that stay in the caches 267). Small states by the
-// way from the arguments to the indices to the rows (18 of 4 rows, 13 MB: 6.8 us): the state of a
+// way from the arguments to the indices to the rows (18 of 4 rows, 13 MB: 6.4 us): the state of a
 // workgroup is found by all lanes at once, the request's indices are one load, a lane each.
 constexpr int kReorderThreads = 256;
 template <int MOST>

@@ -100,8 +100,8 @@ template <bool STREAM, typename T> __device__ inline Pack<T, 8> mx4_load_unit(co
 }
 
 // Four lanes share a block, 8 elements each; U times 256 lanes to a workgroup, their loads first.
-// HBM-bound: 2 or 4 bytes in and 17 / 32 out of an element. 8192 x 8192 bf16 27.8 us (6.1 TB/s), 16384 x
-// 8192 53.2; with loads that stay in the caches 28.4 and 60.3.
+// HBM-bound: 2 or 4 bytes in and 17 / 32 out of an element. 8192 x 8192 bf16 28.6 us (5.9 TB/s); loads past
+// the caches against loads that stay there, taken in turn: 27.8 and 28.4, at 16384 x 8192 53.2 and 60.3.
 template <int DT, int U>
 __global__ __launch_bounds__(256) void k_mx4_quantize(Mx4RowArgs p)
 {
